@@ -19,6 +19,7 @@ from .abi import (  # noqa: F401
     awq_act_stats_finish,
     awq_act_sums,
     awq_block_grams,
+    awq_block_norm,
     awq_bounds_checks_enabled,
     awq_bounds_status,
     awq_candidate_codes,
@@ -34,6 +35,8 @@ from .abi import (  # noqa: F401
     awq_search_scale_sse,
     awq_select_scale,
     awq_w4a16_gemm,
+    awq_w4a16_lora_gemm,
+    awq_w4a16_lora_workspace_size,
     awq_w4a16_workspace_size,
     awq_workspace_size,
     awq_workspace_size_min,

@@ -94,6 +94,14 @@ _SIGNATURES = {
                                  c_int64, POINTER(AwqConfig), c_void_p, c_int64, c_void_p, c_size_t,
                                  c_void_p]),
     "awq_w4a16_workspace_size": (c_size_t, [c_int64, c_int64, c_int64, POINTER(AwqConfig)]),
+    "awq_w4a16_lora_gemm": (c_int32, [c_void_p, c_int64, c_int64, c_int64, c_void_p, c_void_p, c_void_p,
+                                      c_int64, POINTER(AwqConfig), c_void_p, c_void_p, c_void_p, c_int32,
+                                      c_int32, c_void_p, c_void_p, c_int64, c_void_p, c_size_t, c_void_p]),
+    "awq_w4a16_lora_workspace_size": (c_size_t, [c_int64, c_int64, c_int64, c_int32,
+                                                 POINTER(AwqConfig)]),
+    "awq_block_norm": (c_int32, [c_void_p, c_int64, c_void_p, c_int64, c_int64, c_int64, c_void_p, c_void_p,
+                                 c_int64, c_float, c_void_p, c_float, c_void_p, c_int64, c_void_p, c_int64,
+                                 c_void_p]),
     "awq_act_sums": (c_int32, [c_void_p, c_int64, c_int64, c_int64, c_void_p, c_void_p]),
     "awq_act_stats_finish": (c_int32, [c_void_p, c_int64, c_int64, c_void_p, c_void_p]),
     "awq_search_scale_sse": (c_int32, [c_void_p, c_int64, c_int64, c_int64, c_void_p, c_int64,
@@ -314,6 +322,37 @@ def awq_w4a16_workspace_size(T: int, inn: int, out: int, cfg: AwqConfig) -> int:
     if n == 0:
         raise AwqError("awq_w4a16_workspace_size", 1, last_error())
     return int(n)
+
+
+def awq_w4a16_lora_gemm(X, qweight, qzeros, scales, cfg: AwqConfig, A, B, c, adapter, Y, ws,
+                        stream=None) -> None:
+    """Y [T, out] fp16 = X times the packed weights, plus for each token its
+    adapter's c_a (X A_a^T) B_a^T: A fp16 [n, rank, in], B fp16 [n, out, rank],
+    c fp32 [n], adapter int32 [T] (-1: none)."""
+    n, rank, _ = A.shape
+    _check("awq_w4a16_lora_gemm", LIB.awq_w4a16_lora_gemm(
+        _ptr(X), X.shape[0], X.shape[1], X.stride(0), _ptr(qweight), _ptr(qzeros), _ptr(scales),
+        Y.shape[1], ctypes.byref(cfg), _ptr(A), _ptr(B), _ptr(c), n, rank, _ptr(adapter), _ptr(Y),
+        Y.stride(0), _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)))
+
+
+def awq_w4a16_lora_workspace_size(T: int, inn: int, out: int, rank: int, cfg: AwqConfig) -> int:
+    n = LIB.awq_w4a16_lora_workspace_size(T, inn, out, rank, ctypes.byref(cfg))
+    if n == 0:
+        raise AwqError("awq_w4a16_lora_workspace_size", 1, last_error())
+    return int(n)
+
+
+def awq_block_norm(R, V, post, gate, c: float, pre, eps: float, R_out, N_out, stream=None) -> None:
+    """R_out = R + c gate rmsnorm(V) post and N_out = rmsnorm(R_out) pre over
+    fp16 rows [T, d]; V, post, gate ([T, d] or [d]), pre and one of the outputs
+    may be None."""
+    T, d = R.shape
+    _check("awq_block_norm", LIB.awq_block_norm(
+        _ptr(R), R.stride(0), _ptr(V), 0 if V is None else V.stride(0), T, d, _ptr(post), _ptr(gate),
+        gate.stride(0) if gate is not None and gate.dim() == 2 else 0, c, _ptr(pre), eps, _ptr(R_out),
+        0 if R_out is None else R_out.stride(0), _ptr(N_out), 0 if N_out is None else N_out.stride(0),
+        _stream(stream)))
 
 
 def awq_device_status(ws, stream=None) -> None:

@@ -15,6 +15,7 @@
 
 #include "awq.h"
 #include "awq_launch.h"
+#include "serve_launch.h"
 
 using namespace awq;
 
@@ -853,6 +854,113 @@ size_t awq_w4a16_workspace_size(int64_t T, int64_t in, int64_t out, const awq_co
   return splits > 1 ? w4a16_ws_bytes(T, out, splits) : kHeader;
 }
 
+// status word plus U of the adapter product
+static size_t lora_ws_bytes(int64_t T, int32_t rank) {
+  return kHeader + align256(sizeof(float) * (size_t)T * (size_t)rank);
+}
+
+static awq_status check_lora_shape(int64_t T, int64_t in, int64_t out, int32_t rank, const awq_config *cfg) {
+  awq_status st = check_cfg(cfg);
+  if (st != AWQ_OK) return st;
+  if ((st = check_shape(T, in, out, cfg)) != AWQ_OK) return st;
+  if (in % 64 != 0 || out % 32 != 0)
+    return fail(AWQ_ERR_UNSUPPORTED, "in=%lld, out=%lld: the adapter product needs in %% 64 == 0 and out %% 32 == 0",
+                (long long)in, (long long)out);
+  if (rank < 1) return fail(AWQ_ERR_INVALID_ARG, "rank=%d", rank);
+  if (rank % 8 != 0 || rank > 256)
+    return fail(AWQ_ERR_UNSUPPORTED, "rank=%d (a multiple of 8 up to 256 supported)", rank);
+  return AWQ_OK;
+}
+
+size_t awq_w4a16_lora_workspace_size(int64_t T, int64_t in, int64_t out, int32_t rank,
+                                     const awq_config *cfg) {
+  g_err.clear();
+  NvtxCall nvtx_call_(__func__);
+  if (fault_mode() == Fault::kAlloc) {
+    fail(AWQ_ERR_WORKSPACE, "injected allocation failure (AWQ_FAULT=alloc)");
+    return 0;
+  }
+  if (check_lora_shape(T, in, out, rank, cfg) != AWQ_OK) return 0;
+  return lora_ws_bytes(T, rank);
+}
+
+awq_status awq_w4a16_lora_gemm(const void *X, int64_t T, int64_t in, int64_t ldx,
+                               const int32_t *qweight, const int32_t *qzeros, const void *scales,
+                               int64_t out, const awq_config *cfg, const void *A, const void *B,
+                               const float *c, int32_t n_adapters, int32_t rank,
+                               const int32_t *adapter, void *Y, int64_t ldy, void *ws,
+                               size_t ws_bytes, awq_stream_t stream) {
+  g_err.clear();
+  NvtxCall nvtx_call_(__func__);
+  awq_status st = check_lora_shape(T, in, out, rank, cfg);
+  if (st != AWQ_OK) return st;
+  if ((st = check_x(X, in, ldx)) != AWQ_OK) return st;
+  if (!qweight || !qzeros || !scales || !aligned(qweight, 16) || !aligned(qzeros, 16) || !aligned(scales, 16))
+    return fail(AWQ_ERR_INVALID_ARG, "qweight, qzeros and scales must be non-NULL and 16-byte aligned");
+  if (n_adapters < 1 || n_adapters > 65536)
+    return fail(AWQ_ERR_INVALID_ARG, "n_adapters=%d (1..65536)", n_adapters);
+  if (!A || !B || !aligned(A, 16) || !aligned(B, 16))
+    return fail(AWQ_ERR_INVALID_ARG, "A and B must be non-NULL and 16-byte aligned");
+  if (!c || !adapter || !aligned(c, 4) || !aligned(adapter, 4))
+    return fail(AWQ_ERR_INVALID_ARG, "c and adapter must be non-NULL and 4-byte aligned");
+  if (!Y || !aligned(Y, 16)) return fail(AWQ_ERR_INVALID_ARG, "Y is NULL or not 16-byte aligned");
+  if (ldy < out || ldy % 8 != 0)
+    return fail(AWQ_ERR_INVALID_ARG, "ldy=%lld must be >= out and a multiple of 8", (long long)ldy);
+  if ((st = check_ws(ws, ws_bytes, lora_ws_bytes(T, rank))) != AWQ_OK) return st;
+  AWQ_LAUNCH_GATE();
+  cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  LoraArgs a = {static_cast<const __half *>(X), T, in, ldx, qweight, qzeros, static_cast<const __half *>(scales),
+                out, cfg->group_size, static_cast<const __half *>(A), static_cast<const __half *>(B), c, adapter,
+                rank, n_adapters, static_cast<__half *>(Y), ldy,
+                reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + kHeader), static_cast<DevStatus *>(ws)};
+  ProfScope p("w4a16_lora", cs);
+  AWQ_TRY_CUDA(launch_lora(a, num_sms_current(), cs), "w4a16_lora launch");
+  return AWQ_OK;
+}
+
+static awq_status check_rows(const char *name, const void *p, int64_t ld, int64_t d) {
+  if (!aligned(p, 16)) return fail(AWQ_ERR_INVALID_ARG, "%s must be 16-byte aligned", name);
+  if (ld < d || ld % 8 != 0)
+    return fail(AWQ_ERR_INVALID_ARG, "the row stride of %s, %lld, must be >= d and a multiple of 8", name,
+                (long long)ld);
+  return AWQ_OK;
+}
+
+awq_status awq_block_norm(const void *R, int64_t ldr, const void *V, int64_t ldv, int64_t T,
+                          int64_t d, const void *post, const void *gate, int64_t ldg, float c,
+                          const void *pre, float eps, void *R_out, int64_t ldro, void *N_out,
+                          int64_t ldno, awq_stream_t stream) {
+  g_err.clear();
+  NvtxCall nvtx_call_(__func__);
+  awq_status st;
+  if (T < 1 || T > (int64_t(1) << 22)) return fail(AWQ_ERR_INVALID_ARG, "T=%lld (1..2^22)", (long long)T);
+  if (d < 8 || d % 8 != 0) return fail(AWQ_ERR_INVALID_ARG, "d=%lld must be a positive multiple of 8", (long long)d);
+  if (d > 32768) return fail(AWQ_ERR_UNSUPPORTED, "d=%lld (up to 32768 supported)", (long long)d);
+  if (!(eps >= 0.0f)) return fail(AWQ_ERR_INVALID_ARG, "eps=%g", (double)eps);
+  if (!R) return fail(AWQ_ERR_INVALID_ARG, "R is NULL");
+  if ((st = check_rows("R", R, ldr, d)) != AWQ_OK) return st;
+  if (V && (st = check_rows("V", V, ldv, d)) != AWQ_OK) return st;
+  if (!V && (post || gate)) return fail(AWQ_ERR_INVALID_ARG, "post and gate need V");
+  if (!aligned(post, 16) || !aligned(pre, 16))
+    return fail(AWQ_ERR_INVALID_ARG, "post and pre must be 16-byte aligned");
+  if (gate && (ldg != 0 ? check_rows("gate", gate, ldg, d) : check_rows("gate", gate, d, d)) != AWQ_OK)
+    return AWQ_ERR_INVALID_ARG;
+  if (!R_out && !N_out) return fail(AWQ_ERR_INVALID_ARG, "R_out and N_out are both NULL");
+  if (R_out && (st = check_rows("R_out", R_out, ldro, d)) != AWQ_OK) return st;
+  if (N_out && (st = check_rows("N_out", N_out, ldno, d)) != AWQ_OK) return st;
+  if (pre && !N_out) return fail(AWQ_ERR_INVALID_ARG, "pre needs N_out");
+  if (R_out && R_out == N_out) return fail(AWQ_ERR_INVALID_ARG, "R_out and N_out are the same buffer");
+  AWQ_LAUNCH_GATE();
+  cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  const NormArgs a = {static_cast<const __half *>(R), static_cast<const __half *>(V),
+                      static_cast<const __half *>(post), static_cast<const __half *>(gate),
+                      static_cast<const __half *>(pre), ldr, ldv, ldg, T, d, ldro, ldno, c, eps,
+                      static_cast<__half *>(R_out), static_cast<__half *>(N_out)};
+  ProfScope p("block_norm", cs);
+  AWQ_TRY_CUDA(launch_block_norm(a, cs), "block_norm launch");
+  return AWQ_OK;
+}
+
 awq_status awq_fold_inv_scale(void *v, int64_t rows, int64_t cols, const float *s,
                               awq_stream_t stream) {
   g_err.clear();
@@ -883,6 +991,8 @@ awq_status awq_device_status(void *ws, awq_stream_t stream) {
   if (h.flags & kDevTimeout)
     return fail(AWQ_ERR_TIMEOUT, "a bounded device wait ran out (site 0x%x)", h.where);
   if (h.flags & kDevNonFinite) return fail(AWQ_ERR_NONFINITE, "a candidate score is not finite");
+  if (h.flags & kDevBadAdapter)
+    return fail(AWQ_ERR_INVALID_ARG, "an adapter id lies outside [-1, n_adapters) (computed without an adapter)");
   if (h.flags & kDevBadIndex)
     return fail(AWQ_ERR_INVALID_ARG,
                 "awq_quant_pack was given a clip index >= n_clip (those groups got a NaN scale)");

@@ -1,0 +1,55 @@
+// Internal launchers of the serving operators (host side): the adapter
+// product, the mixture-of-experts layer and the norms around a block.  Every
+// launcher only enqueues work on `stream` and returns the launch error, if any.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "awq_device.cuh"
+
+namespace awq {
+
+// DevStatus flag: an adapter id outside [-1, n_adapters) (beside awq_device.cuh's kDev* bits)
+constexpr uint32_t kDevBadAdapter = 1u << 4;
+
+// Sets a kernel's dynamic shared memory limit once per device.
+template <class K>
+inline cudaError_t allow_smem(K kernel, size_t bytes, bool (&done)[64]) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 0 && dev < 64 && done[dev]) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (e == cudaSuccess && dev >= 0 && dev < 64) done[dev] = true;
+  return e;
+}
+
+struct LoraArgs {
+  const __half *X;
+  int64_t T, in, ldx;
+  const int32_t *qweight, *qzeros;
+  const __half *scales;
+  int64_t out;
+  int group;
+  const __half *A, *B;
+  const float *c;
+  const int32_t *ids;
+  int rank, adapters;
+  __half *Y;
+  int64_t ldy;
+  float *U;       // workspace: [T, rank] fp32
+  DevStatus *st;
+};
+// Y = X W^T + c_a (X A_a^T) B_a^T; in % 64 == 0, out % 32 == 0, rank % 8 == 0.
+cudaError_t launch_lora(const LoraArgs &a, int num_sms, cudaStream_t stream);
+
+struct NormArgs {
+  const __half *R, *V, *post, *gate, *pre;
+  int64_t ldr, ldv, ldg, T, d, ldro, ldno;
+  float c, eps;
+  __half *R_out, *N_out;
+};
+cudaError_t launch_block_norm(const NormArgs &a, cudaStream_t stream);
+
+}  // namespace awq
