@@ -395,6 +395,45 @@ awq_status awq_w4a16_lora_gemm(const void *X, int64_t T, int64_t in, int64_t ldx
 size_t awq_w4a16_lora_workspace_size(int64_t T, int64_t in, int64_t out, int32_t rank,
                                      const awq_config *cfg);
 
+/* A whole mixture-of-experts layer on packed experts, for a few tokens (a
+ * decode step or a small batch), in one kernel: router, choice, gate|up,
+ * SwiGLU, down and the weighted sum,
+ *   l_te = sum_j X[t][j] router[e][j];  the top_k largest of a row, ties to the
+ *   lowest expert;  p = softmax of l_t over all experts, divided by the chosen
+ *   ones' sum when renormalize = 1;
+ *   H = RN16( silu(x gate_e) (x up_e) );  Y[t] = RN16( sum_k p_k down_e(H) )
+ * with every packed weight (q - z) scale unrounded.
+ *   X       device fp16 [T, hidden], row stride ldx
+ *   mask    device uint8 [T] or NULL: rows with 0 (the padding of a captured
+ *           step) meet no expert and get ids -1, weights 0 and Y = 0; their X
+ *           is not used
+ *   router  device fp16 [n_experts, hidden]
+ *   gu_*    the experts' gate|up linears packed by awq_quant_pack, gate's
+ *           outputs first: qweight [n_experts, hidden, 2 inter/8], qzeros
+ *           [n_experts, hidden/g, 2 inter/8], scales fp16 [n_experts, hidden/g, 2 inter]
+ *   dn_*    the down linears: qweight [n_experts, inter, hidden/8], qzeros and
+ *           scales over inter/g groups
+ *   Y       device fp16 [T, hidden] (output), row stride ldy; not X
+ *   ids     device int32 [T, top_k] (output), in falling order of their logits
+ *   weights device fp32 [T, top_k] (output)
+ *   ws      awq_w4a16_moe_workspace_size() bytes
+ * Requires 1 <= T <= 64, 1 <= top_k <= min(16, n_experts), n_experts <= 256,
+ * hidden and inter multiples of 64 and of cfg->group_size, hidden <= 16384,
+ * inter <= 65536; X, router, the packed tensors and Y 16-byte aligned.  The
+ * kernel is launched cooperatively (its blocks meet at bounded barriers): a
+ * barrier that runs out is recorded as AWQ_ERR_TIMEOUT in ws. */
+awq_status awq_w4a16_moe(const void *X, int64_t T, int64_t hidden, int64_t ldx, const uint8_t *mask,
+                         const void *router, int32_t n_experts, int32_t top_k, int32_t renormalize,
+                         const int32_t *gu_qweight, const int32_t *gu_qzeros, const void *gu_scales,
+                         int64_t inter, const int32_t *dn_qweight, const int32_t *dn_qzeros,
+                         const void *dn_scales, const awq_config *cfg, void *Y, int64_t ldy,
+                         int32_t *ids, float *weights, void *ws, size_t ws_bytes,
+                         awq_stream_t stream);
+
+/* Workspace bytes of awq_w4a16_moe; 0 when the arguments are invalid. */
+size_t awq_w4a16_moe_workspace_size(int64_t T, int64_t hidden, int64_t inter, int32_t n_experts,
+                                    int32_t top_k, const awq_config *cfg);
+
 /* The end of one block and the start of the next, for T token rows of d:
  *   v' = V rsqrt(mean V^2 + eps) post        (v' = V when post is NULL)
  *   r' = R + c gate v'                       (gate = 1 when gate is NULL)

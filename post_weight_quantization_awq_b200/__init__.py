@@ -37,6 +37,8 @@ from .abi import (  # noqa: F401
     awq_w4a16_gemm,
     awq_w4a16_lora_gemm,
     awq_w4a16_lora_workspace_size,
+    awq_w4a16_moe,
+    awq_w4a16_moe_workspace_size,
     awq_w4a16_workspace_size,
     awq_workspace_size,
     awq_workspace_size_min,

@@ -99,6 +99,12 @@ _SIGNATURES = {
                                       c_int32, c_void_p, c_void_p, c_int64, c_void_p, c_size_t, c_void_p]),
     "awq_w4a16_lora_workspace_size": (c_size_t, [c_int64, c_int64, c_int64, c_int32,
                                                  POINTER(AwqConfig)]),
+    "awq_w4a16_moe": (c_int32, [c_void_p, c_int64, c_int64, c_int64, c_void_p, c_void_p, c_int32, c_int32,
+                                c_int32, c_void_p, c_void_p, c_void_p, c_int64, c_void_p, c_void_p,
+                                c_void_p, POINTER(AwqConfig), c_void_p, c_int64, c_void_p, c_void_p,
+                                c_void_p, c_size_t, c_void_p]),
+    "awq_w4a16_moe_workspace_size": (c_size_t, [c_int64, c_int64, c_int64, c_int32, c_int32,
+                                                POINTER(AwqConfig)]),
     "awq_block_norm": (c_int32, [c_void_p, c_int64, c_void_p, c_int64, c_int64, c_int64, c_void_p, c_void_p,
                                  c_int64, c_float, c_void_p, c_float, c_void_p, c_int64, c_void_p, c_int64,
                                  c_void_p]),
@@ -340,6 +346,29 @@ def awq_w4a16_lora_workspace_size(T: int, inn: int, out: int, rank: int, cfg: Aw
     n = LIB.awq_w4a16_lora_workspace_size(T, inn, out, rank, ctypes.byref(cfg))
     if n == 0:
         raise AwqError("awq_w4a16_lora_workspace_size", 1, last_error())
+    return int(n)
+
+
+def awq_w4a16_moe(X, router, gate_up, down, cfg: AwqConfig, renormalize: bool, mask, Y, ids, weights, ws,
+                  stream=None) -> None:
+    """A mixture-of-experts layer on packed experts: X fp16 [T, hidden], router
+    fp16 [E, hidden], gate_up and down (qweight, qzeros, scales) with a leading
+    expert axis, mask uint8 [T] or None; outputs Y [T, hidden] fp16, ids int32
+    and weights fp32 [T, top_k]."""
+    gq, gz, gs = gate_up
+    dq, dz, ds = down
+    _check("awq_w4a16_moe", LIB.awq_w4a16_moe(
+        _ptr(X), X.shape[0], X.shape[1], X.stride(0), _ptr(mask), _ptr(router), router.shape[0], ids.shape[1],
+        1 if renormalize else 0, _ptr(gq), _ptr(gz), _ptr(gs), dq.shape[1], _ptr(dq), _ptr(dz), _ptr(ds),
+        ctypes.byref(cfg), _ptr(Y), Y.stride(0), _ptr(ids), _ptr(weights), _ptr(ws),
+        ws.numel() * ws.element_size(), _stream(stream)))
+
+
+def awq_w4a16_moe_workspace_size(T: int, hidden: int, inter: int, n_experts: int, top_k: int,
+                                 cfg: AwqConfig) -> int:
+    n = LIB.awq_w4a16_moe_workspace_size(T, hidden, inter, n_experts, top_k, ctypes.byref(cfg))
+    if n == 0:
+        raise AwqError("awq_w4a16_moe_workspace_size", 1, last_error())
     return int(n)
 
 

@@ -918,6 +918,83 @@ awq_status awq_w4a16_lora_gemm(const void *X, int64_t T, int64_t in, int64_t ldx
   return AWQ_OK;
 }
 
+static awq_status check_moe_shape(int64_t T, int64_t hidden, int64_t inter, int32_t n_experts, int32_t top_k,
+                                  const awq_config *cfg) {
+  awq_status st = check_cfg(cfg);
+  if (st != AWQ_OK) return st;
+  if (T < 1) return fail(AWQ_ERR_INVALID_ARG, "T=%lld", (long long)T);
+  if (T > kMoeMaxTokens)
+    return fail(AWQ_ERR_UNSUPPORTED, "T=%lld (up to %d tokens supported)", (long long)T, kMoeMaxTokens);
+  if (n_experts < 1) return fail(AWQ_ERR_INVALID_ARG, "n_experts=%d", n_experts);
+  if (n_experts > kMoeMaxExperts)
+    return fail(AWQ_ERR_UNSUPPORTED, "n_experts=%d (up to %d supported)", n_experts, kMoeMaxExperts);
+  if (top_k < 1 || top_k > n_experts)
+    return fail(AWQ_ERR_INVALID_ARG, "top_k=%d (1..n_experts)", top_k);
+  if (top_k > kMoeMaxTopK) return fail(AWQ_ERR_UNSUPPORTED, "top_k=%d (up to %d supported)", top_k, kMoeMaxTopK);
+  for (int64_t n : {hidden, inter})
+    if (n < cfg->group_size || n % cfg->group_size != 0)
+      return fail(AWQ_ERR_INVALID_ARG, "hidden=%lld and inter=%lld must be positive multiples of group_size=%d",
+                  (long long)hidden, (long long)inter, cfg->group_size);
+  if (hidden % 64 != 0 || inter % 64 != 0 || hidden > 16384 || inter > 65536)
+    return fail(AWQ_ERR_UNSUPPORTED,
+                "hidden=%lld, inter=%lld: multiples of 64, hidden <= 16384 and inter <= 65536 supported",
+                (long long)hidden, (long long)inter);
+  return AWQ_OK;
+}
+
+size_t awq_w4a16_moe_workspace_size(int64_t T, int64_t hidden, int64_t inter, int32_t n_experts,
+                                    int32_t top_k, const awq_config *cfg) {
+  g_err.clear();
+  NvtxCall nvtx_call_(__func__);
+  if (fault_mode() == Fault::kAlloc) {
+    fail(AWQ_ERR_WORKSPACE, "injected allocation failure (AWQ_FAULT=alloc)");
+    return 0;
+  }
+  if (check_moe_shape(T, hidden, inter, n_experts, top_k, cfg) != AWQ_OK) return 0;
+  return moe_layout(T, hidden, inter, n_experts, top_k, num_sms_current()).end;
+}
+
+awq_status awq_w4a16_moe(const void *X, int64_t T, int64_t hidden, int64_t ldx, const uint8_t *mask,
+                         const void *router, int32_t n_experts, int32_t top_k, int32_t renormalize,
+                         const int32_t *gu_qweight, const int32_t *gu_qzeros, const void *gu_scales,
+                         int64_t inter, const int32_t *dn_qweight, const int32_t *dn_qzeros,
+                         const void *dn_scales, const awq_config *cfg, void *Y, int64_t ldy,
+                         int32_t *ids, float *weights, void *ws, size_t ws_bytes,
+                         awq_stream_t stream) {
+  g_err.clear();
+  NvtxCall nvtx_call_(__func__);
+  awq_status st = check_moe_shape(T, hidden, inter, n_experts, top_k, cfg);
+  if (st != AWQ_OK) return st;
+  if (renormalize != 0 && renormalize != 1) return fail(AWQ_ERR_INVALID_ARG, "renormalize=%d (0 or 1)", renormalize);
+  if ((st = check_x(X, hidden, ldx)) != AWQ_OK) return st;
+  const void *const packed[] = {router, gu_qweight, gu_qzeros, gu_scales, dn_qweight, dn_qzeros, dn_scales};
+  for (const void *p : packed)
+    if (!p || !aligned(p, 16))
+      return fail(AWQ_ERR_INVALID_ARG, "router and the packed tensors must be non-NULL and 16-byte aligned");
+  if (!Y || !aligned(Y, 16)) return fail(AWQ_ERR_INVALID_ARG, "Y is NULL or not 16-byte aligned");
+  if (Y == X) return fail(AWQ_ERR_INVALID_ARG, "Y and X are the same buffer");
+  if (ldy < hidden || ldy % 8 != 0)
+    return fail(AWQ_ERR_INVALID_ARG, "ldy=%lld must be >= hidden and a multiple of 8", (long long)ldy);
+  if (!ids || !weights || !aligned(ids, 4) || !aligned(weights, 4))
+    return fail(AWQ_ERR_INVALID_ARG, "ids and weights must be non-NULL and 4-byte aligned");
+  const MoeLayout l = moe_layout(T, hidden, inter, n_experts, top_k, num_sms_current());
+  if ((st = check_ws(ws, ws_bytes, l.end)) != AWQ_OK) return st;
+  AWQ_LAUNCH_GATE();
+  cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  uint8_t *b = static_cast<uint8_t *>(ws);
+  MoeArgs a = {static_cast<const __half *>(X), ldx, mask, static_cast<const __half *>(router),
+               gu_qweight, gu_qzeros, static_cast<const __half *>(gu_scales),
+               dn_qweight, dn_qzeros, static_cast<const __half *>(dn_scales),
+               (int)T, n_experts, top_k, cfg->group_size, renormalize, hidden, inter, l.max_seg,
+               static_cast<__half *>(Y), ldy, ids, weights,
+               static_cast<DevStatus *>(ws), reinterpret_cast<uint32_t *>(b + 64),
+               reinterpret_cast<double *>(b + l.logits), reinterpret_cast<int *>(b + l.tile_count),
+               reinterpret_cast<__half *>(b + l.H), reinterpret_cast<float *>(b + l.partial), poll_cap()};
+  ProfScope p("w4a16_moe", cs);
+  AWQ_TRY_CUDA(launch_moe(a, num_sms_current(), cs), "w4a16_moe launch");
+  return AWQ_OK;
+}
+
 static awq_status check_rows(const char *name, const void *p, int64_t ld, int64_t d) {
   if (!aligned(p, 16)) return fail(AWQ_ERR_INVALID_ARG, "%s must be 16-byte aligned", name);
   if (ld < d || ld % 8 != 0)

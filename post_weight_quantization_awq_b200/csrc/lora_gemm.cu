@@ -62,7 +62,8 @@ __global__ void __launch_bounds__(kThreads, MINB) lora_stream_kernel(const __gri
   const int64_t tile = blockIdx.x / (unsigned)splits;
   const int64_t t0 = (int64_t)blockIdx.y * MAXTOK;
   const int n = (int)(a.T - t0 < MAXTOK ? a.T - t0 : MAXTOK);
-  Weights w{a.qweight, a.qzeros, a.scales, a.out / 8, a.group, {tile * 32, tile * 32 + 16}, {a.out / 8, a.out / 8}};
+  Weights w{a.qweight, a.qzeros, a.scales, a.out / 8, group_shift(a.group),
+            tile * 32, a.out / 8, tile * 32 + 16, a.out / 8};
   const Rows x{a.X + t0 * a.ldx, a.ldx, nullptr, n};
   // input rows of this rank, in units of 256 (128) rows so that groups stay whole
   const int64_t unit = a.in >= 512 * splits ? 256 : 128, units = (a.in + unit - 1) / unit;
@@ -70,7 +71,7 @@ __global__ void __launch_bounds__(kThreads, MINB) lora_stream_kernel(const __gri
   int64_t k1 = units * (rank + 1) / splits * unit;
   if (k1 > a.in) k1 = a.in;
   Acc<NT> acc;
-  product<NT, SP, MAXTOK, STAGES>(acc, smem, w, x, k0, k1);
+  product<NT, SP, MAXTOK, STAGES>(acc, smem, w, x, (int)k0, (int)(k1 > k0 ? k1 : k0));
   float *red = reinterpret_cast<float *>(smem);
   store_sums<NT, SP>(acc, red);
   pdl_wait();  // U and the cleared status word

@@ -52,4 +52,39 @@ struct NormArgs {
 };
 cudaError_t launch_block_norm(const NormArgs &a, cudaStream_t stream);
 
+constexpr int kMoeMaxTokens = 64, kMoeMaxTopK = 16, kMoeMaxExperts = 256;
+constexpr uint32_t kMoeRing = 96256;  // shared memory of the cp.async ring
+
+struct MoeArgs {
+  const __half *X;
+  int64_t ldx;
+  const uint8_t *mask;     // [T] or NULL
+  const __half *router;    // [experts, hidden]
+  const int32_t *gu_q, *gu_z;
+  const __half *gu_s;
+  const int32_t *dn_q, *dn_z;
+  const __half *dn_s;
+  int T, experts, top_k, group, renormalize;
+  int64_t hidden, inter, max_seg;
+  __half *Y;
+  int64_t ldy;
+  int32_t *ids;
+  float *weights;
+  // workspace
+  DevStatus *st;
+  uint32_t *barrier;       // 3 counters, in the status word's 256 bytes
+  double *logits;
+  int *tile_count;
+  __half *H;
+  float *partial;
+  uint32_t max_polls;
+};
+struct MoeLayout {
+  size_t logits, tile_count, H, partial, end;
+  int64_t max_seg;
+};
+__host__ __device__ constexpr int64_t i64max_(int64_t a, int64_t b) { return a > b ? a : b; }
+MoeLayout moe_layout(int64_t T, int64_t hidden, int64_t inter, int64_t experts, int64_t top_k, int num_sms);
+cudaError_t launch_moe(const MoeArgs &a, int num_sms, cudaStream_t stream);
+
 }  // namespace awq

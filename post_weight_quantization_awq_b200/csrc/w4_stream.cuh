@@ -46,10 +46,11 @@ __host__ __device__ constexpr uint32_t stage_bytes(int max_tok) {
   return 2 * kPieceW + 2 * (uint32_t)max_tok * kXPitch + 4 * kSz;
 }
 
-__device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool ok) {
-  const uint32_t n = ok ? 16u : 0u;  // 0: the 16 bytes are zero-filled, nothing is read
+__device__ __forceinline__ void cp16(uint32_t dst, const void *src, uint32_t n) {  // n = 0: zero-filled
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
 }
+__device__ __forceinline__ int group_shift(int group) { return group == 32 ? 5 : group == 64 ? 6 : 7; }
+
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void cp_wait() {
@@ -74,8 +75,8 @@ struct Weights {
   const int32_t *qweight, *qzeros;
   const __half *scales;
   int64_t words;  // out / 8
-  int group;
-  int64_t col[2], end[2];  // word columns of outputs 0..127 / 128..255 of the tile
+  int group_shift;  // log2 of the group size
+  int64_t col0, end0, col1, end1;
 };
 
 // Tokens of a product: row t is base + row(t) * ld.
@@ -94,59 +95,95 @@ enum class Split { kK, kTok };
 // 128 p .. 128 p + 127 of it, 64 in each stage, so that a group of 128 stays
 // with one warp.
 template <Split SP>
-__device__ __forceinline__ int64_t piece_row(int64_t k0, int s, int p) {
-  return SP == Split::kK ? k0 + (int64_t)(s >> 1) * 256 + p * 128 + (s & 1) * 64
-                         : k0 + (int64_t)s * 128 + p * 64;
+__device__ __forceinline__ int piece_row(int k0, int s, int p) {
+  return SP == Split::kK ? k0 + (s >> 1) * 256 + p * 128 + (s & 1) * 64 : k0 + s * 128 + p * 64;
 }
 template <Split SP>
-__device__ __forceinline__ int num_stages(int64_t rows) {  // rows a multiple of 64
-  if (SP == Split::kTok) return (int)((rows + 127) / 128);
-  const int rem = (int)(rows % 256);
-  return (int)(rows / 256) * 2 + (rem == 0 ? 0 : rem == 64 ? 1 : 2);
+__device__ __forceinline__ int num_stages(int rows) {  // rows a multiple of 64
+  if (SP == Split::kTok) return (rows + 127) / 128;
+  const int rem = rows % 256;
+  return rows / 256 * 2 + (rem == 0 ? 0 : rem == 64 ? 1 : 2);
 }
 
-// Copies of one stage into shared memory at `st` (not committed).
+// This thread's copies of a stage, their addresses worked out once per product:
+// rows r and r + 32 of one 16-byte word chunk of both pieces, up to NX chunks
+// of X, and one chunk of the groups' steps or zero words.
 template <Split SP, int MAXTOK>
-__device__ __forceinline__ void issue_stage(uint32_t st, const Weights &w, const Rows &x, int64_t k0, int64_t k1,
-                                            int s) {
-  const int tid = threadIdx.x;
-  const int r = tid >> 3, c = tid & 7;
-  const int64_t col = w.col[c >> 2] + 4 * (c & 3);
-  const bool col_ok = col < w.end[c >> 2];
-#pragma unroll
-  for (int p = 0; p < 2; ++p) {
-    const int64_t kb = piece_row<SP>(k0, s, p);
-    if (kb >= k1) continue;  // the piece is outside the range: nobody reads it
-    const uint32_t dst = st + p * kPieceW + r * 128 + ((uint32_t)(c ^ (((r >> 2) & 3) << 1)) << 4);
-    const int32_t *src = w.qweight + (kb + r) * w.words + (col_ok ? col : 0);
-    cp16(dst, src, col_ok);
-    cp16(dst + 32 * 128, src + 32 * w.words, col_ok);  // row + 32: the same swizzle
-    const uint32_t xd = st + 2 * kPieceW + p * MAXTOK * kXPitch;
-    for (int i = tid; i < x.n * 8; i += kThreads) {
-      const int t = i >> 3, xc = i & 7;
-      const int64_t row = x.index ? x.index[t] : t;
-      cp16(xd + t * kXPitch + xc * 16, x.base + row * x.ld + kb + xc * 8, true);
+struct Loader {
+  static constexpr int NX = (16 * MAXTOK + kThreads - 1) / kThreads;
+  const char *w;   // row r of the matrix
+  int64_t wrow;    // bytes of a row of words
+  uint32_t wdst, wn;
+  const char *x[NX];  // NULL: nothing to copy
+  const char *sz;     // group 0's chunk
+  int64_t szrow;
+  uint32_t szdst, szn;
+  int role, shift;  // role: -1, or piece * 2 + group of the piece
+
+  __device__ __forceinline__ void init(const Weights &m, const Rows &rows) {
+    const int tid = threadIdx.x;
+    shift = m.group_shift;
+    {
+      const int r = tid >> 3, c = tid & 7;
+      const int64_t col = (c < 4 ? m.col0 : m.col1) + 4 * (c & 3);
+      const bool ok = col < (c < 4 ? m.end0 : m.end1);
+      wrow = m.words * 4;
+      w = reinterpret_cast<const char *>(m.qweight + (ok ? col : 0)) + r * wrow;
+      wdst = r * 128 + ((uint32_t)(c ^ (((r >> 2) & 3) << 1)) << 4);
+      wn = ok ? 16u : 0u;  // 0: the chunk is zero-filled, nothing is read
     }
-    // steps and zero words of the piece's groups (two when g = 32); a group of
-    // 128 is closed by its second piece, which alone brings them
-    if (w.group == 128 && !(kb & 64)) continue;
-    if (tid < (w.group == 32 ? 80 : 40)) {
-      const int gi = tid / 40, e = tid % 40;
-      const int64_t grp = (kb + 32 * gi) / w.group;
-      const uint32_t zd = st + 2 * kPieceW + 2 * MAXTOK * kXPitch + (p * 2 + gi) * kSz;
-      if (e < 32) {
-        const int64_t wc = w.col[e >> 4] + (e & 15);
-        const bool ok = wc < w.end[e >> 4];
-        cp16(zd + e * 16, w.scales + grp * w.words * 8 + (ok ? wc : 0) * 8, ok);
-      } else {
-        const int zc = e - 32;
-        const int64_t wc = w.col[zc >> 2] + 4 * (zc & 3);
-        const bool ok = wc < w.end[zc >> 2];
-        cp16(zd + 512 + zc * 16, w.qzeros + grp * w.words + (ok ? wc : 0), ok);
+#pragma unroll
+    for (int j = 0; j < NX; ++j) {
+      const int i = tid + j * kThreads, c = i & 7, pt = i >> 3, t = pt % MAXTOK;
+      x[j] = nullptr;
+      if (pt < 2 * MAXTOK && t < rows.n) {
+        const int64_t row = rows.index ? rows.index[t] : t;
+        x[j] = reinterpret_cast<const char *>(rows.base + row * rows.ld + c * 8);
       }
     }
+    role = tid / 40;  // a piece has one group, two when g = 32
+    const int e = tid - role * 40;
+    if (role >= 4 || (shift != 5 && (role & 1))) {
+      role = -1;
+      return;
+    }
+    const int ch = e < 32 ? e >> 2 : e - 32;  // the 16-byte word chunk it belongs to
+    const int64_t col = (ch < 4 ? m.col0 : m.col1) + 4 * (ch & 3) + (e < 32 ? e & 3 : 0);
+    const bool ok = col < (ch < 4 ? m.end0 : m.end1);
+    szrow = e < 32 ? m.words * 16 : m.words * 4;
+    sz = e < 32 ? reinterpret_cast<const char *>(m.scales + (ok ? col : 0) * 8)
+                : reinterpret_cast<const char *>(m.qzeros + (ok ? col : 0));
+    szdst = 2 * kPieceW + 2 * MAXTOK * kXPitch + role * kSz + (e < 32 ? e * 16 : 512 + (e - 32) * 16);
+    szn = ok ? 16u : 0u;
   }
-}
+
+  // Copies of stage s of the range [k0, k1) into shared memory at `st` (not
+  // committed).  A piece outside the range is skipped: nobody reads it.
+  __device__ __forceinline__ void issue(uint32_t st, int k0, int k1, int s) const {
+    const int tid = threadIdx.x;
+    const int kb0 = piece_row<SP>(k0, s, 0), kb1 = piece_row<SP>(k0, s, 1);
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+      const int kb = p ? kb1 : kb0;
+      if (kb >= k1) continue;
+      const char *src = w + (int64_t)kb * wrow;
+      cp16(st + p * kPieceW + wdst, src, wn);
+      cp16(st + p * kPieceW + wdst + 32 * 128, src + 32 * wrow, wn);  // row r + 32: the same swizzle
+    }
+#pragma unroll
+    for (int j = 0; j < NX; ++j) {
+      const int i = tid + j * kThreads, pt = i >> 3;
+      const int kb = pt < MAXTOK ? kb0 : kb1;
+      if (x[j] && kb < k1) cp16(st + 2 * kPieceW + pt * kXPitch + (i & 7) * 16, x[j] + 2 * kb, 16u);
+    }
+    if (role >= 0) {
+      const int kb = (role & 2) ? kb1 : kb0;
+      // a group of 128 is closed by its second piece, which alone brings it
+      if (kb < k1 && (shift != 7 || (kb & 64)))
+        cp16(st + szdst, sz + (int64_t)((kb + 32 * (role & 1)) >> shift) * szrow, szn);
+    }
+  }
+};
 
 // Accumulators of one warp: 64 outputs x 8 NT tokens.
 template <int NT>
@@ -205,7 +242,7 @@ __device__ __forceinline__ void flush_group(Acc<NT> &a, const uint8_t *sz, int w
 // addresses in the piece.
 template <int NT>
 __device__ __forceinline__ void piece(Acc<NT> &a, const uint8_t *wb, const uint8_t *xb, const uint8_t *sz,
-                                      int wcol, int group, bool close128) {
+                                      int wcol, int shift, bool close128) {
 #pragma unroll
   for (int ks = 0; ks < 4; ++ks) {
     uint32_t w[4];
@@ -230,49 +267,50 @@ __device__ __forceinline__ void piece(Acc<NT> &a, const uint8_t *wb, const uint8
 #pragma unroll
     for (int n = 0; n < NT; ++n)
       mma16816(a.sx[n], 0x00010001u, 0x00010001u, 0x00010001u, 0x00010001u, b[n].x, b[n].y);
-    if (group == 32 && (ks & 1)) flush_group<NT>(a, sz + (ks >> 1) * kSz, wcol);
+    if (shift == 5 && (ks & 1)) flush_group<NT>(a, sz + (ks >> 1) * kSz, wcol);
   }
-  if (group == 64 || (group == 128 && close128)) flush_group<NT>(a, sz, wcol);
+  if (shift == 6 || (shift == 7 && close128)) flush_group<NT>(a, sz, wcol);
 }
 
 // The product of the block over rows [k0, k1) of its tile (k0 and k1
 // multiples of 64; of 128 when g = 128).  Uses the ring at `ring` (STAGES x
 // stage_bytes(MAXTOK)), which is free again on return for every thread.
 template <int NT, Split SP, int MAXTOK, int STAGES>
-__device__ __forceinline__ void product(Acc<NT> &a, uint8_t *ring, const Weights &w, const Rows &x, int64_t k0,
-                                        int64_t k1) {
+__device__ __forceinline__ void product(Acc<NT> &a, uint8_t *ring, const Weights &w, const Rows &x, int k0,
+                                        int k1) {
+  constexpr uint32_t kStage = stage_bytes(MAXTOK);
   const uint32_t ring_u = smem_u32(ring);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int nw = warp & 3, half = warp >> 2, g = lane >> 2, q = lane & 3;
   const int wcol = nw * 8 + g;
   const int ns = num_stages<SP>(k1 - k0);
-  acc_zero<NT>(a);
+  Loader<SP, MAXTOK> ld;
+  ld.init(w, x);
 #pragma unroll
   for (int s = 0; s < STAGES - 1; ++s) {
-    if (s < ns) issue_stage<SP, MAXTOK>(ring_u + s * stage_bytes(MAXTOK), w, x, k0, k1, s);
+    if (s < ns) ld.issue(ring_u + s * kStage, k0, k1, s);
     cp_commit();
   }
+  acc_zero<NT>(a);
   const uint32_t wlane = (uint32_t)(4 * q) * 128 + ((uint32_t)((wcol >> 2) ^ (q << 1)) << 4) + (wcol & 3) * 4;
   const uint32_t xlane = (uint32_t)g * kXPitch + q * 8 + (SP == Split::kTok ? half * NT * 8 * kXPitch : 0);
-  int slot = 0;
+  uint32_t slot = 0, next = (STAGES - 1) * kStage;
   for (int s = 0; s < ns; ++s) {
     cp_wait<STAGES - 2>();
     __syncthreads();  // stage s has landed for all, and the slot of s - 1 is free
-    if (s + STAGES - 1 < ns) {
-      const int ps = slot == 0 ? STAGES - 1 : slot - 1;
-      issue_stage<SP, MAXTOK>(ring_u + ps * stage_bytes(MAXTOK), w, x, k0, k1, s + STAGES - 1);
-    }
+    if (s + STAGES - 1 < ns) ld.issue(ring_u + next, k0, k1, s + STAGES - 1);
     cp_commit();
-    const uint8_t *st = ring + slot * stage_bytes(MAXTOK);
+    const uint8_t *st = ring + slot;
 #pragma unroll
     for (int p = 0; p < 2; ++p) {
       if (SP == Split::kK && p != half) continue;
-      const int64_t kb = piece_row<SP>(k0, s, p);
+      const int kb = piece_row<SP>(k0, s, p);
       if (kb < k1)
         piece<NT>(a, st + p * kPieceW + wlane, st + 2 * kPieceW + p * MAXTOK * kXPitch + xlane,
-                  st + 2 * kPieceW + 2 * MAXTOK * kXPitch + p * 2 * kSz, wcol, w.group, (kb & 64) != 0);
+                  st + 2 * kPieceW + 2 * MAXTOK * kXPitch + p * 2 * kSz, wcol, w.group_shift, (kb & 64) != 0);
     }
-    if (++slot == STAGES) slot = 0;
+    next = slot;
+    slot = slot + kStage == STAGES * kStage ? 0 : slot + kStage;
   }
   cp_wait<0>();
   __syncthreads();

@@ -80,3 +80,45 @@ def block_norm(R, V, post, gate, c, pre, eps):
     if pre is not None:
         n = n * pre.astype(np.float64)
     return r, n
+
+
+def moe(X, router, gate_up, down, group, top_k, renormalize, mask=None):
+    """(Y, ids, weights, tolerance) in fp64: gate_up and down are lists of one
+    packed layer per expert.  The tolerance per output follows the roundings:
+    n-term fp32 sums lose at most n 2^-23 of the sums of magnitudes
+    (lora_tolerance), silu(g) u carries g's and u's errors by its derivatives
+    (|silu'| < 1.1) and one fp16 rounding, the softmax weights 2^-19 (their
+    exponent, exp and division), then one fp16 rounding of the result (and one
+    fp32 subnormal step where everything underflows)."""
+    T, h = X.shape
+    E = router.shape[0]
+    x = X.astype(np.float64)
+    logits = np.where(np.isfinite(x), x, 0) @ router.astype(np.float64).T
+    Y, tol = np.zeros((T, h)), np.zeros((T, h))
+    ids = np.full((T, top_k), -1, np.int32)
+    wt = np.zeros((T, top_k))
+    cache = {}
+    for t in range(T):
+        if mask is not None and not mask[t]:
+            continue
+        order = sorted(range(E), key=lambda e: (-logits[t, e], e))[:top_k]
+        p = np.exp(logits[t] - logits[t].max())
+        p = p[order] / (p[order].sum() if renormalize else p.sum())
+        ids[t], wt[t] = order, p
+        for e, pe in zip(order, p):
+            if e not in cache:
+                cache[e] = weights(gate_up[e], group) + weights(down[e], group)
+            Wg, Mg, Wd, Md = cache[e]
+            inter = Wd.shape[1]
+            gu = Wg @ x[t]
+            dgu = (h + 8) * 2.0 ** -23 * (Mg @ np.abs(x[t]))
+            g, u = gu[:inter], gu[inter:]
+            sig = 1 / (1 + np.exp(-g))
+            H = g * sig * u
+            dH = 1.1 * dgu[:inter] * (np.abs(u) + dgu[inter:]) + np.abs(g * sig) * dgu[inter:]
+            dH = dH + 2.0 ** -11 * np.abs(H) + 2.0 ** -21 * np.abs(H) + 2.0 ** -25
+            Y[t] += pe * (Wd @ H)
+            tol[t] += pe * (np.abs(Wd) @ dH + ((inter + 64) * 2.0 ** -23) * (Md @ np.abs(H)))
+            tol[t] += pe * 2.0 ** -19 * np.abs(Wd @ H)
+    tol = tol + 0.5 * ulp16(np.abs(Y) + tol)
+    return Y, ids, wt, tol

@@ -90,3 +90,48 @@ def test_injected_launch_failure_reaches_the_serving_calls(monkeypatch):
     assert _name(_lora()) == "AWQ_ERR_WORKSPACE"
     with pytest.raises(awq.AwqError):
         awq.awq_w4a16_lora_workspace_size(4, 512, 256, 16, CFG)
+
+
+def _moe(cfg=CFG, **kw):
+    a = dict(X=16, T=4, hidden=512, ldx=512, mask=None, router=16, E=8, k=2, ren=1, gq=16, gz=16, gs=16, inter=256,
+             dq=16, dz=16, ds=16, Y=32, ldy=512, ids=16, wt=16, ws=256, nbytes=1 << 40)
+    a.update(kw)
+    return abi.LIB.awq_w4a16_moe(a["X"], a["T"], a["hidden"], a["ldx"], a["mask"], a["router"], a["E"], a["k"],
+                                 a["ren"], a["gq"], a["gz"], a["gs"], a["inter"], a["dq"], a["dz"], a["ds"],
+                                 ctypes.byref(cfg), a["Y"], a["ldy"], a["ids"], a["wt"], a["ws"], a["nbytes"], None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(T=0), "AWQ_ERR_INVALID_ARG"), (dict(T=65), "AWQ_ERR_UNSUPPORTED"),
+    (dict(hidden=500, ldx=504, ldy=504), "AWQ_ERR_INVALID_ARG"), (dict(inter=200), "AWQ_ERR_INVALID_ARG"),
+    (dict(hidden=16512, ldx=16512, ldy=16512), "AWQ_ERR_UNSUPPORTED"), (dict(inter=65664), "AWQ_ERR_UNSUPPORTED"),
+    (dict(E=0), "AWQ_ERR_INVALID_ARG"), (dict(E=257), "AWQ_ERR_UNSUPPORTED"),
+    (dict(k=0), "AWQ_ERR_INVALID_ARG"), (dict(k=9), "AWQ_ERR_INVALID_ARG"),
+    (dict(E=64, k=17), "AWQ_ERR_UNSUPPORTED"), (dict(ren=2), "AWQ_ERR_INVALID_ARG"),
+    (dict(X=None), "AWQ_ERR_INVALID_ARG"), (dict(X=24), "AWQ_ERR_INVALID_ARG"),
+    (dict(ldx=504), "AWQ_ERR_INVALID_ARG"), (dict(ldy=516), "AWQ_ERR_INVALID_ARG"),
+    (dict(router=None), "AWQ_ERR_INVALID_ARG"), (dict(gz=8), "AWQ_ERR_INVALID_ARG"),
+    (dict(ds=None), "AWQ_ERR_INVALID_ARG"), (dict(Y=None), "AWQ_ERR_INVALID_ARG"),
+    (dict(Y=16), "AWQ_ERR_INVALID_ARG"), (dict(ids=None), "AWQ_ERR_INVALID_ARG"),
+    (dict(wt=18), "AWQ_ERR_INVALID_ARG"), (dict(ws=None), "AWQ_ERR_WORKSPACE"),
+    (dict(nbytes=4096), "AWQ_ERR_WORKSPACE")])
+def test_moe_refusals(kw, status):
+    assert _name(_moe(**kw)) == status, awq.last_error()
+    assert awq.last_error()
+
+
+def test_moe_refuses_bad_settings_and_sizes_its_workspace():
+    assert _name(_moe(cfg=awq.AwqConfig.make(group_size=96))) == "AWQ_ERR_UNSUPPORTED"
+    assert _name(_moe(cfg=awq.AwqConfig.make(group_size=32), hidden=544, ldx=544, ldy=544)) == "AWQ_ERR_UNSUPPORTED"
+    n = awq.awq_w4a16_moe_workspace_size(4, 512, 256, 8, 2, CFG)
+    assert n < 64 << 20
+    assert _name(_moe(nbytes=n - 1)) == "AWQ_ERR_WORKSPACE" and str(n) in awq.last_error()
+    with pytest.raises(awq.AwqError):
+        awq.awq_w4a16_moe_workspace_size(65, 512, 256, 8, 2, CFG)
+
+
+def test_injected_launch_failure_reaches_the_moe_call(monkeypatch):
+    monkeypatch.setenv("AWQ_FAULT", "launch")
+    assert _name(_moe()) == "AWQ_ERR_CUDA"
+    monkeypatch.setenv("AWQ_FAULT", "alloc")
+    assert _name(_moe()) == "AWQ_ERR_WORKSPACE"
