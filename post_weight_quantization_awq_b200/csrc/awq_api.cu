@@ -912,7 +912,7 @@ awq_status awq_w4a16_lora_gemm(const void *X, int64_t T, int64_t in, int64_t ldx
   LoraArgs a = {static_cast<const __half *>(X), T, in, ldx, qweight, qzeros, static_cast<const __half *>(scales),
                 out, cfg->group_size, static_cast<const __half *>(A), static_cast<const __half *>(B), c, adapter,
                 rank, n_adapters, static_cast<__half *>(Y), ldy,
-                reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + kHeader), static_cast<DevStatus *>(ws)};
+                reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + kHeader), static_cast<DevStatus *>(ws), poll_cap()};
   ProfScope p("w4a16_lora", cs);
   AWQ_TRY_CUDA(launch_lora(a, num_sms_current(), cs), "w4a16_lora launch");
   return AWQ_OK;
@@ -988,8 +988,10 @@ awq_status awq_w4a16_moe(const void *X, int64_t T, int64_t hidden, int64_t ldx, 
                (int)T, n_experts, top_k, cfg->group_size, renormalize, hidden, inter, l.max_seg,
                static_cast<__half *>(Y), ldy, ids, weights,
                static_cast<DevStatus *>(ws), reinterpret_cast<uint32_t *>(b + 64),
-               reinterpret_cast<double *>(b + l.logits), reinterpret_cast<int *>(b + l.tile_count),
-               reinterpret_cast<__half *>(b + l.H), reinterpret_cast<float *>(b + l.partial), poll_cap()};
+               reinterpret_cast<int *>(b + 256), reinterpret_cast<double *>(b + l.logits), reinterpret_cast<int *>(b + l.tile_count),
+               reinterpret_cast<__half *>(b + l.H), reinterpret_cast<float *>(b + l.sums),
+               reinterpret_cast<float *>(b + l.dn_sums), reinterpret_cast<float *>(b + l.partial),
+               reinterpret_cast<float *>(b + l.dn_partial), poll_cap()};
   ProfScope p("w4a16_moe", cs);
   AWQ_TRY_CUDA(launch_moe(a, num_sms_current(), cs), "w4a16_moe launch");
   return AWQ_OK;

@@ -8,6 +8,7 @@
 // streams the packed weights and waits for U only before its epilogue.
 #include <cooperative_groups.h>
 
+#include "awq_launch.h"
 #include "serve_launch.h"
 #include "w4_stream.cuh"
 
@@ -51,90 +52,201 @@ __global__ void __launch_bounds__(256) lora_shrink_kernel(const LoraArgs a) {
 }
 
 // A cluster of `splits` blocks covers 256 outputs x MAXTOK tokens, each block
-// a range of input rows; the blocks' fp32 sums meet through distributed shared
-// memory in rank order.
-template <int NT, Split SP, int MAXTOK, int STAGES, int MINB>
-__global__ void __launch_bounds__(kThreads, MINB) lora_stream_kernel(const __grid_constant__ LoraArgs a,
-                                                                     const int splits) {
-  extern __shared__ __align__(128) uint8_t smem[];
+// a range of input rows and a share of the adapters; the blocks' fp32 sums meet
+// through distributed shared memory in rank order.
+//
+// The adapters' part joins the accumulators on the tensor cores too: B_a's rows
+// are A operands straight from global memory, and U (fp32) is an fp16 pair
+// hi + lo of 22 bits under a power of two of its token, so nothing is rounded
+// away and no U overflows.  An adapter's sums are added for its own tokens only.
+template <Mode M, int NT, int MAXTOK, int STAGES>
+struct LoraShared {
+  static constexpr uint32_t kRing = STAGES * stage_bytes<M, MAXTOK>();
+  static constexpr uint32_t kRed = (MAXTOK * kRedPitch * 4 + 15) / 16 * 16;  // in the ring, after the product
+  static constexpr int kUPitch = 2 * (256 + 8);                               // bytes of a token's hi (lo) row
+  static constexpr uint32_t kU = 2 * MAXTOK * kUPitch;                        // behind it
+  static constexpr uint32_t kTail = sizeof(RingBars<STAGES>) + MAXTOK * 12 + 16;
+  static constexpr uint32_t kBytes = 1024 + kRing + kTail;
+  static_assert(kRed + kU <= kRing, "the sums and U reuse the ring");
+};
+
+template <Mode M, int NT, int MAXTOK, int STAGES, int MINB>
+__global__ void __launch_bounds__(kThreads, MINB)
+    lora_stream_kernel(const __grid_constant__ LoraArgs a, const __grid_constant__ CUtensorMap map, const int splits) {
+  using L = LoraShared<M, NT, MAXTOK, STAGES>;
+  extern __shared__ uint8_t raw[];
+  uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
+  float *red = reinterpret_cast<float *>(ring);
+  uint8_t *uhl = ring + L::kRed;
+  auto *bars = reinterpret_cast<RingBars<STAGES> *>(ring + L::kRing);
+  int *ids = reinterpret_cast<int *>(bars + 1);  // the tokens' adapters, -1: none
+  int *list = ids + MAXTOK;                      // the different ones
+  float *uscale = reinterpret_cast<float *>(list + MAXTOK);
+  int *n_list = reinterpret_cast<int *>(uscale + MAXTOK);
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = (int)(blockIdx.x % (unsigned)splits);
   const int64_t tile = blockIdx.x / (unsigned)splits;
   const int64_t t0 = (int64_t)blockIdx.y * MAXTOK;
   const int n = (int)(a.T - t0 < MAXTOK ? a.T - t0 : MAXTOK);
-  Weights w{a.qweight, a.qzeros, a.scales, a.out / 8, group_shift(a.group),
-            tile * 32, a.out / 8, tile * 32 + 16, a.out / 8};
-  const Rows x{a.X + t0 * a.ldx, a.ldx, nullptr, n};
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) ring_init(bars);
+  __syncthreads();
   // input rows of this rank, in units of 256 (128) rows so that groups stay whole
   const int64_t unit = a.in >= 512 * splits ? 256 : 128, units = (a.in + unit - 1) / unit;
-  const int64_t k0 = units * rank / splits * unit;
-  int64_t k1 = units * (rank + 1) / splits * unit;
-  if (k1 > a.in) k1 = a.in;
-  Acc<NT> acc;
-  product<NT, SP, MAXTOK, STAGES>(acc, smem, w, x, (int)k0, (int)(k1 > k0 ? k1 : k0));
-  float *red = reinterpret_cast<float *>(smem);
-  store_sums<NT, SP>(acc, red);
-  pdl_wait();  // U and the cleared status word
-  if (blockIdx.x == 0) {
-    for (int t = threadIdx.x; t < n; t += kThreads) {
+  const int k0 = (int)(units * rank / splits * unit);
+  const int k1 = (int)i64min(units * (rank + 1) / splits * unit, a.in);
+  if (tid >= kConsumers) {
+    Producer<M, MAXTOK> p;
+    p.w = Weights{&map, 0, a.qzeros, a.scales, a.out / 8, group_shift(a.group),
+                  (int)(tile * 32), (int)(a.out / 8), (int)(tile * 32), (int)(a.out / 8)};
+    p.rows(a.X + t0 * a.ldx, a.ldx, n, [](int t) { return t; });
+    RingPos pos;
+    p.run(pos, smem_u32(ring), bars, k0, k1, a.max_polls, a.st);
+    if (*reinterpret_cast<volatile int *>(&bars->abort)) ring_drain(bars, pos);
+  } else {
+    RingPos pos;
+    Acc<NT> acc;
+    // the tokens' adapters, while the first words travel
+    for (int t = tid; t < MAXTOK; t += kConsumers) {
+      const int id = t < n ? __ldg(a.ids + t0 + t) : -1;
+      ids[t] = id >= 0 && id < a.adapters ? id : -1;
+    }
+    consumer_sync();
+    if (warp == 0) {  // the first token of each adapter lists it
+      int count = 0;
+      for (int c = 0; c < n; c += 32) {
+        const int t = c + lane, id = t < n ? ids[t] : -1;
+        bool first = id >= 0;
+        for (int s = 0; s < t && first; ++s) first = ids[s] != id;
+        const uint32_t b = __ballot_sync(0xffffffffu, first);
+        if (first) list[count + __popc(b & ((1u << lane) - 1u))] = id;
+        count += __popc(b);
+      }
+      if (lane == 0) *n_list = count;
+    }
+    consume<M, NT, MAXTOK, STAGES>(acc, pos, ring, bars, group_shift(a.group), k0, k1, true, a.max_polls, a.st);
+    pdl_wait();  // U and the cleared status word
+    consumer_sync();
+    const int r16 = (a.rank + 15) / 16 * 16;
+    for (int t = warp; t < MAXTOK; t += kConsumers / 32) {
+      const bool on = t < n && ids[t] >= 0;
+      const float *u = a.U + (t0 + t) * a.rank;
+      float m = 0.0f;
+      for (int k = lane; on && k < a.rank; k += 32) m = fmaxf(m, fabsf(u[k]));
+#pragma unroll
+      for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+      // 2^e with |u| / 2^e in [1, 2) at most; not for 0, infinities and the ends of the range
+      const int e = (int)(__float_as_uint(m) >> 23) - 127;
+      const bool scaled = e > -120 && e < 120;
+      const float up = scaled ? __uint_as_float((uint32_t)(127 + e) << 23) : 1.0f;
+      const float down = scaled ? __uint_as_float((uint32_t)(127 - e) << 23) : 1.0f;
+      if (lane == 0) uscale[t] = up;
+      for (int k = lane; k < r16; k += 32) {
+        const float v = on && k < a.rank ? u[k] * down : 0.0f;
+        const __half hi = __float2half_rn(v);
+        __half *d = reinterpret_cast<__half *>(uhl + t * L::kUPitch) + k;
+        *d = hi;
+        d[L::kU / 4] = __float2half_rn(isfinite(__half2float(hi)) ? v - __half2float(hi) : 0.0f);
+      }
+    }
+    consumer_sync();
+    const int nw = warp & 3, half = warp >> 2, g = lane >> 2, q = lane & 3;
+    const int64_t o0 = tile * kBoxN + (nw * 8 + g) * 8;
+    const int tt = M == Mode::kTok ? half * NT * 8 : 0;  // this warp's first token column
+    const int step = M == Mode::kK ? 2 * splits : splits, first = M == Mode::kK ? 2 * rank + half : rank;
+    const uint32_t ua = smem_u32(uhl) + (tt + (NT == 1 ? lane & 7 : (lane >> 4) * 8 + (lane & 7))) * L::kUPitch +
+                        (NT == 1 ? lane >> 3 : (lane >> 3) & 1) * 16;
+    for (int j = first; j < *n_list; j += step) {
+      const int id = list[j];
+#pragma unroll
+      for (int p = 0; p < 4; ++p)
+#pragma unroll
+        for (int x = 0; x < NT; ++x)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) acc.grp[p][x][c] = 0.0f;
+      const __half *bp = a.B + ((int64_t)id * a.out + o0) * a.rank + 2 * q;
+      const bool o_ok = o0 < a.out;  // out % 32 == 0: the 8 outputs are all in or all out
+#pragma unroll 2
+      for (int k = 0; k < r16; k += 16) {
+        uint32_t af[4][4];
+#pragma unroll
+        for (int p = 0; p < 4; ++p)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int kk = k + 8 * (i >> 1);
+            af[p][i] = o_ok && kk < a.rank
+                           ? __ldg(reinterpret_cast<const uint32_t *>(bp + (int64_t)(p + 4 * (i & 1)) * a.rank + kk))
+                           : 0u;
+          }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {  // hi, lo
+          uint32_t b[(NT + 1) / 2][4];
+#pragma unroll
+          for (int x = 0; x < (NT + 1) / 2; ++x) ldsm4(b[x], ua + h * (L::kU / 2) + x * 16 * L::kUPitch + k * 2);
+#pragma unroll
+          for (int p = 0; p < 4; ++p)
+#pragma unroll
+            for (int x = 0; x < NT; ++x)
+              mma16816(acc.grp[p][x], af[p][0], af[p][1], af[p][2], af[p][3], b[x / 2][2 * (x & 1)],
+                       b[x / 2][2 * (x & 1) + 1]);
+        }
+      }
+#pragma unroll
+      for (int x = 0; x < NT; ++x)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int t = tt + x * 8 + 2 * q + e;
+          if (ids[t] != id) continue;
+          const float sc = uscale[t];
+#pragma unroll
+          for (int p = 0; p < 4; ++p)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) acc.out[p][x][e + 2 * h] = fmaf(sc, acc.grp[p][x][e + 2 * h], acc.out[p][x][e + 2 * h]);
+        }
+    }
+    store_sums<M, NT>(acc, red);
+  }
+  if (blockIdx.x == 0 && warp == kConsumers / 32) {
+    pdl_wait();
+    for (int t = lane; t < n; t += 32) {
       const int id = a.ids[t0 + t];
       if (id < -1 || id >= a.adapters) dev_fail(a.st, kDevBadAdapter, 0xE01u);
     }
   }
   cluster.sync();
-  for (int i = rank * kThreads + threadIdx.x; i < n * (kTileN / 2); i += splits * kThreads) {
-    const int t = i / (kTileN / 2), oo = 2 * (i % (kTileN / 2));
-    const int64_t o = tile * kTileN + oo;
+  for (int i = rank * kConsumers + tid; tid < kConsumers && i < n * (kBoxN / 2); i += splits * kConsumers) {
+    const int t = i / (kBoxN / 2), oo = 2 * (i % (kBoxN / 2));
+    const int64_t o = tile * kBoxN + oo;
     if (o >= a.out) continue;
     float s0 = 0.0f, s1 = 0.0f;
+#pragma unroll 8
     for (int s = 0; s < splits; ++s) {
       const float *p = cluster.map_shared_rank(red, s) + t * kRedPitch + oo;
       s0 += p[0];
       s1 += p[1];
-    }
-    const int id = a.ids[t0 + t];
-    if (id >= 0 && id < a.adapters) {
-      const float4 *u = reinterpret_cast<const float4 *>(a.U + (t0 + t) * a.rank);
-      const uint4 *b0 = reinterpret_cast<const uint4 *>(a.B + ((int64_t)id * a.out + o) * a.rank);
-      const uint4 *b1 = b0 + a.rank / 8;
-      float l0 = 0.0f, l1 = 0.0f;
-      for (int k = 0; k < a.rank / 8; ++k) {
-        const float4 ua = u[2 * k], ub = u[2 * k + 1];
-        const float uu[8] = {ua.x, ua.y, ua.z, ua.w, ub.x, ub.y, ub.z, ub.w};
-        const uint4 p = __ldg(b0 + k), q = __ldg(b1 + k);
-        const uint32_t pw[4] = {p.x, p.y, p.z, p.w}, qw[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&pw[e]));
-          const float2 h = __half22float2(*reinterpret_cast<const __half2 *>(&qw[e]));
-          l0 = fmaf(uu[2 * e], f.x, l0);
-          l0 = fmaf(uu[2 * e + 1], f.y, l0);
-          l1 = fmaf(uu[2 * e], h.x, l1);
-          l1 = fmaf(uu[2 * e + 1], h.y, l1);
-        }
-      }
-      s0 += l0;
-      s1 += l1;
     }
     *reinterpret_cast<__half2 *>(a.Y + (t0 + t) * a.ldy + o) = __floats2half2_rn(s0, s1);
   }
   cluster.sync();  // no block leaves while its sums are read
 }
 
-template <int NT, Split SP, int MAXTOK, int STAGES, int MINB>
+template <Mode M, int NT, int MAXTOK, int STAGES, int MINB>
 cudaError_t launch_stream(const LoraArgs &a, int num_sms, cudaStream_t stream) {
   static bool done[64];
-  constexpr size_t kSmem = STAGES * stage_bytes(MAXTOK);
-  static_assert((size_t)MAXTOK * kRedPitch * 4 <= kSmem, "the sums reuse the ring");
-  auto kernel = lora_stream_kernel<NT, SP, MAXTOK, STAGES, MINB>;
+  constexpr size_t kSmem = LoraShared<M, NT, MAXTOK, STAGES>::kBytes;
+  static_assert(MINB * (kSmem + 1024) <= 233472, "resident blocks");
+  auto kernel = lora_stream_kernel<M, NT, MAXTOK, STAGES, MINB>;
   cudaError_t e = allow_smem(kernel, kSmem, done);
   if (e != cudaSuccess) return e;
-  const int64_t tiles = (a.out + kTileN - 1) / kTileN, ttiles = (a.T + MAXTOK - 1) / MAXTOK;
-  int64_t s = (int64_t)num_sms * MINB / (tiles * ttiles);
+  CUtensorMap map;  // the words as pairs of 16-bit values
+  e = make_tmap_f16_box(&map, a.qweight, a.in, a.out / 4, a.out / 4, 64, kBoxK);
+  if (e != cudaSuccess) return e;
+  const int64_t tiles = (a.out + kBoxN - 1) / kBoxN, ttiles = (a.T + MAXTOK - 1) / MAXTOK;
+  // blocks of a cluster: as many as fill the SMs, a power of two (clusters of 3
+  // or 5 leave SMs of a GPC over: 48 of 3 ran as two waves)
   const int64_t most = (a.in + 127) / 128;
-  s = s > 8 ? 8 : s;
-  s = s > most ? most : s;
-  s = s < 1 ? 1 : s;
+  int64_t s = 1;
+  while (s < 8 && 2 * s <= most && 2 * s * tiles * ttiles <= (int64_t)num_sms * MINB) s *= 2;
   cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeClusterDimension;
   at[0].val.clusterDim.x = (unsigned)s;
@@ -148,7 +260,7 @@ cudaError_t launch_stream(const LoraArgs &a, int num_sms, cudaStream_t stream) {
   cfg.stream = stream;
   cfg.attrs = at;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, kernel, a, (int)s);
+  return cudaLaunchKernelEx(&cfg, kernel, a, map, (int)s);
 }
 }  // namespace
 
@@ -157,11 +269,11 @@ cudaError_t launch_lora(const LoraArgs &a, int num_sms, cudaStream_t stream) {
   lora_shrink_kernel<<<(unsigned)blocks, 256, 0, stream>>>(a);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  if (a.T <= 8) return launch_stream<1, Split::kK, 8, 4, 2>(a, num_sms, stream);
-  if (a.T <= 16) return launch_stream<2, Split::kK, 16, 4, 2>(a, num_sms, stream);
-  if (a.T <= 32) return launch_stream<2, Split::kTok, 32, 3, 2>(a, num_sms, stream);
-  if (a.T <= 48) return launch_stream<3, Split::kTok, 48, 4, 1>(a, num_sms, stream);
-  return launch_stream<4, Split::kTok, 64, 4, 1>(a, num_sms, stream);
+  if (a.T <= 8) return launch_stream<Mode::kK, 1, 8, 4, 2>(a, num_sms, stream);
+  if (a.T <= 16) return launch_stream<Mode::kK, 2, 16, 8, 1>(a, num_sms, stream);
+  if (a.T <= 32) return launch_stream<Mode::kTok, 2, 32, 6, 1>(a, num_sms, stream);
+  if (a.T <= 48) return launch_stream<Mode::kTok, 3, 48, 6, 1>(a, num_sms, stream);
+  return launch_stream<Mode::kTok, 4, 64, 5, 1>(a, num_sms, stream);
 }
 
 }  // namespace awq

@@ -8,22 +8,24 @@
 // The layer is bound by reading the met experts' words once.  Phases, between
 // grid barriers:
 //   router   a warp per (token, expert): fp32 products summed in fp64, so that
-//            a choice next to a border is the definition's;
-//   choice   every block redoes the top-k and the experts' token lists in
-//            shared memory (nothing to wait for a second time);
-//   gate|up  tiles of 128 gate and the same 128 up outputs of one expert over
-//            its tokens, in units of 128 input rows.  The units of all tiles
-//            are dealt out evenly and in order, so a block computes the end of
-//            one tile, whole tiles, and the start of another; tiles that are
-//            split meet as fp32 partial sums, added in block order by the last
-//            block to arrive, which also applies silu(g) u;
-//   down     tiles of 256 outputs whose inner axis runs over all met experts;
-//            each expert's sums are weighted with p in fp32 and added to the
-//            block's rows of the tile;
-//   combine  the blocks' rows of a tile added in block order, one rounding.
+//            a choice next to a border is the definition's; the warp that
+//            writes a token's last logit picks its experts;
+//   lists    every block makes the experts' token lists in shared memory;
+//   gate|up  tiles of 512 consecutive outputs (256 bytes of every row: 128-byte
+//            pieces of rows read HBM at 4.6-5.0 TB/s, 256-byte ones at 6.1-6.6),
+//            gate's and up's of one expert in turn, in units of 128 input rows.
+//            The units are dealt out evenly by cost and in order; fp32 sums go
+//            to L2, and the last block to finish a pair of tiles adds them in
+//            block order and applies silu(g) u.  While the blocks meet, the
+//            producer warps load the first words of the next phase;
+//   down     the same over hidden's tiles and all met experts;
+//   combine  a token's experts' sums, weighted with p in fp32, one rounding.
 // Sums are added in an order fixed by the sizes and the routing alone.
+#include <climits>
 #include <cuda_runtime.h>
+#include <type_traits>
 
+#include "awq_launch.h"
 #include "serve_launch.h"
 #include "w4_stream.cuh"
 
@@ -31,22 +33,51 @@ namespace awq {
 namespace {
 using namespace w4s;
 
-constexpr int kMaxPairs = kMoeMaxTokens * kMoeMaxTopK;
-constexpr int kMaxSeg = kMoeMaxExperts + kMaxPairs / 32;  // (expert, up to 32 tokens) entries
+constexpr int kTile = 2 * kBoxN;  // outputs of a block's tile
+constexpr int kCap = 24;          // tokens of an entry: three token tiles are what 168 registers hold
 
-struct MoeShared {
-  int16_t id[kMaxPairs];     // chosen expert of (token, slot), -1: masked row
-  float wt[kMaxPairs];
-  int16_t pair[kMaxPairs];   // the entries' (token, slot) pairs, expert by expert
-  int row[32];               // rows of X or H of the running product
-  int16_t count[kMoeMaxExperts];
-  int16_t seg_expert[kMaxSeg], seg_first[kMaxSeg], seg_n[kMaxSeg];
+// Up to 8 tokens (V = 1), or more: the (token, slot) pairs and the entries (an
+// expert and up to kTok of its tokens) at most, the depth of the ring, the
+// resident blocks of an SM.
+template <int V>
+struct Cfg {
+  static constexpr int kTok = V == 1 ? 8 : kCap;
+  static constexpr int kPairs = (V == 1 ? 8 : kMoeMaxTokens) * kMoeMaxTopK;
+  static constexpr int kSegs = V == 1 ? kPairs : kMoeMaxExperts + kPairs / kCap + 1;
+  static constexpr int kStages = V == 1 ? 5 : 9;
+  static constexpr int kBlocks = V == 1 ? 2 : 1;
+  static constexpr uint32_t kStage = stage_bytes<Mode::kN, kTok>();
+  static constexpr uint32_t kRing = kStages * kStage;
+};
+
+// Where every block computes all logits itself: so many of them, from so many
+// router values (64 KB from L2 in about the time of a barrier).
+constexpr int kAloneLogits = 32, kAloneRouter = 32768;
+
+template <int V>
+struct MoeLists {
+  using C = Cfg<V>;
+  float wt[C::kPairs];
+  int16_t pair[C::kPairs];   // the entries' pairs, expert by expert
+  int16_t where[C::kPairs];  // position of a pair among them
+  int count[kMoeMaxExperts];
+  int16_t seg_expert[C::kSegs], seg_first[C::kSegs], seg_n[C::kSegs];
+  int seg_cost[C::kSegs + 1];  // cost of a unit, summed over the entries before
+  double logit[kAloneLogits];
+  uint8_t last[kConsumers];
   int n_seg;
   int flag;
 };
 
+template <int V>
+constexpr uint32_t moe_smem() {
+  constexpr uint32_t n = 1024 + Cfg<V>::kRing + sizeof(RingBars<Cfg<V>::kStages>) + sizeof(MoeLists<V>);
+  static_assert(Cfg<V>::kBlocks * (n + 1024) <= 233472, "resident blocks");
+  return n;
+}
+
 // All blocks meet (counter from 0 to gridDim.x); false when the wait ran out.
-__device__ __forceinline__ bool grid_barrier(uint32_t *counter, MoeShared *sh, DevStatus *st, uint32_t max_polls,
+__device__ __forceinline__ bool grid_barrier(uint32_t *counter, int *flag, DevStatus *st, uint32_t max_polls,
                                              uint32_t site) {
   __syncthreads();
   if (threadIdx.x == 0) {
@@ -65,10 +96,10 @@ __device__ __forceinline__ bool grid_barrier(uint32_t *counter, MoeShared *sh, D
       }
     }
     __threadfence();
-    sh->flag = ok;
+    *flag = ok;
   }
   __syncthreads();
-  return sh->flag != 0;
+  return *flag != 0;
 }
 
 __device__ __forceinline__ double dot8d(uint4 a, uint4 b) {
@@ -84,31 +115,27 @@ __device__ __forceinline__ double dot8d(uint4 a, uint4 b) {
   return (double)s;
 }
 
-__device__ void router(const MoeArgs &a) {
+// The logit of one (token, expert) pair by a warp.
+__device__ __forceinline__ double warp_logit(const MoeArgs &a, int t, int e) {
   const int lane = threadIdx.x & 31;
-  const int warps = gridDim.x * (kThreads / 32);
-  for (int i = blockIdx.x + gridDim.x * (threadIdx.x >> 5); i < a.T * a.experts; i += warps) {
-    const int t = i / a.experts, e = i - t * a.experts;
-    if (a.mask && !a.mask[t]) continue;
-    const uint4 *x = reinterpret_cast<const uint4 *>(a.X + t * a.ldx);
-    const uint4 *w = reinterpret_cast<const uint4 *>(a.router + (int64_t)e * a.hidden);
-    double s = 0.0;
-    for (int k = lane; k < a.hidden / 8; k += 32) s += dot8d(__ldg(x + k), __ldg(w + k));
+  const uint4 *x = reinterpret_cast<const uint4 *>(a.X + t * a.ldx);
+  const uint4 *w = reinterpret_cast<const uint4 *>(a.router + (int64_t)e * a.hidden);
+  double s = 0.0;
+#pragma unroll 8
+  for (int k = lane; k < a.hidden / 8; k += 32) s += dot8d(__ldg(x + k), __ldg(w + k));
 #pragma unroll
-    for (int m = 16; m; m >>= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
-    if (lane == 0) a.logits[i] = s + 0.0;  // -0 becomes 0: the order below is of bit patterns
-  }
+  for (int m = 16; m; m >>= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
+  return s + 0.0;  // -0 becomes 0: the choice compares bit patterns
 }
 
-// Top-k of one token by a warp; a lane holds experts lane, lane + 32, ...
-__device__ void choose(const MoeArgs &a, MoeShared *sh, int t) {
+// Top-k of one token by a warp; a lane holds experts lane, lane + 32, ...  The
+// choices go to id(slot, expert, weight).
+template <class Put>
+__device__ __forceinline__ void choose(const MoeArgs &a, const double *logits, bool masked, Put put) {
   const int lane = threadIdx.x & 31;
   constexpr int PER = kMoeMaxExperts / 32;
-  if (a.mask && !a.mask[t]) {
-    if (lane < a.top_k) {
-      sh->id[t * a.top_k + lane] = -1;
-      sh->wt[t * a.top_k + lane] = 0.0f;
-    }
+  if (masked) {
+    if (lane < a.top_k) put(lane, -1, 0.0f);
     return;
   }
   // fp64 bit patterns in an order-preserving form; NaN sorts by its bits
@@ -116,10 +143,9 @@ __device__ void choose(const MoeArgs &a, MoeShared *sh, int t) {
   double top = -INFINITY;
 #pragma unroll
   for (int j = 0; j < PER; ++j) {
-    const int e = lane + 32 * j;
     key[j] = LLONG_MIN;
-    if (e < a.experts) {
-      const double l = __ldcg(a.logits + (int64_t)t * a.experts + e);
+    if (32 * j < a.experts && lane + 32 * j < a.experts) {
+      const double l = __isGlobal(logits) ? __ldcg(logits + lane + 32 * j) : logits[lane + 32 * j];
       const long long b = __double_as_longlong(l);
       key[j] = b ^ ((b >> 63) & 0x7fffffffffffffffLL);
       top = fmax(top, l);
@@ -129,27 +155,22 @@ __device__ void choose(const MoeArgs &a, MoeShared *sh, int t) {
   for (int m = 16; m; m >>= 1) top = fmax(top, __shfl_xor_sync(0xffffffffu, top, m));
   // exp(l - top): the fp64 difference as two floats, exp of the first exact to
   // fp32 and the second's factor 1 + lo
-  float sum = 0.0f;
-  auto weight = [&](long long kk) {
+  const auto weight = [&](long long kk) {
     const long long b = kk ^ ((kk >> 63) & 0x7fffffffffffffffLL);
     const double d = __longlong_as_double(b) - top;
     const float hi = (float)d;
     const float ex = expf(hi);
     return fmaf(ex, isfinite(hi) ? (float)(d - (double)hi) : 0.0f, ex);
   };
-#pragma unroll
-  for (int j = 0; j < PER; ++j)
-    if (lane + 32 * j < a.experts) sum += weight(key[j]);
-#pragma unroll
-  for (int m = 16; m; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
   uint32_t taken = 0;
-  float mine = 0.0f, chosen = 0.0f;
+  long long my_key = 0;
   int my_id = -1;
   for (int s = 0; s < a.top_k; ++s) {
     long long best = LLONG_MIN;
     int at = 0x7fff;
 #pragma unroll
     for (int j = 0; j < PER; ++j) {
+      if (32 * j >= a.experts) break;
       const int e = lane + 32 * j;
       if (e < a.experts && !((taken >> j) & 1u) && (at == 0x7fff || key[j] > best)) {
         best = key[j];
@@ -165,274 +186,583 @@ __device__ void choose(const MoeArgs &a, MoeShared *sh, int t) {
     const bool in2 = in1 && (uint32_t)best == mlo;
     const uint32_t e = __reduce_min_sync(0xffffffffu, in2 ? (uint32_t)at : 0x7fffu);
     if ((e & 31u) == (uint32_t)lane) taken |= 1u << (e >> 5);
-    const long long kk = ((long long)mhi << 32) | (long long)mlo;
-    const float w = weight(kk);
-    chosen += w;
     if (lane == s) {
-      mine = w;
+      my_key = ((long long)mhi << 32) | (long long)mlo;
       my_id = (int)e;
     }
   }
-  if (lane < a.top_k) {
-    sh->id[t * a.top_k + lane] = (int16_t)my_id;
-    sh->wt[t * a.top_k + lane] = mine / (a.renormalize ? chosen : sum);
+  const float mine = lane < a.top_k ? weight(my_key) : 0.0f;
+  float sum = 0.0f;
+  if (a.renormalize) {
+    sum = mine;
+  } else {
+#pragma unroll
+    for (int j = 0; j < PER; ++j)
+      if (32 * j < a.experts && lane + 32 * j < a.experts) sum += weight(key[j]);
+  }
+#pragma unroll
+  for (int m = 16; m; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
+  if (lane < a.top_k) put(lane, my_id, mine / sum);
+}
+
+// Past 8 tokens: the warp that writes a token's last logit picks its experts.
+__device__ void router(const MoeArgs &a) {
+  const int lane = threadIdx.x & 31;
+  const int warps = gridDim.x * (kThreads / 32);
+  for (int i = blockIdx.x + gridDim.x * (threadIdx.x >> 5); i < a.T * a.experts; i += warps) {
+    const int t = i / a.experts, e = i - t * a.experts;
+    const bool masked = a.mask && !a.mask[t];
+    int last = masked && e == 0;
+    if (!masked) {
+      const double s = warp_logit(a, t, e);
+      if (lane == 0) {
+        a.logits[i] = s;
+        __threadfence();
+        last = atomicAdd(a.tok_count + t, 1) == a.experts - 1;
+      }
+      last = __shfl_sync(0xffffffffu, last, 0);
+    }
+    if (last) {
+      __threadfence();
+      choose(a, a.logits + (int64_t)t * a.experts, masked, [&](int slot, int id, float w) {
+        a.ids[t * a.top_k + slot] = id;
+        a.weights[t * a.top_k + slot] = w;
+      });
+    }
   }
 }
 
-// The experts' token lists, and the entries (expert, at most 32 tokens).
-__device__ void make_lists(const MoeArgs &a, MoeShared *sh) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+// Time of a unit of 128 input rows by its token tiles, measured: 174, 236 and
+// 300 cycles a step for 1, 2 and 3 tiles with 8 warps on an SM.
+__host__ __device__ constexpr int unit_cost(int n) { return n <= 8 ? 3 : n <= 16 ? 4 : 5; }
+
+// The experts' token lists, and the entries.  Every block makes its own: an
+// expert's pairs stand in rising order, since blocks that share a tile must agree
+// on the rows.
+template <int V>
+__device__ void make_lists(const MoeArgs &a, MoeLists<V> *sh) {
+  constexpr int cap = Cfg<V>::kTok;
+  const int tid = threadIdx.x, lane = tid & 31;
   const int pairs = a.T * a.top_k;
-  for (int e = warp; e < a.experts; e += kThreads / 32) {
-    int n = 0;
-    for (int c = 0; c < pairs; c += 32) n += __popc(__ballot_sync(0xffffffffu, c + lane < pairs && sh->id[c + lane] == e));
-    if (lane == 0) sh->count[e] = (int16_t)n;
+  for (int e = tid; e < a.experts; e += kThreads) sh->count[e] = 0;
+  if (V != 1)
+    for (int i = tid; i < pairs; i += kThreads) {
+      sh->pair[i] = (int16_t)__ldcg(a.ids + i);  // for now: its expert
+      sh->wt[i] = __ldcg(a.weights + i);
+    }
+  __syncthreads();
+  if (tid < 32) {  // a pair's place among its expert's
+    for (int c = 0; c < pairs; c += 32) {
+      const int i = c + lane, id = i < pairs ? sh->pair[i] : -1;
+      const uint32_t same = __match_any_sync(0xffffffffu, id), before = same & ((1u << lane) - 1u);
+      const int base = id >= 0 ? sh->count[id] : 0;
+      __syncwarp();
+      if (id >= 0 && !before) sh->count[id] = base + __popc(same);
+      if (i < pairs) sh->where[i] = (int16_t)(id >= 0 ? base + __popc(before) : -1);
+      __syncwarp();
+    }
   }
   __syncthreads();
-  if (warp == 0) {  // first pair of each expert and its entries
-    int first = 0, segs = 0;
+  if (tid < 32) {  // first pair of each expert and its entries
+    int first = 0, segs = 0, costs = 0;
     for (int c = 0; c < a.experts; c += 32) {
       const int n = c + lane < a.experts ? sh->count[c + lane] : 0;
-      const int m = (n + 31) / 32;
-      int pn = n, pm = m;
+      const int m = (n + cap - 1) / cap;
+      int cost = 0;
+      for (int j = 0; j < m; ++j) cost += unit_cost(n - cap * j < cap ? n - cap * j : cap);
+      int pn = n, pm = m, pc = cost;
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
-        const int u = __shfl_up_sync(0xffffffffu, pn, d), v = __shfl_up_sync(0xffffffffu, pm, d);
+        const int u = __shfl_up_sync(0xffffffffu, pn, d), v = __shfl_up_sync(0xffffffffu, pm, d),
+                  x = __shfl_up_sync(0xffffffffu, pc, d);
         if (lane >= d) {
           pn += u;
           pm += v;
+          pc += x;
         }
       }
+      int before = costs + pc - cost;
       for (int j = 0; j < m; ++j) {
-        const int at = segs + pm - m + j;
-        sh->seg_expert[at] = (int16_t)(c + lane);
-        sh->seg_first[at] = (int16_t)(first + pn - n + 32 * j);
-        sh->seg_n[at] = (int16_t)(n - 32 * j < 32 ? n - 32 * j : 32);
+        const int s = segs + pm - m + j;
+        sh->seg_expert[s] = (int16_t)(c + lane);
+        sh->seg_first[s] = (int16_t)(first + pn - n + cap * j);
+        sh->seg_n[s] = (int16_t)(n - cap * j < cap ? n - cap * j : cap);
+        sh->seg_cost[s] = before;
+        before += unit_cost(sh->seg_n[s]);
       }
-      if (c + lane < a.experts) sh->count[c + lane] = (int16_t)(first + pn - n);  // now: first pair
+      if (c + lane < a.experts) sh->count[c + lane] = first + pn - n;  // now: first pair
       first += __shfl_sync(0xffffffffu, pn, 31);
       segs += __shfl_sync(0xffffffffu, pm, 31);
+      costs += __shfl_sync(0xffffffffu, pc, 31);
     }
-    if (lane == 0) sh->n_seg = segs;
+    if (lane == 0) {
+      sh->n_seg = segs;
+      sh->seg_cost[segs] = costs;
+    }
   }
   __syncthreads();
-  for (int e = warp; e < a.experts; e += kThreads / 32) {
-    int at = sh->count[e];
-    for (int c = 0; c < pairs; c += 32) {
-      const bool hit = c + lane < pairs && sh->id[c + lane] == e;
-      const uint32_t b = __ballot_sync(0xffffffffu, hit);
-      if (hit) sh->pair[at + __popc(b & ((1u << lane) - 1u))] = (int16_t)(c + lane);
-      at += __popc(b);
+  constexpr int PER = (Cfg<V>::kPairs + kThreads - 1) / kThreads;
+  int id[PER];
+#pragma unroll
+  for (int j = 0; j < PER; ++j) id[j] = tid + j * kThreads < pairs ? sh->pair[tid + j * kThreads] : -1;
+  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < PER; ++j)
+    if (id[j] >= 0) {
+      const int i = tid + j * kThreads, at = sh->count[id[j]] + sh->where[i];
+      sh->pair[at] = (int16_t)i;
+      sh->where[i] = (int16_t)at;
     }
-  }
   __syncthreads();
 }
 
-// red[token][output] of the tile over rows [k0, k1), n tokens.
-template <int NT>
-__device__ __forceinline__ void tile_sums(uint8_t *smem, const Weights &w, const Rows &x, int k0, int k1) {
-  float *red = reinterpret_cast<float *>(smem);
-  Acc<NT> acc;
-  if (NT == 1 || x.n <= 16) {
-    product<NT, Split::kK, NT * 8, 4>(acc, smem, w, x, k0, k1);
-    store_sums<NT, Split::kK>(acc, red);
-  } else {
-    product<NT, Split::kTok, 2 * NT * 8, 3>(acc, smem, w, x, k0, k1);
-    store_sums<NT, Split::kTok>(acc, red);
-  }
-}
+// Rows of the down product's left side: a value of H is an fp16 and, where the
+// token tile has the columns to spare, the fp16 of what its rounding left
+// (two rows for a token: free, since the instruction computes 8 columns).
+__device__ __forceinline__ int h_rows(int n) { return 2 * n <= 8 ? 2 * n : n; }
 
 __device__ __forceinline__ float silu_mul(float g, float u) { return g / (1.0f + expf(-g)) * u; }
 
-// Units of a phase dealt out evenly: block b takes [b quota, (b + 1) quota).
-__device__ __forceinline__ int64_t quota_of(int64_t units, int64_t per_tile) {
-  int64_t q = (units + gridDim.x - 1) / gridDim.x;
-  q = (q + 1) / 2 * 2;  // both K halves of a block busy
-  return q < 1 ? 1 : (q > per_tile && units / per_tile <= gridDim.x ? per_tile : q);
-}
+// The units of a phase: for each tile, each entry and each 128 input rows, in
+// that order (gate|up: entry, then pair of tiles, then gate, up).  Blocks take
+// even shares of their cost.  `per` units of equal cost follow one another; a
+// run of them is a "stretch": (entry, tile) pairs.
+template <int V, bool DOWN>
+struct Work {
+  const MoeLists<V> *sh;
+  int n_seg, tiles, len;  // tiles: gate|up 2 x the pairs of tiles, down the tiles; len: units of a stretch
+  int64_t quota;
 
-template <int NT>
-__global__ void __launch_bounds__(kThreads, 2) moe_kernel(const __grid_constant__ MoeArgs a) {
-  extern __shared__ __align__(128) uint8_t smem[];
-  MoeShared *sh = reinterpret_cast<MoeShared *>(smem + kMoeRing);
+  __device__ __forceinline__ Work(const MoeLists<V> *l, int tiles_, int len_) : sh(l), n_seg(l->n_seg), tiles(tiles_), len(len_) {
+    const int64_t total = (int64_t)sh->seg_cost[n_seg] * tiles * len;
+    quota = (total + gridDim.x - 1) / gridDim.x;
+    // at least a unit's cost, so that every block between a stretch's first and last has a unit of it
+    quota = quota < unit_cost(Cfg<V>::kTok) ? unit_cost(Cfg<V>::kTok) : quota;
+  }
+  __device__ __forceinline__ int cost(int seg) const { return sh->seg_cost[seg + 1] - sh->seg_cost[seg]; }
+  // stretch = seg * tiles + tile (gate|up), tile * n_seg + seg (down)
+  __device__ __forceinline__ int seg_of(int stretch) const { return DOWN ? stretch % n_seg : stretch / tiles; }
+  __device__ __forceinline__ int tile_of(int stretch) const { return DOWN ? stretch / n_seg : stretch % tiles; }
+  __device__ __forceinline__ int64_t cost_before(int stretch) const {
+    const int seg = seg_of(stretch), tile = tile_of(stretch);
+    const int64_t c = DOWN ? (int64_t)tile * sh->seg_cost[n_seg] + sh->seg_cost[seg]
+                           : (int64_t)sh->seg_cost[seg] * tiles + (int64_t)tile * cost(seg);
+    return c * len;
+  }
+  // Units of a stretch that a block takes begin at its first unit whose cost
+  // offset is at least the block's share: first unit of block b in the stretch.
+  __device__ __forceinline__ int first_unit(int stretch, int64_t b) const {
+    const int64_t d = b * quota - cost_before(stretch);
+    const int c = cost(seg_of(stretch));
+    const int64_t u = d <= 0 ? 0 : (d + c - 1) / c;
+    return (int)(u < len ? u : len);
+  }
+  // The blocks that take units of a stretch: those of its first and last unit.
+  __device__ __forceinline__ int block_of(int stretch, int unit) const {
+    return (int)((cost_before(stretch) + (int64_t)unit * cost(seg_of(stretch))) / quota);
+  }
+  // The stretch that holds cost offset c.
+  __device__ __forceinline__ int find(int64_t c) const {
+    int lo = 0, hi = n_seg * tiles;  // the last stretch with cost_before <= c
+    while (hi - lo > 1) {
+      const int m = (lo + hi) / 2;
+      if (cost_before(m) <= c)
+        lo = m;
+      else
+        hi = m;
+    }
+    return lo;
+  }
+};
+
+template <int V>
+__global__ void __launch_bounds__(kThreads, Cfg<V>::kBlocks)
+    moe_kernel(const __grid_constant__ MoeArgs a, const __grid_constant__ CUtensorMap gu_map,
+               const __grid_constant__ CUtensorMap dn_map) {
+  using C = Cfg<V>;
+  extern __shared__ uint8_t raw[];
+  uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
+  auto *bars = reinterpret_cast<RingBars<C::kStages> *>(ring + C::kRing);
+  auto *sh = reinterpret_cast<MoeLists<V> *>(bars + 1);
+  const uint32_t ring_u = smem_u32(ring);
   const int tid = threadIdx.x;
   DevStatus *st = a.st;
   const int shift = group_shift(a.group);
-  const int64_t itiles = (a.inter + 127) / 128, htiles = (a.hidden + kTileN - 1) / kTileN;
-  const int64_t kgh = (a.hidden + 127) / 128, kgi = (a.inter + 127) / 128;
+  const int hidden = (int)a.hidden, inter = (int)a.inter;
+  const int itiles = (inter + kTile - 1) / kTile, htiles = (hidden + kTile - 1) / kTile;
+  const int kgh = (hidden + 127) / 128, kgi = (inter + 127) / 128;
 
-  // counters of split gate|up tiles
-  for (int64_t i = blockIdx.x * (int64_t)kThreads + tid; i < a.max_seg * itiles; i += (int64_t)gridDim.x * kThreads)
-    a.tile_count[i] = 0;
-  router(a);
-  if (!grid_barrier(a.barrier + 0, sh, st, a.max_polls, 0xE10u)) return;
-  for (int t = tid >> 5; t < a.T; t += kThreads / 32) choose(a, sh, t);
-  __syncthreads();
-  make_lists(a, sh);
-  if (blockIdx.x == 0)
-    for (int i = tid; i < a.T * a.top_k; i += kThreads) {
-      a.ids[i] = sh->id[i];
-      a.weights[i] = sh->wt[i];
+  if (tid == 0) {
+    ring_init(bars);
+    tma_prefetch_desc(&gu_map);
+    tma_prefetch_desc(&dn_map);
+  }
+  if (V == 1) {
+    // A few tokens: every block chooses for itself, from logits that the blocks
+    // compute together, or each on its own where that is cheaper than meeting
+    // (a barrier is 1.8 us)
+    const int warp = tid >> 5, lane = tid & 31;
+    const bool alone = a.T * a.experts <= kAloneLogits && a.experts * hidden <= kAloneRouter;
+    const int first = alone ? warp : (int)blockIdx.x + (int)gridDim.x * warp;
+    const int step = (alone ? 1 : (int)gridDim.x) * (kThreads / 32);
+    for (int i = first; i < a.T * a.experts; i += step) {
+      const int t = i / a.experts;
+      if (a.mask && !a.mask[t]) continue;
+      const double l = warp_logit(a, t, i - t * a.experts);
+      if (lane == 0) (alone ? sh->logit : a.logits)[i] = l;
     }
-  const int n_seg = sh->n_seg;
+    if (alone)
+      __syncthreads();
+    else if (!grid_barrier(a.barrier + 0, &sh->flag, st, a.max_polls, 0xE10u))
+      return;
+    for (int t = warp; t < a.T; t += kThreads / 32)
+      choose(a, (alone ? sh->logit : a.logits) + (int64_t)t * a.experts, a.mask && !a.mask[t],
+             [&](int slot, int id, float w) {
+               sh->pair[t * a.top_k + slot] = (int16_t)id;
+               sh->wt[t * a.top_k + slot] = w;
+               if (blockIdx.x == 0) {
+                 a.ids[t * a.top_k + slot] = id;
+                 a.weights[t * a.top_k + slot] = w;
+               }
+             });
+  } else {
+    // counters of the pairs of gate|up tiles
+    for (int64_t i = blockIdx.x * (int64_t)kThreads + tid; i < a.max_seg * itiles; i += (int64_t)gridDim.x * kThreads)
+      a.tile_count[i] = 0;
+    router(a);
+    if (!grid_barrier(a.barrier + 0, &sh->flag, st, a.max_polls, 0xE10u)) return;
+  }
+  make_lists<V>(a, sh);
 
-  // ---------------------------------------------------------------- gate|up
-  {
-    const int64_t units = n_seg * itiles * kgh, quota = quota_of(units, kgh);
-    int64_t u = (int64_t)blockIdx.x * quota;
-    const int64_t u_end = u + quota < units ? u + quota : units;
-    float *red = reinterpret_cast<float *>(smem);
-    const int64_t wo = 2 * a.inter / 8;
-    while (u < u_end) {
-      const int64_t tile = u / kgh, g0 = u - tile * kgh;
-      const int64_t g1 = g0 + (u_end - u) < kgh ? g0 + (u_end - u) : kgh;
-      const int s = (int)(tile / itiles);
-      const int64_t it = tile - s * itiles;
-      const int e = sh->seg_expert[s], p0 = sh->seg_first[s], n = sh->seg_n[s];
-      __syncthreads();
-      if (tid < n) sh->row[tid] = sh->pair[p0 + tid] / a.top_k;
-      __syncthreads();
-      Weights w{a.gu_q + e * a.hidden * wo, a.gu_z + e * (a.hidden / a.group) * wo,
-                a.gu_s + e * (a.hidden / a.group) * wo * 8, wo, shift, it * 16, wo / 2, wo / 2 + it * 16, wo};
-      Rows x{a.X, a.ldx, sh->row, n};
-      const int k1 = (int)(g1 * 128 < a.hidden ? g1 * 128 : a.hidden);
-      tile_sums<NT>(smem, w, x, (int)g0 * 128, k1);
-      bool done = true;
-      const int64_t b0 = tile * kgh / quota, b1 = ((tile + 1) * kgh - 1) / quota;  // the tile's blocks
-      const int rows = NT == 1 ? 8 : 32;
-      if (b0 != b1) {
-        float *slot = a.partial + ((int64_t)blockIdx.x * 2 + (g0 == 0)) * rows * kTileN;
-        for (int t = 0; t < n; ++t) slot[t * kTileN + tid] = red[t * kRedPitch + tid];
-        __threadfence();
-        __syncthreads();
-        if (tid == 0) sh->flag = atomicAdd(a.tile_count + tile, 1) == (int)(b1 - b0);
-        __syncthreads();
-        done = sh->flag != 0;
-        if (done) {
-          __threadfence();
-          for (int t = 0; t < n; ++t) {
-            float v = 0.0f;
-            for (int64_t b = b0; b <= b1; ++b)
-              v += __ldcg(a.partial + (b * 2 + (b == b0)) * rows * kTileN + t * kTileN + tid);
-            red[t * kRedPitch + tid] = v;
+  const Work<V, false> up(sh, 2 * itiles, kgh);
+  const Work<V, true> down(sh, htiles, kgi);
+  const int wi = inter / 8, wh = hidden / 8;  // word columns
+  const int64_t up_end = (int64_t)up.n_seg * up.tiles, dn_end = (int64_t)down.n_seg * down.tiles;
+  const int64_t pitch_gu = 2 * a.inter;  // a row of the gate|up sums
+  // the words of a stretch
+  const auto up_weights = [&](int stretch) {
+    const int e = sh->seg_expert[up.seg_of(stretch)], tile = up.tile_of(stretch);
+    const int64_t groups = (int64_t)e * (hidden / a.group);
+    const int c0 = (tile & 1) * wi + (tile >> 1) * 64, end = (tile & 1) ? 2 * wi : wi;
+    return Weights{&gu_map, e * hidden, a.gu_z + groups * 2 * wi, a.gu_s + groups * 2 * inter, 2 * wi, shift,
+                   c0, end, c0 + 32, end};
+  };
+  const auto down_weights = [&](int stretch) {
+    const int e = sh->seg_expert[down.seg_of(stretch)], c0 = down.tile_of(stretch) * 64;
+    const int64_t groups = (int64_t)e * (inter / a.group);
+    return Weights{&dn_map, e * inter, a.dn_z + groups * wh, a.dn_s + groups * hidden, wh, shift, c0, wh, c0 + 32, wh};
+  };
+  const int up_first = up_end ? up.find((int64_t)blockIdx.x * up.quota) : 0;
+  const int dn_first = dn_end ? down.find((int64_t)blockIdx.x * down.quota) : 0;
+  bool ok = true;
+
+  if (tid >= kConsumers) {
+    // ------------------------------------------------------------ producer
+    RingPos pos;
+    {
+      for (int s = up_first; s < up_end; ++s) {
+        const int u0 = up.first_unit(s, blockIdx.x), u1 = up.first_unit(s, blockIdx.x + 1);
+        if (u0 >= u1) {
+          if (u0 < up.len) break;  // the block's share ended
+          continue;
+        }
+        Producer<Mode::kN, C::kTok> p;
+        p.w = up_weights(s);
+        const int seg = up.seg_of(s), p0 = sh->seg_first[seg];
+        p.rows(a.X, a.ldx, sh->seg_n[seg], [&](int t) { return sh->pair[p0 + t] / a.top_k; });
+        p.template run<C::kStages>(pos, ring_u, bars, u0 * 128, min(u1 * 128, hidden), a.max_polls, st);
+      }
+    }
+    // the first words of a down stretch do not wait for its H
+    const auto words_ahead = [&](const Producer<Mode::kN, C::kTok> &p, int k0, int k1) {
+      RingPos r = pos;
+      const int most = min(num_stages<Mode::kN>(k1 - k0), C::kStages);
+      int n = 0;
+      while (n < most && ring_wait(bars, &bars->empty[r.slot], r.phase ^ 1u, a.max_polls, st, 0xE22u)) {
+        p.issue_words(ring_u + r.slot * C::kStage, &bars->full[r.slot], k0, k1, n++);
+        r.next<C::kStages>();
+      }
+      return n;
+    };
+    bool met = false;
+    int ahead = 0;
+    for (int s = dn_first; s < dn_end && ok; ++s) {
+      const int u0 = down.first_unit(s, blockIdx.x), u1 = down.first_unit(s, blockIdx.x + 1);
+      if (u0 >= u1) {
+        if (u0 < down.len) break;
+        continue;
+      }
+      Producer<Mode::kN, C::kTok> p;
+      p.w = down_weights(s);
+      const int seg = down.seg_of(s), p0 = sh->seg_first[seg], n = sh->seg_n[seg], pairs = a.T * a.top_k;
+      const int k0 = u0 * 128, k1 = min(u1 * 128, inter);
+      ahead = V == 1 || !met ? words_ahead(p, k0, k1) : 0;
+      if (!met) {
+        met = true;
+        ok = grid_barrier(a.barrier + 1, &sh->flag, st, a.max_polls, 0xE11u);
+        if (!ok) break;
+      }
+      if (V == 1) asm volatile("bar.sync 2, 288;" ::: "memory");  // H of this range is there
+      p.rows(a.H, inter, h_rows(n),
+             [&](int t) { return t < n ? sh->pair[p0 + t] : pairs + sh->pair[p0 + t - n]; });
+      p.template run<C::kStages>(pos, ring_u, bars, k0, k1, a.max_polls, st, ahead);
+      ahead = 0;
+    }
+    if (!met) ok = grid_barrier(a.barrier + 1, &sh->flag, st, a.max_polls, 0xE11u);
+    for (int i = 0; i < ahead; ++i) pos.next<C::kStages>();
+    if (!ok || *reinterpret_cast<volatile int *>(&bars->abort)) ring_drain(bars, pos);
+  } else {
+    // ------------------------------------------------------------ consumers
+    const int warp = tid >> 5, lane = tid & 31, g = lane >> 2, q = lane & 3;
+    const int lane_col = (warp >> 2) * kBoxN + ((warp & 3) * 8 + g) * 8;  // first of this lane's 8 outputs in a tile
+    RingPos pos;
+    // sums of rows [k0, k1) into d(token row) + column, for `rows` token rows and `cols` outputs
+    const auto sums = [&](int rows, int k0, int k1, int cols, auto dst) {
+      const auto run = [&](auto nt) {
+        constexpr int NT = decltype(nt)::value;
+        Acc<NT> acc;
+        consume<Mode::kN, NT, C::kTok, C::kStages>(acc, pos, ring, bars, shift, k0, k1, cols > kBoxN, a.max_polls, st);
+        if (lane_col >= cols) return;
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int t = n * 8 + 2 * q + e;
+            float v[8];
+            outputs8<NT>(acc, n, e, v);
+            if (t < rows) {
+              float4 *d = reinterpret_cast<float4 *>(dst(t) + lane_col);
+              __stcg(d, make_float4(v[0], v[1], v[2], v[3]));
+              __stcg(d + 1, make_float4(v[4], v[5], v[6], v[7]));
+            }
           }
-          __syncthreads();
-        }
-      }
-      if (done)
-        for (int i = tid; i < n * 128; i += kThreads) {
-          const int t = i >> 7, c = i & 127;
-          if (it * 128 + c < a.inter)
-            a.H[(int64_t)sh->pair[p0 + t] * a.inter + it * 128 + c] =
-                __float2half_rn(silu_mul(red[t * kRedPitch + c], red[t * kRedPitch + 128 + c]));
-        }
-      u += g1 - g0;
-    }
-  }
-  if (!grid_barrier(a.barrier + 1, sh, st, a.max_polls, 0xE11u)) return;
+      };
+      if (V == 1 || rows <= 8)
+        run(std::integral_constant<int, 1>{});
+      else if (rows <= 16)
+        run(std::integral_constant<int, 2>{});
+      else
+        run(std::integral_constant<int, 3>{});
+    };
+    // a block's two partial tiles: one it enters inside, one it leaves inside
+    const auto slot = [&](int64_t b, int which) { return a.partial + (b * 2 + which) * C::kTok * kTile; };
+    const auto dn_slot = [&](int64_t b, int which) { return a.dn_partial + (b * 2 + which) * C::kTok * kTile; };
 
-  // ------------------------------------------------------------------- down
-  const int64_t per_tile = n_seg * kgi, units = htiles * per_tile;
-  const int64_t quota = per_tile ? quota_of(units, per_tile) : 1;
-  {
-    int64_t u = (int64_t)blockIdx.x * quota;
-    const int64_t u_end = u + quota < units ? u + quota : units;
-    const float *red = reinterpret_cast<const float *>(smem);
-    const int64_t wo = a.hidden / 8;
-    float *slot = nullptr;
-    int64_t cur = -1;
-    while (u < u_end) {
-      const int64_t tile = u / per_tile, in_tile = u - tile * per_tile;
-      if (tile != cur) {  // this block's rows of the tile: thread tid owns column tid
-        cur = tile;
-        slot = a.partial + ((int64_t)blockIdx.x * 2 + (in_tile == 0)) * a.T * kTileN;
-        for (int t = 0; t < a.T; ++t) slot[t * kTileN + tid] = 0.0f;
+    for (int s = up_first; s < up_end; ++s) {
+      const int u0 = up.first_unit(s, blockIdx.x), u1 = up.first_unit(s, blockIdx.x + 1);
+      if (u0 >= u1) {
+        if (u0 < up.len) break;
+        continue;
       }
-      const int s = (int)(in_tile / kgi);
-      const int64_t g0 = in_tile - s * kgi;
-      const int64_t g1 = g0 + (u_end - u) < kgi ? g0 + (u_end - u) : kgi;
-      const int e = sh->seg_expert[s], p0 = sh->seg_first[s], n = sh->seg_n[s];
-      __syncthreads();
-      if (tid < n) sh->row[tid] = sh->pair[p0 + tid];
-      __syncthreads();
-      Weights w{a.dn_q + e * a.inter * wo, a.dn_z + e * (a.inter / a.group) * wo,
-                a.dn_s + e * (a.inter / a.group) * wo * 8, wo, shift, tile * 32, wo, tile * 32 + 16, wo};
-      Rows x{a.H, a.inter, sh->row, n};
-      const int k1 = (int)(g1 * 128 < a.inter ? g1 * 128 : a.inter);
-      tile_sums<NT>(smem, w, x, (int)g0 * 128, k1);
-      for (int t = 0; t < n; ++t) {
-        const int p = sh->pair[p0 + t];
-        float *d = slot + (p / a.top_k) * kTileN + tid;
-        *d = fmaf(sh->wt[p], red[t * kRedPitch + tid], *d);
+      const int seg = up.seg_of(s), tile = up.tile_of(s), p0 = sh->seg_first[seg], n = sh->seg_n[seg];
+      const int ch = (tile >> 1) * kTile, cols = min(kTile, inter - ch);  // the tile's channels
+      const bool whole = u0 == 0 && u1 == up.len;
+      float *part = slot(blockIdx.x, u0 == 0);
+      float *gu = a.sums + (tile & 1) * a.inter + ch;
+      sums(n, u0 * 128, min(u1 * 128, hidden), cols, [&](int t) {
+        return whole ? gu + sh->pair[p0 + t] * pitch_gu : part + t * kTile;
+      });
+    }
+    // four channels of H for row t of entry seg: the sums of the blocks that
+    // share gate's and up's tile, silu(g) u, and what its rounding leaves
+    const auto finish = [&](int sg, int t, int c) {
+      const int su = sg + 1, seg = up.seg_of(sg), ch = (up.tile_of(sg) >> 1) * kTile;
+      const int64_t row = sh->pair[sh->seg_first[seg] + t];
+      const auto gather = [&](int stretch, int64_t off) {
+        const int first = up.block_of(stretch, 0), last = up.block_of(stretch, up.len - 1);
+        if (first == last) return __ldcg(reinterpret_cast<const float4 *>(a.sums + row * pitch_gu + off + ch + c));
+        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        for (int b = first; b <= last; ++b) {  // all but the first block enter inside the tile
+          const float4 p = __ldcg(reinterpret_cast<const float4 *>(slot(b, b == first) + t * kTile + c));
+          v.x += p.x;
+          v.y += p.y;
+          v.z += p.z;
+          v.w += p.w;
+        }
+        return v;
+      };
+      const float4 gv = gather(sg, 0), uv = gather(su, a.inter);
+      const float h[4] = {silu_mul(gv.x, uv.x), silu_mul(gv.y, uv.y), silu_mul(gv.z, uv.z), silu_mul(gv.w, uv.w)};
+      __align__(8) __half hi[4], rest[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        hi[k] = __float2half_rn(h[k]);
+        rest[k] = __float2half_rn(isfinite(h[k]) ? h[k] - __half2float(hi[k]) : 0.0f);
       }
-      u += g1 - g0;
+      __half *d = a.H + row * inter + ch + c;
+      *reinterpret_cast<uint2 *>(d) = *reinterpret_cast<const uint2 *>(hi);
+      if (h_rows(sh->seg_n[seg]) > sh->seg_n[seg])
+        *reinterpret_cast<uint2 *>(d + (int64_t)a.T * a.top_k * inter) = *reinterpret_cast<const uint2 *>(rest);
+    };
+    if (V != 1) {
+      // the last block to arrive at a pair of tiles finishes it
+      __threadfence();
+      consumer_sync();
+      for (int base = up_first; base < up_end; base += kConsumers) {
+        const int s = base + tid;
+        bool mine = false, more = false;
+        if (s < up_end) {
+          const int u0 = up.first_unit(s, blockIdx.x), u1 = up.first_unit(s, blockIdx.x + 1);
+          mine = u0 < u1;
+          more = mine || u0 >= up.len;
+        }
+        int last = 0;
+        if (mine) {
+          const int sg = s - (up.tile_of(s) & 1), su = sg + 1;
+          const int arrivals = up.block_of(sg, up.len - 1) - up.block_of(sg, 0) + up.block_of(su, up.len - 1) -
+                               up.block_of(su, 0) + 2;
+          last = atomicAdd(a.tile_count + sg / 2, 1) == arrivals - 1;
+        }
+        sh->last[tid] = (uint8_t)last;
+        const int run = consumer_count(more);  // stretches before the block's end, from `base`
+        __threadfence();
+        for (int j = 0; j < run; ++j) {
+          if (!sh->last[j]) continue;
+          const int sg = base + j - (up.tile_of(base + j) & 1), n = sh->seg_n[up.seg_of(sg)];
+          const int quads = min(kTile, inter - (up.tile_of(sg) >> 1) * kTile) / 4;
+          for (int i = tid; i < n * quads; i += kConsumers) finish(sg, i / quads, 4 * (i % quads));
+        }
+        consumer_sync();
+        if (run < kConsumers) break;
+      }
+    }
+    ok = grid_barrier(a.barrier + 1, &sh->flag, st, a.max_polls, 0xE11u);
+    if (ok) {
+      for (int s = dn_first; s < dn_end; ++s) {
+        const int u0 = down.first_unit(s, blockIdx.x), u1 = down.first_unit(s, blockIdx.x + 1);
+        if (u0 >= u1) {
+          if (u0 < down.len) break;
+          continue;
+        }
+        const int seg = down.seg_of(s), ch = down.tile_of(s) * kTile, p0 = sh->seg_first[seg], n = sh->seg_n[seg];
+        const bool whole = u0 == 0 && u1 == down.len;
+        float *part = dn_slot(blockIdx.x, u0 == 0);
+        const int rows = h_rows(n), pairs = a.T * a.top_k;
+        if (V == 1) {
+          // the block makes the H it reads: other blocks may write the same values
+          const int k0 = u0 * 128, quads = (min(u1 * 128, inter) - k0) / 4;
+          for (int i = tid; i < n * quads; i += kConsumers) {
+            const int c = k0 + 4 * (i % quads);
+            finish(seg * up.tiles + 2 * (c / kTile), i / quads, c % kTile);
+          }
+          asm volatile("bar.sync 2, 288;" ::: "memory");  // the producer waits for it
+        }
+        sums(rows, u0 * 128, min(u1 * 128, inter), min(kTile, hidden - ch), [&](int t) {
+          // the remainders' sums have rows of their own
+          return whole ? a.dn_sums + (int64_t)(t < n ? sh->pair[p0 + t] : pairs + sh->pair[p0 + t - n]) * hidden + ch
+                       : part + t * kTile;
+        });
+      }
     }
   }
-  if (!grid_barrier(a.barrier + 2, sh, st, a.max_polls, 0xE12u)) return;
+  if (!ok) return;
+  if (!grid_barrier(a.barrier + 2, &sh->flag, st, a.max_polls, 0xE12u)) return;
 
   // ---------------------------------------------------------------- combine
-  const int64_t half = a.hidden / 2;
-  for (int64_t i = blockIdx.x * (int64_t)kThreads + tid; i < a.T * half; i += (int64_t)gridDim.x * kThreads) {
-    const int64_t t = i / half, o = 2 * (i - t * half), tile = o / kTileN;
-    float2 v = make_float2(0.0f, 0.0f);
-    if (units) {
-      const int64_t b0 = tile * per_tile / quota, b1 = ((tile + 1) * per_tile - 1) / quota;
-      for (int64_t b = b0; b <= b1; ++b) {
-        // a block that starts inside the tile uses its first slot for it
-        const float2 p = __ldcg(reinterpret_cast<const float2 *>(
-            a.partial + ((b * 2 + (b * quota <= tile * per_tile)) * a.T + t) * kTileN + (o - tile * kTileN)));
-        v.x += p.x;
-        v.y += p.y;
+  const int quads = hidden / 4;
+  for (int i = blockIdx.x * kThreads + tid; i < a.T * quads; i += gridDim.x * kThreads) {
+    const int t = i / quads, o = 4 * (i - t * quads), tile = o / kTile;
+    float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int k = 0; k < a.top_k; ++k) {
+      const int p = t * a.top_k + k;
+      const int at = sh->where[p];
+      if (at < 0) continue;  // a masked row
+      int seg = 0;  // the entry that holds position `at`
+      {
+        int lo = 0, hi = down.n_seg;
+        while (hi - lo > 1) {
+          const int m = (lo + hi) / 2;
+          if (sh->seg_first[m] <= at)
+            lo = m;
+          else
+            hi = m;
+        }
+        seg = lo;
       }
+      const int stretch = tile * down.n_seg + seg, n = sh->seg_n[seg], row = at - sh->seg_first[seg];
+      const int b0 = down.block_of(stretch, 0), b1 = down.block_of(stretch, down.len - 1);
+      const bool two = h_rows(n) > n;
+      float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      const auto add = [&](const float *src) {
+        const float4 x = __ldcg(reinterpret_cast<const float4 *>(src));
+        v.x += x.x;
+        v.y += x.y;
+        v.z += x.z;
+        v.w += x.w;
+      };
+      if (b0 == b1) {
+        add(a.dn_sums + (int64_t)p * hidden + o);
+        if (two) add(a.dn_sums + (int64_t)(a.T * a.top_k + p) * hidden + o);
+      } else {
+        for (int b = b0; b <= b1; ++b) {
+          const float *src = a.dn_partial + ((int64_t)b * 2 + (b == b0)) * C::kTok * kTile + row * kTile + o - tile * kTile;
+          add(src);
+          if (two) add(src + n * kTile);
+        }
+      }
+      const float w = sh->wt[p];
+      y.x = fmaf(w, v.x, y.x);
+      y.y = fmaf(w, v.y, y.y);
+      y.z = fmaf(w, v.z, y.z);
+      y.w = fmaf(w, v.w, y.w);
     }
-    *reinterpret_cast<__half2 *>(a.Y + t * a.ldy + o) = __floats2half2_rn(v.x, v.y);
+    const __half2 h0 = __floats2half2_rn(y.x, y.y), h1 = __floats2half2_rn(y.z, y.w);
+    *reinterpret_cast<uint2 *>(a.Y + t * a.ldy + o) =
+        make_uint2(*reinterpret_cast<const uint32_t *>(&h0), *reinterpret_cast<const uint32_t *>(&h1));
   }
 }
 
-template <int NT>
-cudaError_t go(const MoeArgs &a, int blocks, cudaStream_t stream) {
+template <int V>
+cudaError_t go(const MoeArgs &a, int num_sms, cudaStream_t stream) {
   static bool done[64];
-  cudaError_t e = allow_smem(moe_kernel<NT>, kMoeRing + sizeof(MoeShared), done);
+  cudaError_t e = allow_smem(moe_kernel<V>, moe_smem<V>(), done);
+  if (e != cudaSuccess) return e;
+  CUtensorMap gu, dn;  // the words of all experts as pairs of 16-bit values
+  e = make_tmap_f16_box(&gu, a.gu_q, a.experts * a.hidden, a.inter / 2, a.inter / 2, 64, kBoxK);
+  if (e != cudaSuccess) return e;
+  e = make_tmap_f16_box(&dn, a.dn_q, a.experts * a.inter, a.hidden / 4, a.hidden / 4, 64, kBoxK);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeCooperative;
   at[0].val.cooperative = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)blocks);
+  cfg.gridDim = dim3((unsigned)(Cfg<V>::kBlocks * num_sms));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = kMoeRing + sizeof(MoeShared);
+  cfg.dynamicSmemBytes = moe_smem<V>();
   cfg.stream = stream;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, moe_kernel<NT>, a);
+  return cudaLaunchKernelEx(&cfg, moe_kernel<V>, a, gu, dn);
 }
-
-static_assert(kMoeRing >= 4 * stage_bytes(16) && kMoeRing >= 3 * stage_bytes(32), "ring");
-static_assert(32 * kRedPitch * 4 <= kMoeRing, "the sums reuse the ring");
-static_assert(2 * (kMoeRing + sizeof(MoeShared) + 1024) <= 233472, "two blocks per SM");
 }  // namespace
 
 cudaError_t launch_moe(const MoeArgs &a, int num_sms, cudaStream_t stream) {
-  cudaError_t e = cudaMemsetAsync(a.st, 0, 256, stream);  // status word and barrier counters
+  cudaError_t e = cudaMemsetAsync(a.st, 0, 512, stream);  // status word and counters
   if (e != cudaSuccess) return e;
-  return a.T <= 8 ? go<1>(a, 2 * num_sms, stream) : go<2>(a, 2 * num_sms, stream);
+  return a.T <= 8 ? go<1>(a, num_sms, stream) : go<2>(a, num_sms, stream);
 }
 
 MoeLayout moe_layout(int64_t T, int64_t hidden, int64_t inter, int64_t experts, int64_t top_k, int num_sms) {
   MoeLayout l;
   const int64_t pairs = T * top_k;
-  l.max_seg = (experts < pairs ? experts : pairs) + pairs / 32;
+  l.max_seg = (experts < pairs ? experts : pairs) + pairs / kCap + 1;
   auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
-  size_t off = 256;
+  size_t off = 512;
   l.logits = off;
   off = up(off + sizeof(double) * (size_t)(T * experts));
   l.tile_count = off;
-  off = up(off + sizeof(int) * (size_t)(l.max_seg * ((inter + 127) / 128)));
-  l.H = off;
-  off = up(off + sizeof(__half) * (size_t)(pairs * inter));
-  l.partial = off;
-  const int64_t rows = i64max_(T, T <= 8 ? 8 : 32);
-  off = up(off + sizeof(float) * (size_t)(2 * num_sms * 2 * rows * kTileN));
+  off = up(off + sizeof(int) * (size_t)(l.max_seg * ((inter + kTile - 1) / kTile)));
+  l.H = off;  // and the remainders
+  off = up(off + 2 * sizeof(__half) * (size_t)(pairs * inter));
+  l.sums = off;  // whole tiles' sums: gate|up, and down (the remainders' apart)
+  off = up(off + 2 * sizeof(float) * (size_t)(pairs * inter));
+  l.dn_sums = off;
+  off = up(off + 2 * sizeof(float) * (size_t)(pairs * hidden));
+  const int64_t blocks = T <= 8 ? 2 * num_sms : num_sms, rows = T <= 8 ? 8 : kCap;
+  l.partial = off;  // split tiles' sums, by block
+  off = up(off + sizeof(float) * (size_t)(blocks * 2 * rows * kTile));
+  l.dn_partial = off;
+  off = up(off + sizeof(float) * (size_t)(blocks * 2 * rows * kTile));
   l.end = off;
   return l;
 }

@@ -40,6 +40,7 @@ struct LoraArgs {
   int64_t ldy;
   float *U;       // workspace: [T, rank] fp32
   DevStatus *st;
+  uint32_t max_polls;
 };
 // Y = X W^T + c_a (X A_a^T) B_a^T; in % 64 == 0, out % 32 == 0, rank % 8 == 0.
 cudaError_t launch_lora(const LoraArgs &a, int num_sms, cudaStream_t stream);
@@ -53,7 +54,6 @@ struct NormArgs {
 cudaError_t launch_block_norm(const NormArgs &a, cudaStream_t stream);
 
 constexpr int kMoeMaxTokens = 64, kMoeMaxTopK = 16, kMoeMaxExperts = 256;
-constexpr uint32_t kMoeRing = 96256;  // shared memory of the cp.async ring
 
 struct MoeArgs {
   const __half *X;
@@ -71,16 +71,18 @@ struct MoeArgs {
   int32_t *ids;
   float *weights;
   // workspace
-  DevStatus *st;
-  uint32_t *barrier;       // 3 counters, in the status word's 256 bytes
+  DevStatus *st;           // 512 bytes cleared by the launch: status word,
+  uint32_t *barrier;       // 3 counters,
+  int *tok_count;          // [T] logits written
   double *logits;
   int *tile_count;
   __half *H;
-  float *partial;
+  float *sums, *dn_sums;        // [pairs, 2 inter]; [2 pairs, hidden]
+  float *partial, *dn_partial;  // [blocks, 2, rows, 512] each
   uint32_t max_polls;
 };
 struct MoeLayout {
-  size_t logits, tile_count, H, partial, end;
+  size_t logits, tile_count, H, sums, dn_sums, partial, dn_partial, end;
   int64_t max_seg;
 };
 __host__ __device__ constexpr int64_t i64max_(int64_t a, int64_t b) { return a > b ? a : b; }

@@ -4,29 +4,33 @@
 //
 //   S[t][o] = sum over k in [k0, k1) of x[t][k] (q - z)[k][o] s[k/g][o]
 //
-// Mathematics.  Within a group the step is common, so
-//   S = sum_groups s (sum_k q x - z sum_k x):
-// the codes themselves are the A operand.  A nibble at bit 0 (bit 4) of a
-// 16-bit half, read as fp16, is the subnormal q 2^-24 (q 2^-20), exactly, so
-// a code needs one AND and no conversion; sum_k x comes from one more MMA
-// whose A operand is 2^-24 everywhere.  Products are exact in fp32, the group
-// sums and their scaled total are fp32, and no weight is rounded to fp16.
+// Mathematics.  Within a group the step is common: S = sum_groups s (sum_k
+// (q - z) x).  The integers q - z are the A operand: a nibble at bit 0 (bit 4)
+// of a 16-bit half, read as fp16, is the subnormal q 2^-24 (q 2^-20), so a code
+// needs one AND and no conversion, and subtracting the zero point's subnormal
+// is exact.  Products are exact in fp32, the group sums and their scaled total
+// are fp32, and no weight is rounded to fp16.
 //
-// Layout.  m16n8k16: 16 rows = 8 word columns x 2 nibbles (p, p + 4), 16
-// k = 4 consecutive input rows for each of the 4 lanes of a quad, 8 columns =
-// 8 tokens.  Lane (g, q) holds word column g and input rows 4q..4q+3 of a
-// 16-row step: four words give, after one byte permute per pair and mask, the
-// A fragments of four MMAs (p = 0..3), 64 outputs per warp.  The order of k
-// inside a step is free as long as A and B agree; 4q..4q+3 makes the B
-// fragment of a token one 64-bit shared load.
+// Layout.  m16n8k16: 16 rows = 8 word columns x 2 nibbles (p, p + 4), 8
+// columns = 8 tokens.  Lane (g, q) reads word column g of input rows 2q, 2q + 1,
+// 2q + 8, 2q + 9 of a 16-row step: four words give, after one byte permute per
+// pair, a mask and a subtraction, the A fragments of four MMAs (p = 0..3), 64
+// outputs per warp.  Words reach shared memory by TMA as boxes of 64 rows x 128
+// bytes with the 128-byte swizzle, under which the four rows a quad reads lie in
+// different banks.
 //
-// A block of 8 warps covers 256 outputs (4 warps) and either two K halves or
-// two token halves (2 warps); a stage of the cp.async ring is 2 pieces of 64
-// input rows x 128 bytes of words, the same rows of X, and the groups' steps
-// and zero words.  The words' 16-byte chunks are XOR-swizzled by the row so
-// that the four rows a quad reads fall in different banks.
+// Eight consumer warps, four to each of a stage's two boxes, and one producer
+// warp that issues every copy into a ring of stages; full and empty barriers let the warps
+// drift apart by the depth of the ring, and the producer runs ahead into the
+// next tile.  What the two boxes are is the mode's choice:
+//   kN    the same 64 input rows of two 256-output column blocks;
+//   kK    one column block, input rows 64 of two different 128-row halves: the
+//         warp halves' sums are added at the end;
+//   kTok  one column block, 128 consecutive input rows: every warp works
+//         through both boxes for its half of the tokens.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_fp16.h>
 #include <stdint.h>
 
@@ -35,162 +39,255 @@
 namespace awq {
 namespace w4s {
 
-constexpr int kThreads = 256;
-constexpr int kTileN = 256;                    // outputs per block
-constexpr int kPiece = 64;                     // input rows per piece
-constexpr uint32_t kPieceW = kPiece * 128;     // bytes of words of a piece
-constexpr uint32_t kSz = 640;                  // 256 steps (fp16) + 32 zero words
-constexpr uint32_t kXPitch = kPiece * 2 + 32;  // bytes between token rows of a piece
+constexpr int kConsumers = 256;
+constexpr int kThreads = kConsumers + 32;      // the producer is warp 8
+constexpr int kBoxN = 256;                     // outputs of a box
+constexpr int kBoxK = 64;                      // input rows of a box
+constexpr uint32_t kBoxBytes = kBoxK * 128;
+constexpr uint32_t kSz = 640;                  // a group's 256 steps (fp16) and 32 zero words
+constexpr uint32_t kXPitch = kBoxK * 2 + 16;   // bytes between token rows: conflict-free for ldmatrix
 
-__host__ __device__ constexpr uint32_t stage_bytes(int max_tok) {
-  return 2 * kPieceW + 2 * (uint32_t)max_tok * kXPitch + 4 * kSz;
+enum class Mode { kN, kK, kTok };
+
+__host__ __device__ constexpr uint32_t x_offset() { return 2 * kBoxBytes; }
+template <Mode M, int MAXTOK>
+__host__ __device__ constexpr uint32_t sz_offset() {
+  return x_offset() + (M == Mode::kN ? 1 : 2) * MAXTOK * kXPitch;
+}
+template <Mode M, int MAXTOK>
+__host__ __device__ constexpr uint32_t stage_bytes() {
+  return (sz_offset<M, MAXTOK>() + 4 * kSz + 1023) / 1024 * 1024;
 }
 
-__device__ __forceinline__ void cp16(uint32_t dst, const void *src, uint32_t n) {  // n = 0: zero-filled
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
-}
 __device__ __forceinline__ int group_shift(int group) { return group == 32 ? 5 : group == 64 ? 6 : 7; }
 
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+__device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool ok) {
+  const uint32_t n = ok ? 16u : 0u;  // 0: zero-filled, nothing is read
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+// One arrival on `bar` once this thread's cp.async copies so far have landed.
+__device__ __forceinline__ void cp_arrive(uint64_t *bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
+__device__ __forceinline__ void tma_load_2d_at(uint32_t dst, const CUtensorMap *map, uint64_t *bar, int x, int y) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y)
+      : "memory");
+}
+
+__device__ __forceinline__ void consumer_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+__device__ __forceinline__ int consumer_count(bool v) {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.popc.u32 %0, 1, 256, p;\n\t}"
+               : "=r"(r)
+               : "r"((uint32_t)v)
+               : "memory");
+  return (int)r;
 }
 
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                          uint32_t b0, uint32_t b1) {
-  asm(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ uint32_t lds32(const uint8_t *p) { return *reinterpret_cast<const uint32_t *>(p); }
-__device__ __forceinline__ uint2 lds64(const uint8_t *p) { return *reinterpret_cast<const uint2 *>(p); }
-__device__ __forceinline__ uint4 lds128(const uint8_t *p) { return *reinterpret_cast<const uint4 *>(p); }
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t a) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(a));
+}
 
-// One packed matrix [in, out]: two column bases in words (the tile's first and
-// second 128 outputs) and the first word past each half's columns.
+__device__ __forceinline__ uint32_t lds32(const uint8_t *p) { return *reinterpret_cast<const uint32_t *>(p); }
+
+__device__ __forceinline__ uint32_t sub2(uint32_t a, uint32_t b) {
+  const __half2 r = __hsub2(*reinterpret_cast<const __half2 *>(&a), *reinterpret_cast<const __half2 *>(&b));
+  return *reinterpret_cast<const uint32_t *>(&r);
+}
+
+// The barriers of a ring and whether a wait ran out.
+template <int STAGES>
+struct __align__(8) RingBars {
+  uint64_t full[STAGES], empty[STAGES];
+  int abort;
+};
+
+template <int STAGES>
+__device__ __forceinline__ void ring_init(RingBars<STAGES> *b) {  // one thread
+  for (int s = 0; s < STAGES; ++s) {
+    mbar_init(&b->full[s], 1 + 32);  // the words' byte count, the producer's lanes
+    mbar_init(&b->empty[s], kConsumers / 32);
+  }
+  b->abort = 0;
+  fence_mbar_init();
+}
+
+// Bounded wait, uniform over the warp; false when it ran out here or elsewhere
+// in the block (max_polls x 64 ns, as mbar_wait_long).
+template <int STAGES>
+__device__ __forceinline__ bool ring_wait(RingBars<STAGES> *b, uint64_t *bar, uint32_t parity, uint32_t max_polls,
+                                          DevStatus *st, uint32_t site) {
+  bool ok = mbar_try_wait(bar, parity);
+  if (__all_sync(0xffffffffu, ok)) return true;
+  if (!ok) ok = mbar_wait_long(bar, parity, max_polls, &b->abort);
+  if (__all_sync(0xffffffffu, ok)) return true;
+  if ((threadIdx.x & 31) == 0) {
+    if (!*reinterpret_cast<volatile int *>(&b->abort)) dev_fail(st, kDevTimeout, site);
+    *reinterpret_cast<volatile int *>(&b->abort) = 1;
+  }
+  return false;
+}
+
+// Where a warp role stands in the ring; both roles count the same stages.
+struct RingPos {
+  uint32_t slot = 0, phase = 0, count = 0;
+  template <int STAGES>
+  __device__ __forceinline__ void next() {
+    ++count;
+    if (++slot == STAGES) {
+      slot = 0;
+      phase ^= 1u;
+    }
+  }
+};
+
+// After a wait ran out: waits (bounded) for the producer's own copies in flight.
+template <int STAGES>
+__device__ __forceinline__ void ring_drain(RingBars<STAGES> *b, const RingPos &pos) {
+  for (uint32_t j = 1; j <= STAGES && j <= pos.count; ++j) {
+    const uint32_t i = pos.count - j;
+    (void)mbar_wait_bounded(&b->full[i % STAGES], (i / STAGES) & 1u, 1u << 20, nullptr);
+  }
+  asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
+// One packed matrix [.., in, out]: its words' tensor map with the first row, and
+// the first word column and the end of the columns of either box.
 struct Weights {
-  const int32_t *qweight, *qzeros;
+  const CUtensorMap *map;
+  int row0;  // row of the map that is input row 0
+  const int32_t *qzeros;
   const __half *scales;
   int64_t words;  // out / 8
-  int group_shift;  // log2 of the group size
-  int64_t col0, end0, col1, end1;
+  int shift;      // log2 of the group size
+  int col0, end0, col1, end1;
 };
 
-// Tokens of a product: row t is base + row(t) * ld.
-struct Rows {
-  const __half *base;
-  int64_t ld;
-  const int *index;  // shared memory, or NULL: row t itself
-  int n;
-};
-
-// How the block's second warp axis is used.
-enum class Split { kK, kTok };
-
-// First input row of piece p of stage s of a range that starts at k0.  With
-// the K split a super-chunk of 256 rows is two stages: warp half p takes rows
-// 128 p .. 128 p + 127 of it, 64 in each stage, so that a group of 128 stays
-// with one warp.
-template <Split SP>
-__device__ __forceinline__ int piece_row(int k0, int s, int p) {
-  return SP == Split::kK ? k0 + (s >> 1) * 256 + p * 128 + (s & 1) * 64 : k0 + s * 128 + p * 64;
+// First input row of box b of stage s of a range that starts at k0.  In mode
+// kK a super-chunk of 256 rows is two stages, so that a group of 128 stays
+// with one warp half.
+template <Mode M>
+__device__ __forceinline__ int box_row(int k0, int s, int b) {
+  return M == Mode::kN ? k0 + s * 64
+         : M == Mode::kK ? k0 + (s >> 1) * 256 + b * 128 + (s & 1) * 64
+                         : k0 + s * 128 + b * 64;
 }
-template <Split SP>
+template <Mode M>
 __device__ __forceinline__ int num_stages(int rows) {  // rows a multiple of 64
-  if (SP == Split::kTok) return (rows + 127) / 128;
+  if (M == Mode::kN) return rows / 64;
+  if (M == Mode::kTok) return (rows + 127) / 128;
   const int rem = rows % 256;
   return rows / 256 * 2 + (rem == 0 ? 0 : rem == 64 ? 1 : 2);
 }
 
-// This thread's copies of a stage, their addresses worked out once per product:
-// rows r and r + 32 of one 16-byte word chunk of both pieces, up to NX chunks
-// of X, and one chunk of the groups' steps or zero words.
-template <Split SP, int MAXTOK>
-struct Loader {
-  static constexpr int NX = (16 * MAXTOK + kThreads - 1) / kThreads;
-  const char *w;   // row r of the matrix
-  int64_t wrow;    // bytes of a row of words
-  uint32_t wdst, wn;
-  const char *x[NX];  // NULL: nothing to copy
-  const char *sz;     // group 0's chunk
-  int64_t szrow;
-  uint32_t szdst, szn;
-  int role, shift;  // role: -1, or piece * 2 + group of the piece
+// ---------------------------------------------------------------- producer
+// The words come by TMA, one instruction a box; token rows, steps and zero
+// words by the lanes' 16-byte cp.async: bulk copies of a token row's 128 bytes
+// held the copy engine up (16 rows: 1.3 us a stage).
+template <Mode M, int MAXTOK>
+struct Producer {
+  static constexpr int kX = (MAXTOK + 3) / 4;  // token rows of a lane
+  Weights w;
+  int n;
+  const char *x[kX];  // 16-byte chunk lane % 8 of rows lane / 8 + 4 j
 
-  __device__ __forceinline__ void init(const Weights &m, const Rows &rows) {
-    const int tid = threadIdx.x;
-    shift = m.group_shift;
-    {
-      const int r = tid >> 3, c = tid & 7;
-      const int64_t col = (c < 4 ? m.col0 : m.col1) + 4 * (c & 3);
-      const bool ok = col < (c < 4 ? m.end0 : m.end1);
-      wrow = m.words * 4;
-      w = reinterpret_cast<const char *>(m.qweight + (ok ? col : 0)) + r * wrow;
-      wdst = r * 128 + ((uint32_t)(c ^ (((r >> 2) & 3) << 1)) << 4);
-      wn = ok ? 16u : 0u;  // 0: the chunk is zero-filled, nothing is read
-    }
+  template <class RowOf>
+  __device__ __forceinline__ void rows(const __half *base, int64_t ld, int count, RowOf row) {
+    const int lane = threadIdx.x & 31;
+    n = count;
 #pragma unroll
-    for (int j = 0; j < NX; ++j) {
-      const int i = tid + j * kThreads, c = i & 7, pt = i >> 3, t = pt % MAXTOK;
-      x[j] = nullptr;
-      if (pt < 2 * MAXTOK && t < rows.n) {
-        const int64_t row = rows.index ? rows.index[t] : t;
-        x[j] = reinterpret_cast<const char *>(rows.base + row * rows.ld + c * 8);
-      }
+    for (int j = 0; j < kX; ++j) {
+      const int t = (lane >> 3) + 4 * j;
+      x[j] = reinterpret_cast<const char *>(base + (t < n ? (int64_t)row(t) * ld : 0) + (lane & 7) * 8);
     }
-    role = tid / 40;  // a piece has one group, two when g = 32
-    const int e = tid - role * 40;
-    if (role >= 4 || (shift != 5 && (role & 1))) {
-      role = -1;
-      return;
-    }
-    const int ch = e < 32 ? e >> 2 : e - 32;  // the 16-byte word chunk it belongs to
-    const int64_t col = (ch < 4 ? m.col0 : m.col1) + 4 * (ch & 3) + (e < 32 ? e & 3 : 0);
-    const bool ok = col < (ch < 4 ? m.end0 : m.end1);
-    szrow = e < 32 ? m.words * 16 : m.words * 4;
-    sz = e < 32 ? reinterpret_cast<const char *>(m.scales + (ok ? col : 0) * 8)
-                : reinterpret_cast<const char *>(m.qzeros + (ok ? col : 0));
-    szdst = 2 * kPieceW + 2 * MAXTOK * kXPitch + role * kSz + (e < 32 ? e * 16 : 512 + (e - 32) * 16);
-    szn = ok ? 16u : 0u;
   }
 
-  // Copies of stage s of the range [k0, k1) into shared memory at `st` (not
-  // committed).  A piece outside the range is skipped: nobody reads it.
-  __device__ __forceinline__ void issue(uint32_t st, int k0, int k1, int s) const {
-    const int tid = threadIdx.x;
-    const int kb0 = piece_row<SP>(k0, s, 0), kb1 = piece_row<SP>(k0, s, 1);
+  // Words, steps and zero words of stage s (and the stage's byte count).
+  __device__ __forceinline__ void issue_words(uint32_t st, uint64_t *bar, int k0, int k1, int s) const {
+    const int lane = threadIdx.x & 31;
+    const int kb[2] = {box_row<M>(k0, s, 0), box_row<M>(k0, s, 1)};
+    const bool ok[2] = {kb[0] < k1, kb[1] < k1 && w.col1 < w.end1};
+    if (lane == 0) mbar_arrive_expect_tx(bar, (ok[0] ? kBoxBytes : 0u) + (ok[1] ? kBoxBytes : 0u));
+    __syncwarp();
+    if (lane == 0 && ok[0]) tma_load_2d_at(st, w.map, bar, w.col0 * 2, w.row0 + kb[0]);
+    if (lane == 1 && ok[1]) tma_load_2d_at(st + kBoxBytes, w.map, bar, w.col1 * 2, w.row0 + kb[1]);
 #pragma unroll
-    for (int p = 0; p < 2; ++p) {
-      const int kb = p ? kb1 : kb0;
-      if (kb >= k1) continue;
-      const char *src = w + (int64_t)kb * wrow;
-      cp16(st + p * kPieceW + wdst, src, wn);
-      cp16(st + p * kPieceW + wdst + 32 * 128, src + 32 * wrow, wn);  // row r + 32: the same swizzle
+    for (int b = 0; b < 2; ++b) {
+      if (!ok[b] || (w.shift == 7 && (kb[b] & 64))) continue;  // a group of 128: with its first box
+      const int col = b ? w.col1 : w.col0, end = b ? w.end1 : w.end0;
+      for (int gi = 0; gi < (w.shift == 5 ? 2 : 1); ++gi) {
+        const int64_t first = (int64_t)((kb[b] + 32 * gi) >> w.shift) * w.words;
+        const uint32_t d = st + sz_offset<M, MAXTOK>() + (b * 2 + gi) * kSz;
+        const bool in = col + lane < end;  // a word column's 8 steps
+        cp16(d + lane * 16, w.scales + (first + (in ? col + lane : 0)) * 8, in);
+        if (lane < 8) {
+          const bool zin = col + 4 * lane < end;
+          cp16(d + 512 + lane * 16, w.qzeros + first + (zin ? col + 4 * lane : 0), zin);
+        }
+      }
     }
+  }
+
+  // Token rows of stage s, and the lanes' arrivals.
+  __device__ __forceinline__ void issue_rows(uint32_t st, uint64_t *bar, int k0, int k1, int s) const {
+    const int lane = threadIdx.x & 31;
+    const uint32_t d = st + x_offset() + (lane >> 3) * kXPitch + (lane & 7) * 16;
+    const int kb0 = box_row<M>(k0, s, 0), kb1 = box_row<M>(k0, s, 1);
 #pragma unroll
-    for (int j = 0; j < NX; ++j) {
-      const int i = tid + j * kThreads, pt = i >> 3;
-      const int kb = pt < MAXTOK ? kb0 : kb1;
-      if (x[j] && kb < k1) cp16(st + 2 * kPieceW + pt * kXPitch + (i & 7) * 16, x[j] + 2 * kb, 16u);
+    for (int j = 0; j < kX; ++j) {
+      if ((lane >> 3) + 4 * j >= n) break;
+      cp16(d + 4 * j * kXPitch, x[j] + 2 * kb0, true);
+      if (M != Mode::kN && kb1 < k1) cp16(d + (MAXTOK + 4 * j) * kXPitch, x[j] + 2 * kb1, true);
     }
-    if (role >= 0) {
-      const int kb = (role & 2) ? kb1 : kb0;
-      // a group of 128 is closed by its second piece, which alone brings it
-      if (kb < k1 && (shift != 7 || (kb & 64)))
-        cp16(st + szdst, sz + (int64_t)((kb + 32 * (role & 1)) >> shift) * szrow, szn);
+    cp_arrive(bar);
+  }
+
+  // Rows [k0, k1).  skip: stages whose words were issued ahead.  A wait that
+  // runs out ends the ring's work on both sides (ring_wait); what follows then
+  // computes on what there is, and the status says so.
+  template <int STAGES>
+  __device__ __forceinline__ void run(RingPos &pos, uint32_t ring, RingBars<STAGES> *bars, int k0, int k1,
+                                      uint32_t max_polls, DevStatus *st, int skip = 0) const {
+    const int ns = num_stages<M>(k1 - k0);
+    for (int s = 0; s < ns; ++s) {
+      const uint32_t at = ring + pos.slot * stage_bytes<M, MAXTOK>();
+      if (s >= skip) {
+        if (!ring_wait(bars, &bars->empty[pos.slot], pos.phase ^ 1u, max_polls, st, 0xE20u)) return;
+        issue_words(at, &bars->full[pos.slot], k0, k1, s);
+      }
+      issue_rows(at, &bars->full[pos.slot], k0, k1, s);
+      pos.next<STAGES>();
     }
   }
 };
 
-// Accumulators of one warp: 64 outputs x 8 NT tokens.
+// ---------------------------------------------------------------- consumers
+// Accumulators of one warp: 64 outputs x 8 NT tokens.  A group's zero points are
+// either subtracted from the codes (16 packed subtractions a step) or, for one
+// token tile, taken off at the group's end with sum_k x, which one more MMA a step
+// gives: 219 against 255 cycles a step with 16 warps on an SM.
 template <int NT>
 struct Acc {
-  float out[4][NT][4];  // scaled totals: [p][token tile][c]
-  float grp[4][NT][4];  // this group's sum of q x 2^-24 (p even), 2^-20 (p odd)
-  float sx[NT][4];      // this group's sum of x 2^-24
+  static constexpr bool kSumX = NT == 1;
+  float out[4][NT][4];  // totals: [p][token tile][c], 2^-24 (p even) or 2^-20 (p odd) of the sum
+  float grp[4][NT][4];  // this group's sum, in the same units
+  float sx[4];          // this group's sum of x 2^-24
+  uint32_t zp[8];       // the group's zero points as subnormal pairs
+  uint32_t zw;          // the group's zero word
+  uint4 sc;             // the group's steps (8 fp16)
 };
 
 template <int NT>
@@ -202,57 +299,91 @@ __device__ __forceinline__ void acc_zero(Acc<NT> &a) {
 #pragma unroll
       for (int c = 0; c < 4; ++c) a.out[p][n][c] = a.grp[p][n][c] = 0.0f;
 #pragma unroll
-  for (int n = 0; n < NT; ++n)
-#pragma unroll
-    for (int c = 0; c < 4; ++c) a.sx[n][c] = 0.0f;
+  for (int c = 0; c < 4; ++c) a.sx[c] = 0.0f;
 }
 
-// Closes a group: out += s (sum q x - z sum x), then clears the group's sums.
 template <int NT>
-__device__ __forceinline__ void flush_group(Acc<NT> &a, const uint8_t *sz, int wcol) {
-  const uint4 sv = lds128(sz + wcol * 16);
-  const uint32_t zw = lds32(sz + 512 + wcol * 4);
-  const uint32_t sh[4] = {sv.x, sv.y, sv.z, sv.w};
+__device__ __forceinline__ void open_group(Acc<NT> &a, const uint8_t *sz, int wcol) {
+  a.sc = *reinterpret_cast<const uint4 *>(sz + wcol * 16);
+  a.zw = lds32(sz + 512 + wcol * 4);
+  if (Acc<NT>::kSumX) return;
+  uint32_t lo = __byte_perm(a.zw, a.zw, 0x1010), hi = __byte_perm(a.zw, a.zw, 0x3232);
 #pragma unroll
   for (int p = 0; p < 4; ++p) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {  // output p (rows g), output p + 4 (rows g + 8)
-      const int o = p + 4 * h;
-      const __half2 s2 = *reinterpret_cast<const __half2 *>(&sh[o >> 1]);
-      const float s = __half2float((o & 1) ? __high2half(s2) : __low2half(s2));
-      const float sq = s * ((p & 1) ? 1048576.0f : 16777216.0f);                         // 2^20 or 2^24
-      const float szx = -s * 16777216.0f * (float)((zw >> (4 * o)) & 15u);
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int c = 2 * h + e;
-          a.out[p][n][c] = fmaf(sq, a.grp[p][n][c], fmaf(szx, a.sx[n][e], a.out[p][n][c]));
-          a.grp[p][n][c] = 0.0f;
-        }
+    const uint32_t m = (p & 1) ? 0x00F000F0u : 0x000F000Fu;
+    if (p == 2) {
+      lo >>= 8;
+      hi >>= 8;
     }
+    a.zp[p] = lo & m;
+    a.zp[p + 4] = hi & m;
   }
-#pragma unroll
-  for (int n = 0; n < NT; ++n)
-#pragma unroll
-    for (int c = 0; c < 4; ++c) a.sx[n][c] = 0.0f;
 }
 
-// One 64-row piece: four 16-row steps.  `wb` / `xb`: this lane's word and X
-// addresses in the piece.
+// Closes a group: out += s (sum (q - z) x), then clears the group's sums.
 template <int NT>
-__device__ __forceinline__ void piece(Acc<NT> &a, const uint8_t *wb, const uint8_t *xb, const uint8_t *sz,
-                                      int wcol, int shift, bool close128) {
+__device__ __forceinline__ void close_group(Acc<NT> &a) {
+  const uint32_t sh[4] = {a.sc.x, a.sc.y, a.sc.z, a.sc.w};
+#pragma unroll
+  for (int o = 0; o < 8; ++o) {
+    const __half2 s2 = *reinterpret_cast<const __half2 *>(&sh[o >> 1]);
+    const float s = __half2float((o & 1) ? __high2half(s2) : __low2half(s2));
+    const int p = o & 3, h = o >> 2;
+    float nz = 0.0f;  // -z (p even), -16 z (p odd), from the low bits of 2^23 + z
+    if (Acc<NT>::kSumX) {
+      const uint32_t z = (p & 1) ? (a.zw >> (4 * o - 4)) & 0xF0u : (a.zw >> (4 * o)) & 0xFu;
+      nz = 8388608.0f - __uint_as_float(0x4B000000u | z);
+    }
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int c = 2 * h; c < 2 * h + 2; ++c) {
+        const float sum = Acc<NT>::kSumX ? fmaf(nz, a.sx[c & 1], a.grp[p][n][c]) : a.grp[p][n][c];
+        a.out[p][n][c] = fmaf(s, sum, a.out[p][n][c]);
+        a.grp[p][n][c] = 0.0f;
+      }
+  }
+#pragma unroll
+  for (int c = 0; c < 4; ++c) a.sx[c] = 0.0f;
+}
+
+// One box: four 16-row steps, each step's words and token fragments loaded one
+// step ahead.  w0 / w1: this lane's word addresses of rows 2q and 2q + 1; xa:
+// this lane's ldmatrix address.
+template <int NT>
+__device__ __forceinline__ void box(Acc<NT> &a, const uint8_t *w0, const uint8_t *w1, uint32_t xa, const uint8_t *sz,
+                                    int wcol, int shift, bool upper) {
+  if (!(shift == 7 && upper)) open_group<NT>(a, sz, wcol);
+  constexpr int NB = (NT + 1) / 2;
+  uint32_t w[2][4], b[2][NB][4];
+  auto load_w = [&](uint32_t(&d)[4], int ks) {
+    d[0] = lds32(w0 + ks * 2048);
+    d[1] = lds32(w1 + ks * 2048);
+    d[2] = lds32(w0 + ks * 2048 + 1024);
+    d[3] = lds32(w1 + ks * 2048 + 1024);
+  };
+  auto load_x = [&](uint32_t(&d)[NB][4], int ks) {
+    if (NT == 1) {  // both steps of a half at once
+      ldsm4(d[0], xa + (ks >> 1) * 64);
+    } else {
+#pragma unroll
+      for (int n = 0; n < NB; ++n) ldsm4(d[n], xa + n * 16 * kXPitch + ks * 32);
+    }
+  };
+  load_w(w[0], 0);
+  load_x(b[0], 0);
 #pragma unroll
   for (int ks = 0; ks < 4; ++ks) {
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = lds32(wb + (ks * 16 + i) * 128);
-    uint2 b[NT];
-#pragma unroll
-    for (int n = 0; n < NT; ++n) b[n] = lds64(xb + n * 8 * kXPitch + ks * 32);
-    uint32_t v[4] = {__byte_perm(w[0], w[1], 0x5410), __byte_perm(w[0], w[1], 0x7632),
-                     __byte_perm(w[2], w[3], 0x5410), __byte_perm(w[2], w[3], 0x7632)};
+    if (ks < 3) {
+      load_w(w[(ks + 1) & 1], ks + 1);
+      if (NT > 1)
+        load_x(b[(ks + 1) & 1], ks + 1);
+      else if (ks == 1)
+        load_x(b[1], 2);
+    }
+    const uint32_t(&c)[4] = w[ks & 1];
+    uint32_t v[4] = {__byte_perm(c[0], c[1], 0x5410), __byte_perm(c[0], c[1], 0x7632),
+                     __byte_perm(c[2], c[3], 0x5410), __byte_perm(c[2], c[3], 0x7632)};
 #pragma unroll
     for (int p = 0; p < 4; ++p) {
       const uint32_t m = (p & 1) ? 0x00F000F0u : 0x000F000Fu;
@@ -260,70 +391,90 @@ __device__ __forceinline__ void piece(Acc<NT> &a, const uint8_t *wb, const uint8
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[i] >>= 8;
       }
+      uint32_t a0 = v[0] & m, a1 = v[1] & m, a2 = v[2] & m, a3 = v[3] & m;
+      if (!Acc<NT>::kSumX) {
+        a0 = sub2(a0, a.zp[p]);
+        a1 = sub2(a1, a.zp[p + 4]);
+        a2 = sub2(a2, a.zp[p]);
+        a3 = sub2(a3, a.zp[p + 4]);
+      }
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
-        mma16816(a.grp[p][n], v[0] & m, v[1] & m, v[2] & m, v[3] & m, b[n].x, b[n].y);
+      for (int n = 0; n < NT; ++n) {
+        const uint32_t b0 = NT == 1 ? b[ks >> 1][0][2 * (ks & 1)] : b[ks & 1][n / 2][2 * (n & 1)];
+        const uint32_t b1 = NT == 1 ? b[ks >> 1][0][2 * (ks & 1) + 1] : b[ks & 1][n / 2][2 * (n & 1) + 1];
+        mma16816(a.grp[p][n], a0, a1, a2, a3, b0, b1);
+        if (Acc<NT>::kSumX && p == 3)
+          mma16816(a.sx, 0x00010001u, 0x00010001u, 0x00010001u, 0x00010001u, b0, b1);
+      }
     }
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-      mma16816(a.sx[n], 0x00010001u, 0x00010001u, 0x00010001u, 0x00010001u, b[n].x, b[n].y);
-    if (shift == 5 && (ks & 1)) flush_group<NT>(a, sz + (ks >> 1) * kSz, wcol);
+    if (ks == 1 && shift == 5) {
+      close_group<NT>(a);
+      open_group<NT>(a, sz + kSz, wcol);
+    }
   }
-  if (shift == 6 || (shift == 7 && close128)) flush_group<NT>(a, sz, wcol);
+  if (shift != 7 || upper) close_group<NT>(a);
 }
 
-// The product of the block over rows [k0, k1) of its tile (k0 and k1
-// multiples of 64; of 128 when g = 128).  Uses the ring at `ring` (STAGES x
-// stage_bytes(MAXTOK)), which is free again on return for every thread.
-template <int NT, Split SP, int MAXTOK, int STAGES>
-__device__ __forceinline__ void product(Acc<NT> &a, uint8_t *ring, const Weights &w, const Rows &x, int k0,
-                                        int k1) {
-  constexpr uint32_t kStage = stage_bytes(MAXTOK);
-  const uint32_t ring_u = smem_u32(ring);
+// The consumers' side of a product over rows [k0, k1) (multiples of 64; of 128
+// when g = 128).
+template <Mode M, int NT, int MAXTOK, int STAGES>
+__device__ __forceinline__ void consume(Acc<NT> &a, RingPos &pos, uint8_t *ring, RingBars<STAGES> *bars, int shift,
+                                        int k0, int k1, bool box1, uint32_t max_polls, DevStatus *st) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int nw = warp & 3, half = warp >> 2, g = lane >> 2, q = lane & 3;
-  const int wcol = nw * 8 + g;
-  const int ns = num_stages<SP>(k1 - k0);
-  Loader<SP, MAXTOK> ld;
-  ld.init(w, x);
-#pragma unroll
-  for (int s = 0; s < STAGES - 1; ++s) {
-    if (s < ns) ld.issue(ring_u + s * kStage, k0, k1, s);
-    cp_commit();
-  }
+  const int wcol = nw * 8 + g, chunk = wcol >> 2;
+  const uint32_t o0 = (2 * q) * 128 + ((uint32_t)(chunk ^ (2 * q)) << 4) + (wcol & 3) * 4;
+  const uint32_t o1 = (2 * q + 1) * 128 + ((uint32_t)(chunk ^ (2 * q + 1)) << 4) + (wcol & 3) * 4;
+  // ldmatrix: for one token tile the four 8-column blocks of 32 input rows, else
+  // (token tile, 8-column block) pairs of 16 input rows
+  const uint32_t xl = NT == 1 ? (lane & 7) * kXPitch + (lane >> 3) * 16
+                              : ((lane >> 4) * 8 + (lane & 7)) * kXPitch + ((lane >> 3) & 1) * 16;
+  const uint32_t xt = M == Mode::kTok ? half * NT * 8 * kXPitch : 0;
+  const int ns = num_stages<M>(k1 - k0);
   acc_zero<NT>(a);
-  const uint32_t wlane = (uint32_t)(4 * q) * 128 + ((uint32_t)((wcol >> 2) ^ (q << 1)) << 4) + (wcol & 3) * 4;
-  const uint32_t xlane = (uint32_t)g * kXPitch + q * 8 + (SP == Split::kTok ? half * NT * 8 * kXPitch : 0);
-  uint32_t slot = 0, next = (STAGES - 1) * kStage;
+#pragma unroll 1
   for (int s = 0; s < ns; ++s) {
-    cp_wait<STAGES - 2>();
-    __syncthreads();  // stage s has landed for all, and the slot of s - 1 is free
-    if (s + STAGES - 1 < ns) ld.issue(ring_u + next, k0, k1, s + STAGES - 1);
-    cp_commit();
-    const uint8_t *st = ring + slot;
-#pragma unroll
-    for (int p = 0; p < 2; ++p) {
-      if (SP == Split::kK && p != half) continue;
-      const int kb = piece_row<SP>(k0, s, p);
-      if (kb < k1)
-        piece<NT>(a, st + p * kPieceW + wlane, st + 2 * kPieceW + p * MAXTOK * kXPitch + xlane,
-                  st + 2 * kPieceW + 2 * MAXTOK * kXPitch + p * 2 * kSz, wcol, w.group_shift, (kb & 64) != 0);
+    if (!ring_wait(bars, &bars->full[pos.slot], pos.phase, max_polls, st, 0xE21u)) break;
+    const uint8_t *sp = ring + pos.slot * stage_bytes<M, MAXTOK>();
+#pragma unroll 1
+    for (int i = 0; i < (M == Mode::kTok ? 2 : 1); ++i) {
+      const int b = M == Mode::kTok ? i : half;
+      const int kb = box_row<M>(k0, s, b);
+      if (kb < k1 && (M != Mode::kN || b == 0 || box1)) {
+        const int xb = M == Mode::kN ? 0 : b;
+        box<NT>(a, sp + b * kBoxBytes + o0, sp + b * kBoxBytes + o1,
+                smem_u32(sp) + x_offset() + xb * MAXTOK * kXPitch + xl + xt,
+                sp + sz_offset<M, MAXTOK>() + b * 2 * kSz, wcol, shift, (kb & 64) != 0);
+      }
     }
-    next = slot;
-    slot = slot + kStage == STAGES * kStage ? 0 : slot + kStage;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bars->empty[pos.slot]);
+    pos.next<STAGES>();
   }
-  cp_wait<0>();
-  __syncthreads();
+#pragma unroll
+  for (int p = 0; p < 4; ++p)
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) a.out[p][n][c] *= (p & 1) ? 1048576.0f : 16777216.0f;
 }
 
-// The block's sums into shared memory, red[token][kRedPitch]: output o of the
-// tile at column o.  Every thread may read them on return.
-constexpr int kRedPitch = 257;
-template <int NT, Split SP>
+// A lane's 8 consecutive outputs of token column 8 n + 2 q + e.
+template <int NT>
+__device__ __forceinline__ void outputs8(const Acc<NT> &a, int n, int e, float (&v)[8]) {
+#pragma unroll
+  for (int o = 0; o < 8; ++o) v[o] = a.out[o & 3][n][e + 2 * (o >> 2)];
+}
+
+// The block's sums of a 256-output tile into shared memory, red[token][kRedPitch];
+// the consumers may read them after the barrier at the end.
+constexpr int kRedPitch = kBoxN + 1;
+template <Mode M, int NT>
 __device__ __forceinline__ void store_sums(const Acc<NT> &a, float *red) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int nw = warp & 3, half = warp >> 2, g = lane >> 2, q = lane & 3;
-  const int t0 = SP == Split::kTok ? half * NT * 8 : 0;
+  const int t0 = M == Mode::kTok ? half * NT * 8 : 0;
+  float *d0 = red + (t0 + 2 * q) * kRedPitch + (nw * 8 + g) * 8;
   auto each = [&](bool add) {
 #pragma unroll
     for (int p = 0; p < 4; ++p)
@@ -331,18 +482,18 @@ __device__ __forceinline__ void store_sums(const Acc<NT> &a, float *red) {
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          float *d = red + (t0 + n * 8 + 2 * q + (c & 1)) * kRedPitch + (nw * 8 + g) * 8 + p + 4 * (c >> 1);
+          float *d = d0 + (n * 8 + (c & 1)) * kRedPitch + p + 4 * (c >> 1);
           *d = add ? *d + a.out[p][n][c] : a.out[p][n][c];
         }
   };
-  if (SP == Split::kTok) {
+  if (M != Mode::kK) {
     each(false);
   } else {  // the two K halves, in a fixed order
     if (half == 0) each(false);
-    __syncthreads();
+    consumer_sync();
     if (half == 1) each(true);
   }
-  __syncthreads();
+  consumer_sync();
 }
 
 }  // namespace w4s
