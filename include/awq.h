@@ -379,11 +379,13 @@ size_t awq_w4a16_workspace_size(int64_t T, int64_t in, int64_t out, const awq_co
  *            an error found on the device: the row is computed without an
  *            adapter and the status word of ws records AWQ_ERR_INVALID_ARG
  *   ws       awq_w4a16_lora_workspace_size() bytes
- * Up to 64 tokens the weights stay (q - z) scale exactly; beyond, they are
- * rounded to fp16 once, as in awq_w4a16_gemm, and U to fp16.
+ * Up to 64 tokens the packed words are streamed and the weights stay
+ * (q - z) scale exactly; beyond, they are rounded to fp16 once, as in
+ * awq_w4a16_gemm, and c_a U to fp16 (past fp16's range it is infinite), for one
+ * product on the tensor cores.
  * Requires in % 64 == 0, out % 32 == 0, rank % 8 == 0 and 8 <= rank <= 256,
- * 1 <= n_adapters <= 65536; X, A, B and Y 16-byte aligned, c and adapter
- * 4-byte aligned. */
+ * 1 <= n_adapters <= 65536, n_adapters * out < 2^31; X, A, B and Y 16-byte
+ * aligned, c and adapter 4-byte aligned. */
 awq_status awq_w4a16_lora_gemm(const void *X, int64_t T, int64_t in, int64_t ldx,
                                const int32_t *qweight, const int32_t *qzeros, const void *scales,
                                int64_t out, const awq_config *cfg, const void *A, const void *B,

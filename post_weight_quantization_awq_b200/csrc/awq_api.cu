@@ -854,9 +854,10 @@ size_t awq_w4a16_workspace_size(int64_t T, int64_t in, int64_t out, const awq_co
   return splits > 1 ? w4a16_ws_bytes(T, out, splits) : kHeader;
 }
 
-// status word plus U of the adapter product
-static size_t lora_ws_bytes(int64_t T, int32_t rank) {
-  return kHeader + align256(sizeof(float) * (size_t)T * (size_t)rank);
+// status word plus U of the adapter product, or what its form for many tokens keeps
+static size_t lora_ws_bytes(int64_t T, int64_t in, int64_t out, int32_t rank) {
+  return kHeader + (T <= kLoraStreamT ? align256(sizeof(float) * (size_t)T * (size_t)rank)
+                                      : lora_prefill_ws(T, in, out, rank));
 }
 
 static awq_status check_lora_shape(int64_t T, int64_t in, int64_t out, int32_t rank, const awq_config *cfg) {
@@ -881,7 +882,7 @@ size_t awq_w4a16_lora_workspace_size(int64_t T, int64_t in, int64_t out, int32_t
     return 0;
   }
   if (check_lora_shape(T, in, out, rank, cfg) != AWQ_OK) return 0;
-  return lora_ws_bytes(T, rank);
+  return lora_ws_bytes(T, in, out, rank);
 }
 
 awq_status awq_w4a16_lora_gemm(const void *X, int64_t T, int64_t in, int64_t ldx,
@@ -899,6 +900,9 @@ awq_status awq_w4a16_lora_gemm(const void *X, int64_t T, int64_t in, int64_t ldx
     return fail(AWQ_ERR_INVALID_ARG, "qweight, qzeros and scales must be non-NULL and 16-byte aligned");
   if (n_adapters < 1 || n_adapters > 65536)
     return fail(AWQ_ERR_INVALID_ARG, "n_adapters=%d (1..65536)", n_adapters);
+  if ((int64_t)n_adapters * out >= (int64_t(1) << 31))
+    return fail(AWQ_ERR_UNSUPPORTED, "n_adapters=%d x out=%lld: fewer than 2^31 rows of B supported", n_adapters,
+                (long long)out);
   if (!A || !B || !aligned(A, 16) || !aligned(B, 16))
     return fail(AWQ_ERR_INVALID_ARG, "A and B must be non-NULL and 16-byte aligned");
   if (!c || !adapter || !aligned(c, 4) || !aligned(adapter, 4))
@@ -906,7 +910,7 @@ awq_status awq_w4a16_lora_gemm(const void *X, int64_t T, int64_t in, int64_t ldx
   if (!Y || !aligned(Y, 16)) return fail(AWQ_ERR_INVALID_ARG, "Y is NULL or not 16-byte aligned");
   if (ldy < out || ldy % 8 != 0)
     return fail(AWQ_ERR_INVALID_ARG, "ldy=%lld must be >= out and a multiple of 8", (long long)ldy);
-  if ((st = check_ws(ws, ws_bytes, lora_ws_bytes(T, rank))) != AWQ_OK) return st;
+  if ((st = check_ws(ws, ws_bytes, lora_ws_bytes(T, in, out, rank))) != AWQ_OK) return st;
   AWQ_LAUNCH_GATE();
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
   LoraArgs a = {static_cast<const __half *>(X), T, in, ldx, qweight, qzeros, static_cast<const __half *>(scales),
@@ -914,7 +918,8 @@ awq_status awq_w4a16_lora_gemm(const void *X, int64_t T, int64_t in, int64_t ldx
                 rank, n_adapters, static_cast<__half *>(Y), ldy,
                 reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + kHeader), static_cast<DevStatus *>(ws), poll_cap()};
   ProfScope p("w4a16_lora", cs);
-  AWQ_TRY_CUDA(launch_lora(a, num_sms_current(), cs), "w4a16_lora launch");
+  AWQ_TRY_CUDA(T <= kLoraStreamT ? launch_lora(a, num_sms_current(), cs) : launch_lora_prefill(a, num_sms_current(), cs),
+               "w4a16_lora launch");
   return AWQ_OK;
 }
 

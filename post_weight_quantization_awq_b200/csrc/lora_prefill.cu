@@ -1,0 +1,483 @@
+// The adapter product for many tokens (more than 64), on the 5th-generation
+// tensor cores:
+//
+//   Y = X Wd^T + sum over the tile's adapters a of mask_a(U) B_a^T,
+//   Wd = RN16((q - z) scale),  U[t] = RN16( c_a (x_t A_a^T) ),  a = ids[t]
+//
+// Two launches.  lora_prepare_kernel: some blocks dequantise W once (in x out
+// work instead of once per token tile), the others compute U and, for every
+// token tile of the product, the list of the adapters its rows carry.
+// lora_gemm_kernel: the low-rank part is K steps like any other, appended to a
+// tile's K loop for each adapter on its list: A is U's rows, of which the
+// waiting epilogue warps zero those of other adapters in shared memory, B is
+// B_a's rows by TMA.  No partial result leaves the accumulators, so the whole is
+// rounded once, and the part costs rank / in of the product for rows that stand
+// together by adapter.
+#include <cuda.h>
+
+#include "awq_launch.h"
+#include "serve_launch.h"
+#include "w4_dequant.cuh"
+
+namespace awq {
+namespace {
+
+// ---------------------------------------------------------------------------
+// Preparation
+// ---------------------------------------------------------------------------
+constexpr int kShT = 32;   // tokens of a shrink block
+constexpr int kShR = 32;   // rank rows of a pass
+constexpr int kShWarps = 8;
+
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// The different adapters of n ids (shared memory), in order of appearance, into
+// list; returns how many.  All 256 threads.
+__device__ int adapter_list(const int *ids, int n, int *list, int *scratch) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int id = tid < n ? ids[tid] : -1;
+  bool first = id >= 0;
+  for (int s = 0; s < tid && first; ++s) first = ids[s] != id;
+  const uint32_t b = __ballot_sync(0xffffffffu, first);
+  if (lane == 0) scratch[warp] = __popc(b);
+  __syncthreads();
+  int at = 0, total = 0;
+  for (int w = 0; w < 8; ++w) {
+    at += w < warp ? scratch[w] : 0;
+    total += scratch[w];
+  }
+  if (first) list[at + __popc(b & ((1u << lane) - 1u))] = id;
+  __syncthreads();
+  return total;
+}
+
+// U of 32 tokens: for each adapter among them, X (32 rows) times A_a^T on
+// mma.sync, the 8 warps taking eighths of K.  A lane loads 16 bytes of a row: the
+// 8 columns 8q .. 8q + 7 of a 32-column step are its fragments of two MMAs, the
+// order of k inside a step being free as long as both operands agree.
+__device__ void shrink_block(const LoraArgs &a, int64_t t0, uint8_t *smem) {
+  float *red = reinterpret_cast<float *>(smem);                          // [8][32][kShR + 1]
+  int *ids = reinterpret_cast<int *>(smem + kShWarps * kShT * (kShR + 1) * 4);  // [32], list [32], scratch [8]
+  int *list = ids + 256, *scratch = list + 256;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, q = lane & 3;
+  const int n = (int)i64min(kShT, a.T - t0);
+  if (tid < 256) {
+    const int id = tid < n ? a.ids[t0 + tid] : -1;
+    ids[tid] = id >= 0 && id < a.adapters ? id : -1;
+    if (id < -1 || id >= a.adapters) dev_fail(a.st, kDevBadAdapter, 0xE02u);
+  }
+  __syncthreads();
+  const int count = adapter_list(ids, n, list, scratch);
+  const int steps = (int)(a.in / 32), s0 = steps * warp / kShWarps, s1 = steps * (warp + 1) / kShWarps;
+  const __half *xr[4];  // rows g, g + 8, g + 16, g + 24 (the last one again past the end)
+#pragma unroll
+  for (int i = 0; i < 4; ++i) xr[i] = a.X + (t0 + min(g + 8 * i, n - 1)) * a.ldx + 8 * q;
+  for (int j = 0; j < count; ++j) {
+    const int id = list[j];
+    for (int r0 = 0; r0 < a.rank; r0 += kShR) {
+      float acc[2][4][4];
+#pragma unroll
+      for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) acc[m][x][c] = 0.0f;
+      const __half *ar = a.A + ((int64_t)id * a.rank + r0 + g) * a.in + 8 * q;
+#pragma unroll 4
+      for (int s = s0; s < s1; ++s) {
+        uint4 xv[4], av[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) xv[i] = __ldg(reinterpret_cast<const uint4 *>(xr[i] + 32 * s));
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+          av[x] = r0 + 8 * x < a.rank ? __ldg(reinterpret_cast<const uint4 *>(ar + (int64_t)8 * x * a.in + 32 * s))
+                                      : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            mma16816(acc[m][x], xv[2 * m].x, xv[2 * m + 1].x, xv[2 * m].y, xv[2 * m + 1].y, av[x].x, av[x].y);
+            mma16816(acc[m][x], xv[2 * m].z, xv[2 * m + 1].z, xv[2 * m].w, xv[2 * m + 1].w, av[x].z, av[x].w);
+          }
+      }
+#pragma unroll
+      for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            red[(warp * kShT + 16 * m + g + 8 * (c >> 1)) * (kShR + 1) + 8 * x + 2 * q + (c & 1)] = acc[m][x][c];
+      __syncthreads();
+      for (int i = tid; i < kShT * kShR; i += 256) {
+        const int t = i / kShR, r = i % kShR;
+        if (t < n && ids[t] == id && r0 + r < a.rank) {
+          float v = 0.0f;
+#pragma unroll
+          for (int w = 0; w < kShWarps; ++w) v += red[(w * kShT + t) * (kShR + 1) + r];
+          reinterpret_cast<__half *>(a.U)[(t0 + t) * a.rank + r0 + r] = __float2half_rn(a.c[id] * v);
+        }
+      }
+      __syncthreads();
+    }
+  }
+}
+
+constexpr int kPrepSmem = kShWarps * kShT * (kShR + 1) * 4 + (256 + 256 + 16) * 4;
+
+// Blocks [0, n_shrink): U; [n_shrink, n_shrink + n_lists): the lists of `bm`-row
+// tiles, lists[tile][bm + 1] = count, ids; the rest: one dequantised tile each.
+__global__ void __launch_bounds__(256) lora_prepare_kernel(const LoraArgs a, int n_shrink, int n_lists, int bm,
+                                                           int *lists, __half *Wd) {
+  __shared__ __align__(16) uint8_t smem[kPrepSmem];
+  int64_t b = blockIdx.x;
+  if (b < n_shrink) {
+    shrink_block(a, b * kShT, smem);
+    return;
+  }
+  b -= n_shrink;
+  if (b < n_lists) {
+    int *ids = reinterpret_cast<int *>(smem), *list = ids + 256, *scratch = list + 256;
+    const int64_t t0 = b * bm;
+    const int n = (int)i64min(bm, a.T - t0), tid = threadIdx.x;
+    const int id = tid < n ? a.ids[t0 + tid] : -1;
+    ids[tid] = id >= 0 && id < a.adapters ? id : -1;
+    __syncthreads();
+    const int count = adapter_list(ids, n, list, scratch);
+    int *dst = lists + b * (bm + 1);
+    if (tid == 0) dst[0] = count;
+    if (tid < count) dst[1 + tid] = list[tid];
+    return;
+  }
+  b -= n_lists;
+  const int64_t tiles_o = (a.out + kDeqOut - 1) / kDeqOut;
+  dequant_tile(reinterpret_cast<__half *>(smem), a.qweight, a.qzeros, a.scales, a.in, a.out, a.group,
+               b % tiles_o * kDeqOut, b / tiles_o * kDeqIn, Wd);
+}
+static_assert(kPrepSmem >= kDeqIn * kDeqOut * 2, "dequantised tile");
+
+// ---------------------------------------------------------------------------
+// Product.  One block per SM, persistent over BM x BN tiles: warp 0 TMA, warp 1
+// MMA, warps 2..9 zero the U rows of other adapters and store the tile.
+// ---------------------------------------------------------------------------
+constexpr int PK = 64;
+constexpr uint32_t kPDrain = 1u << 22;
+constexpr int kGroupM = 16;  // token tiles whose X stays in L2 while the output tiles stream past
+
+template <int BM, int BN>
+struct PCfg {
+  static constexpr int kMT = BM / 128;  // MMAs of M = 128 per K substep
+  static constexpr uint32_t kA = BM * PK * 2, kB = BN * PK * 2;
+  static constexpr int kStages = (int)(196608 / (kA + kB));
+  static constexpr int kAccs = 512 / (kMT * BN) >= 2 ? 2 : 1;  // tiles in tensor memory
+  static constexpr uint32_t kCols = kAccs * kMT * BN;
+  static constexpr uint32_t kBytes = 1024 + kStages * (kA + kB) + 512;
+};
+
+template <int STAGES>
+struct __align__(8) PTail {
+  uint64_t full[STAGES], empty[STAGES];  // words of X and Wd; read
+  uint64_t ufull[STAGES], masked[STAGES];  // U and B_a: landed; U's other rows zeroed
+  uint64_t tfull[2], tempty[2], done;
+  uint32_t tmem;
+  int abort_flag;
+};
+
+template <int STAGES>
+__device__ __forceinline__ void p_abort(PTail<STAGES> *t, DevStatus *st, uint32_t where) {
+  dev_fail(st, kDevTimeout, where);
+  *reinterpret_cast<volatile int *>(&t->abort_flag) = 1;
+}
+
+struct PrefillArgs {
+  const int32_t *ids;
+  const int *lists;
+  int64_t T, out, ldy;
+  int adapters, rank, num_m, num_n, num_kb;
+  __half *Y;
+  DevStatus *st;
+  uint32_t max_polls;
+};
+
+__device__ __forceinline__ void p_tile(int tile, int num_m, int num_n, int &m, int &n) {
+  const int per = kGroupM * num_n, grp = tile / per, first = grp * kGroupM;
+  const int gm = min(kGroupM, num_m - first), local = tile - grp * per;
+  m = first + local % gm;
+  n = local / gm;
+}
+
+template <int BM, int BN>
+__global__ void __launch_bounds__(320, 1)
+    lora_gemm_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
+                     const __grid_constant__ CUtensorMap tmU, const __grid_constant__ CUtensorMap tmB,
+                     const __grid_constant__ PrefillArgs a) {
+  using C = PCfg<BM, BN>;
+  constexpr int STAGES = C::kStages;
+  extern __shared__ uint8_t raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
+  uint8_t *sA = smem, *sB = smem + STAGES * C::kA;
+  auto *tail = reinterpret_cast<PTail<STAGES> *>(sB + STAGES * C::kB);
+  volatile int *abort_flag = &tail->abort_flag;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int tiles = a.num_m * a.num_n;
+  const int rsteps = (a.rank + PK - 1) / PK;  // K steps of an adapter
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(&tail->full[s], 1);
+      mbar_init(&tail->empty[s], 1);
+      mbar_init(&tail->ufull[s], 1);
+      mbar_init(&tail->masked[s], 8);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&tail->tfull[i], 1);
+      mbar_init(&tail->tempty[i], 8);
+    }
+    mbar_init(&tail->done, 1);
+    tail->abort_flag = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&tmX);
+    tma_prefetch_desc(&tmW);
+    tma_prefetch_desc(&tmU);
+    tma_prefetch_desc(&tmB);
+  }
+  if (warp == 1) {
+    tmem_alloc(&tail->tmem, C::kCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tail->tmem;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      uint32_t step = 0, fphase = 0, uphase = 0, last_u = 0;  // per stage: phases, and whose copy is the last
+      bool ok = true;
+      for (int tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x) {
+        int m, n;
+        p_tile(tile, a.num_m, a.num_n, m, n);
+        const int *list = a.lists + (int64_t)m * (BM + 1);
+        const int steps = a.num_kb + list[0] * rsteps;
+        for (int k = 0; k < steps; ++k, ++step) {
+          const int s = step % STAGES;
+          if (!mbar_wait_long(&tail->empty[s], ((step / STAGES) & 1u) ^ 1u, a.max_polls, abort_flag)) {
+            p_abort(tail, a.st, 0xE30u);
+            ok = false;
+            break;
+          }
+          const bool low = k >= a.num_kb;
+          uint64_t *bar = low ? &tail->ufull[s] : &tail->full[s];
+          mbar_arrive_expect_tx(bar, C::kA + C::kB);
+          if (!low) {
+            tma_load_2d(sA + s * C::kA, &tmX, bar, k * PK, m * BM);
+            tma_load_2d(sB + s * C::kB, &tmW, bar, k * PK, n * BN);
+          } else {
+            const int e = (k - a.num_kb) / rsteps, r = (k - a.num_kb) % rsteps;
+            // rows past this adapter's outputs are the next one's: their columns are not stored
+            tma_load_2d(sA + s * C::kA, &tmU, bar, r * PK, m * BM);
+            tma_load_2d(sB + s * C::kB, &tmB, bar, r * PK, (int)(list[1 + e] * a.out + n * BN));
+          }
+          (low ? uphase : fphase) ^= 1u << s;
+          last_u = (last_u & ~(1u << s)) | (low ? 1u << s : 0u);
+        }
+      }
+      if (!ok || *abort_flag)  // own copies in flight
+        for (uint32_t s = 0; s < STAGES && s < step; ++s) {
+          const bool low = (last_u >> s) & 1u;
+          (void)mbar_wait_bounded(low ? &tail->ufull[s] : &tail->full[s],
+                                  (((low ? uphase : fphase) >> s) & 1u) ^ 1u, kPDrain, nullptr);
+        }
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      uint32_t step = 0, fphase = 0, mphase = 0;  // phases per stage
+      int it = 0;
+      bool ok = true, issued = false;
+      for (int tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x, ++it) {
+        int m, n;
+        p_tile(tile, a.num_m, a.num_n, m, n);
+        const int steps = a.num_kb + a.lists[(int64_t)m * (BM + 1)] * rsteps;
+        const int acc = it % C::kAccs;
+        if (!mbar_wait_long(&tail->tempty[acc], ((it / C::kAccs) & 1) ^ 1u, a.max_polls, abort_flag)) {
+          p_abort(tail, a.st, 0xE31u);
+          break;
+        }
+        tc_fence_after();
+        const uint32_t d = tmem + acc * (C::kMT * BN);
+        for (int k = 0; k < steps; ++k, ++step) {
+          const int s = step % STAGES;
+          bool got;
+          int subs = PK / 16;
+          if (k < a.num_kb) {
+            got = mbar_wait_bounded(&tail->full[s], (fphase >> s) & 1u, a.max_polls, abort_flag);
+            fphase ^= 1u << s;
+          } else {
+            got = mbar_wait_long(&tail->masked[s], (mphase >> s) & 1u, a.max_polls, abort_flag);
+            mphase ^= 1u << s;
+            const int left = a.rank - (k - a.num_kb) % rsteps * PK;  // the rest of the box is zero
+            subs = left < PK ? (left + 15) / 16 : PK / 16;
+          }
+          if (!got) {
+            p_abort(tail, a.st, 0xE32u);
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t sa = smem_u32(sA + s * C::kA), sb = smem_u32(sB + s * C::kB);
+          for (int kk = 0; kk < subs; ++kk) {
+            const uint64_t bd = smem_desc_k_sw128(sb + kk * 32);
+#pragma unroll
+            for (int h = 0; h < C::kMT; ++h)
+              tc_mma_f16(d + h * BN, smem_desc_k_sw128(sa + h * 128 * PK * 2 + kk * 32), bd, idesc_f16_f32(128, BN),
+                         (k | kk) != 0 ? 1u : 0u);
+          }
+          issued = true;
+          tc_commit(&tail->empty[s]);
+        }
+        if (!ok) break;
+        tc_commit(&tail->tfull[acc]);
+      }
+      if (issued) {
+        tc_commit(&tail->done);
+        (void)mbar_wait_bounded(&tail->done, 0, kPDrain, nullptr);
+      }
+    }
+  } else {
+    // warps 2..9: lane quarter q of tensor memory; with two MMA halves warps 2..5
+    // and 6..9 take one each, else half of the columns each
+    const int q = warp & 3, part = (warp - 2) >> 2, tid = threadIdx.x - 64;
+    uint32_t step = 0, uphase = 0;
+    int it = 0;
+    bool ok = true;
+    for (int tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x, ++it) {
+      int m, n;
+      p_tile(tile, a.num_m, a.num_n, m, n);
+      const int *list = a.lists + (int64_t)m * (BM + 1);
+      const int count = list[0];
+      step += a.num_kb;
+      if (count) {
+        const int64_t row = (int64_t)m * BM + tid;  // tid >= BM: no row
+        const int id = tid < BM && row < a.T ? a.ids[row] : -1;
+        for (int e = 0; e < count * rsteps && ok; ++e, ++step) {
+          const int s = step % STAGES;
+          int got = 1;
+          if (lane == 0) got = mbar_wait_long(&tail->ufull[s], (uphase >> s) & 1u, a.max_polls, abort_flag);
+          uphase ^= 1u << s;
+          got = __shfl_sync(0xffffffffu, got, 0);
+          if (!got) {
+            if (lane == 0) p_abort(tail, a.st, 0xE33u);
+            ok = false;
+            break;
+          }
+          if (tid < BM && id != list[1 + e / rsteps]) {
+            uint4 *r = reinterpret_cast<uint4 *>(sA + s * C::kA + tid * (PK * 2));
+#pragma unroll
+            for (int i = 0; i < PK / 8; ++i) r[(i + tid) & 7] = make_uint4(0u, 0u, 0u, 0u);
+          }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&tail->masked[s]);
+        }
+        if (!ok) break;
+      }
+      const int acc = it % C::kAccs;
+      int got = 1;
+      if (lane == 0) got = mbar_wait_long(&tail->tfull[acc], (it / C::kAccs) & 1u, a.max_polls, abort_flag);
+      got = __shfl_sync(0xffffffffu, got, 0);
+      if (!got) {
+        if (lane == 0) p_abort(tail, a.st, 0xE34u);
+        break;
+      }
+      tc_fence_after();
+      const int64_t t = (int64_t)m * BM + (C::kMT == 2 ? part * 128 : 0) + q * 32 + lane;
+      const int c0 = C::kMT == 2 ? 0 : part * (BN / 2), c1 = C::kMT == 2 ? BN : c0 + BN / 2;
+      const uint32_t d = tmem + ((uint32_t)(q * 32) << 16) + acc * (C::kMT * BN) + (C::kMT == 2 ? part * BN : 0);
+#pragma unroll 1
+      for (int c = c0; c < c1; c += 32) {
+        float v[32];
+        tmem_ld_32x32b_x32(d + c, v);
+        tmem_ld_wait();
+        const int64_t o = (int64_t)n * BN + c;
+        if (t < a.T && o < a.out) {  // out % 32 == 0
+          uint4 *y = reinterpret_cast<uint4 *>(a.Y + t * a.ldy + o);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t w[4];
+#pragma unroll
+            for (int h = 0; h < 4; ++h) {
+              const __half2 p = __floats2half2_rn(v[8 * i + 2 * h], v[8 * i + 2 * h + 1]);
+              w[h] = *reinterpret_cast<const uint32_t *>(&p);
+            }
+            y[i] = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&tail->tempty[acc]);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::kCols);
+  }
+}
+
+template <int BM, int BN>
+cudaError_t launch_product(const LoraArgs &a, const int *lists, const __half *Wd, int num_sms, cudaStream_t stream) {
+  using C = PCfg<BM, BN>;
+  static bool done[64];
+  static_assert(sizeof(PTail<C::kStages>) <= 512 && C::kBytes <= 232448, "shared memory");
+  cudaError_t e = allow_smem(lora_gemm_kernel<BM, BN>, C::kBytes, done);
+  if (e != cudaSuccess) return e;
+  CUtensorMap x, w, u, b;
+  if ((e = make_tmap_f16_box(&x, a.X, a.T, a.in, a.ldx, PK, BM)) != cudaSuccess) return e;
+  if ((e = make_tmap_f16_box(&w, Wd, a.out, a.in, a.in, PK, BN)) != cudaSuccess) return e;
+  if ((e = make_tmap_f16_box(&u, a.U, a.T, a.rank, a.rank, PK, BM)) != cudaSuccess) return e;
+  if ((e = make_tmap_f16_box(&b, a.B, (int64_t)a.adapters * a.out, a.rank, a.rank, PK, BN)) != cudaSuccess) return e;
+  const PrefillArgs p = {a.ids, lists, a.T, a.out, a.ldy, a.adapters, a.rank, (int)((a.T + BM - 1) / BM),
+                         (int)((a.out + BN - 1) / BN), (int)(a.in / PK), a.Y, a.st, a.max_polls};
+  const int64_t tiles = (int64_t)p.num_m * p.num_n;
+  lora_gemm_kernel<BM, BN><<<(unsigned)i64min(tiles, num_sms), 320, C::kBytes, stream>>>(x, w, u, b, p);
+  return cudaGetLastError();
+}
+}  // namespace
+
+// Token rows of a tile of the product: 128 where 256 would leave SMs idle.
+int lora_prefill_bm(int64_t T, int64_t out, int num_sms) {
+  return ((T + 255) / 256) * ((out + 255) / 256) >= num_sms ? 256 : 128;
+}
+
+size_t lora_prefill_ws(int64_t T, int64_t in, int64_t out, int rank) {
+  auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
+  return up(sizeof(__half) * (size_t)T * rank) + up(sizeof(int) * (size_t)((T + 127) / 128) * 129) +
+         up(sizeof(__half) * (size_t)in * out);
+}
+
+cudaError_t launch_lora_prefill(const LoraArgs &a, int num_sms, cudaStream_t stream) {
+  auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
+  uint8_t *ws = reinterpret_cast<uint8_t *>(a.U);
+  int *lists = reinterpret_cast<int *>(ws + up(sizeof(__half) * (size_t)a.T * a.rank));
+  __half *Wd = reinterpret_cast<__half *>(reinterpret_cast<uint8_t *>(lists) +
+                                          up(sizeof(int) * (size_t)((a.T + 127) / 128) * 129));
+  const int bm = lora_prefill_bm(a.T, a.out, num_sms);
+  cudaError_t e = cudaMemsetAsync(a.st, 0, sizeof(DevStatus), stream);
+  if (e != cudaSuccess) return e;
+  const int64_t n_shrink = (a.T + kShT - 1) / kShT, n_lists = (a.T + bm - 1) / bm;
+  const int64_t n_deq = ((a.out + kDeqOut - 1) / kDeqOut) * ((a.in + kDeqIn - 1) / kDeqIn);
+  if (n_shrink + n_lists + n_deq > INT32_MAX) return cudaErrorInvalidValue;
+  lora_prepare_kernel<<<(unsigned)(n_shrink + n_lists + n_deq), 256, 0, stream>>>(a, (int)n_shrink, (int)n_lists, bm,
+                                                                                  lists, Wd);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  return bm == 256 ? launch_product<256, 256>(a, lists, Wd, num_sms, stream)
+                   : launch_product<128, 128>(a, lists, Wd, num_sms, stream);
+}
+
+}  // namespace awq

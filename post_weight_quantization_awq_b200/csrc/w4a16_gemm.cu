@@ -37,6 +37,7 @@
 #include <cuda_fp16.h>
 
 #include "awq_launch.h"
+#include "w4_dequant.cuh"
 
 namespace awq {
 
@@ -105,41 +106,6 @@ __device__ __forceinline__ void q_tile_split(int tile, int num_m, int num_n, int
   q_tile_coords(tile / splits, num_m, num_n, m_blk, n_blk);
   kb0 = (int)((int64_t)sp * num_kb / splits);
   kb1 = (int)((int64_t)(sp + 1) * num_kb / splits);
-}
-
-// fp16 pairs {1024 + nibble p, 1024 + nibble p + 4}, p = 0..3, of a word
-__device__ __forceinline__ void nib_pairs(uint32_t w, __half2 (&h)[4]) {
-#pragma unroll
-  for (int p = 0; p < 4; ++p) {
-    const uint32_t bits = ((w >> (4 * p)) & 0x000F000Fu) | 0x64006400u;
-    h[p] = *reinterpret_cast<const __half2 *>(&bits);
-  }
-}
-
-// scales of outputs (p, p + 4), p = 0..3, from 8 consecutive fp16 scales
-__device__ __forceinline__ void scale_pairs(uint4 sc, __half2 (&h)[4]) {
-  const uint32_t lo[2] = {sc.x, sc.y}, hi[2] = {sc.z, sc.w};
-#pragma unroll
-  for (int p = 0; p < 4; ++p) {
-    // half p of the first four, half p of the last four
-    const uint32_t a = lo[p >> 1], b = hi[p >> 1];
-    const uint32_t bits = __byte_perm(a, b, (p & 1) ? 0x7632u : 0x5410u);
-    h[p] = *reinterpret_cast<const __half2 *>(&bits);
-  }
-}
-
-// 8 weights RN16((q - z) * scale) of one word in the order 0,4,1,5,2,6,3,7;
-// (1024 + q) - (1024 + z) is exact
-__device__ __forceinline__ uint4 dequant_word(uint32_t w, const __half2 (&zp)[4], const __half2 (&sp)[4]) {
-  __half2 qp[4];
-  nib_pairs(w, qp);
-  uint32_t o[4];
-#pragma unroll
-  for (int p = 0; p < 4; ++p) {
-    const __half2 r = __hmul2(__hsub2(qp[p], zp[p]), sp[p]);
-    o[p] = *reinterpret_cast<const uint32_t *>(&r);
-  }
-  return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
 __device__ __forceinline__ void q_abort(QTail *t, DevStatus *st, uint32_t where) {
@@ -480,62 +446,14 @@ __global__ void __launch_bounds__(Q_THREADS, 1) w4a16_gemm_kernel(
   }
 }
 
-// The dequantised weights Wd [out, in] fp16, Wd[o][j] = RN16((q - z) scale) --
-// the values the GEMM above builds tile by tile -- written once for a product
-// with many tokens.  A block turns a 128-input x 64-output tile of packed
-// words (input-major) into output-major rows through shared memory, so both
-// the word loads and the 16-byte row stores are contiguous.
+// The dequantised weights, written once for a product with many tokens.
 __global__ void __launch_bounds__(256) w4a16_dequant_kernel(
     const int32_t *__restrict__ qweight, const int32_t *__restrict__ qzeros,
     const __half *__restrict__ scales, int64_t in, int64_t out, int group, __half *__restrict__ Wd) {
-  constexpr int TJ = 128, TO = 64, WPR = TO / 8;  // inputs, outputs, words per input row
-  // [output][input] with the 16-byte chunks of row r XOR-swizzled by r / 8, so
-  // that the 2-byte writes of one warp (8 word columns, i.e. rows 8 apart)
-  // fall in different banks and the 16-byte row reads stay aligned
-  __shared__ __align__(16) __half tile[TO][TJ];
+  __shared__ __align__(16) __half tile[kDeqOut * kDeqIn];
   // outputs along x (up to 2^22 / 64 blocks), inputs along y (at most 2^20 / 128)
-  const int64_t o0 = (int64_t)blockIdx.x * TO, j0 = (int64_t)blockIdx.y * TJ;
-  const int64_t words = out / 8;
-  // a thread converts the words of two consecutive input rows of one word
-  // column (one group: group % 32 == 0) and writes each output's two weights
-  // as one half2
-#pragma unroll
-  for (int i = 0; i < TJ * WPR / 512; ++i) {
-    const int w = threadIdx.x + 256 * i;
-    const int jp = w / WPR, ow = w % WPR;  // input row pair of the tile, word column
-    const int jj = 2 * jp;
-    const int64_t j = j0 + jj, wc = o0 / 8 + ow;
-    uint4 v0 = make_uint4(0u, 0u, 0u, 0u), v1 = v0;
-    if (j < in && wc < words) {  // in % 64 == 0: rows j and j + 1 are both in
-      const int64_t gi = j / group;
-      __half2 zp[4], sp[4];
-      nib_pairs((uint32_t)__ldg(qzeros + gi * words + wc), zp);
-      scale_pairs(__ldg(reinterpret_cast<const uint4 *>(scales + gi * out + 8 * wc)), sp);
-      const int32_t *qp = qweight + j * words + wc;
-      v0 = dequant_word((uint32_t)__ldg(qp), zp, sp);
-      v1 = dequant_word((uint32_t)__ldg(qp + words), zp, sp);
-    }
-    // v0 / v1 hold outputs 0,4,1,5,2,6,3,7 of the word in rows jj / jj + 1
-    const uint32_t h0[4] = {v0.x, v0.y, v0.z, v0.w}, h1[4] = {v1.x, v1.y, v1.z, v1.w};
-    const int col = (((jj >> 3) ^ ow) << 3) | (jj & 7);  // rows 8 ow .. 8 ow + 7 share the swizzle
-#pragma unroll
-    for (int p = 0; p < 4; ++p) {
-      // output p: low halves of row jj and row jj + 1; output p + 4: the high halves
-      const uint32_t lo = __byte_perm(h0[p], h1[p], 0x5410u), hi = __byte_perm(h0[p], h1[p], 0x7632u);
-      *reinterpret_cast<uint32_t *>(&tile[8 * ow + p][col]) = lo;
-      *reinterpret_cast<uint32_t *>(&tile[8 * ow + p + 4][col]) = hi;
-    }
-  }
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < TO * (TJ / 8) / 256; ++i) {
-    const int c = threadIdx.x + 256 * i;
-    const int oo = c / (TJ / 8), jc = c % (TJ / 8);  // output row, 8-input chunk
-    const int64_t o = o0 + oo, j = j0 + 8 * jc;
-    if (o < out && j < in)  // in % 64 == 0: a chunk is whole
-      *reinterpret_cast<uint4 *>(Wd + o * in + j) =
-          *reinterpret_cast<const uint4 *>(&tile[oo][8 * (jc ^ (oo >> 3))]);
-  }
+  dequant_tile(tile, qweight, qzeros, scales, in, out, group, (int64_t)blockIdx.x * kDeqOut,
+               (int64_t)blockIdx.y * kDeqIn, Wd);
 }
 
 cudaError_t launch_w4a16_dequant(const int32_t *qweight, const int32_t *qzeros, const __half *scales,
