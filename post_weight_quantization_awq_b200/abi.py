@@ -196,7 +196,8 @@ def _stream(stream) -> int:
     if stream is not None:
         return int(stream)
     import torch
-    return torch.cuda.current_stream().cuda_stream
+    # the current stream's handle without building a Stream object (0.1 against 3 us)
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
 def awq_workspace_size(T: int, inn: int, out: int, cfg: AwqConfig) -> int:

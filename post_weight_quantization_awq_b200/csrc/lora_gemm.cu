@@ -3,9 +3,12 @@
 //   Y[t][o] = RN16( sum_j X[t][j] (q - z) s  +  c_a sum_r U[t][r] B_a[o][r] ),
 //   U[t][r] = sum_j X[t][j] A_a[r][j],  a = ids[t]  (-1: no adapter)
 //
-// Two launches.  lora_shrink_kernel computes c_a U in fp32; it lets its
-// successor start at once (programmatic dependent launch), which meanwhile
-// streams the packed weights and waits for U only before its epilogue.
+// For a handful of tokens one launch does it all: the blocks of a cluster compute
+// c_a U over their input rows while the first words travel, and add it through
+// distributed shared memory.  Where that would read more of A than of the words
+// (every output tile's cluster reads all of it), lora_shrink_kernel computes U
+// first and lets its successor start at once (programmatic dependent launch),
+// which meanwhile streams the words and waits for U only before its epilogue.
 #include <cooperative_groups.h>
 
 #include "awq_launch.h"
@@ -32,23 +35,46 @@ __device__ __forceinline__ float dot8(uint4 a, uint4 b, float s) {
   return s;
 }
 
-// One warp per (token, rank row).
+// U of one token and kShrinkR rank rows a block: the 8 warps take eighths of the
+// input, all loads of a warp in flight at once, and meet in shared memory.
+constexpr int kShrinkR = 8;
 __global__ void __launch_bounds__(256) lora_shrink_kernel(const LoraArgs a) {
+  __shared__ float part[8][kShrinkR];
   pdl_launch();
   if (blockIdx.x == 0 && threadIdx.x == 0) *a.st = DevStatus{};
-  const int64_t i = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  const int64_t t = i / a.rank, r = i - t * a.rank;
-  if (t >= a.T) return;
+  const int chunks = a.rank / kShrinkR, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t t = blockIdx.x / chunks;
+  const int r0 = (int)(blockIdx.x - t * chunks) * kShrinkR;
   const int id = a.ids[t];
   if (id < 0 || id >= a.adapters) return;  // never read
+  const int n = (int)(a.in / 8), c0 = n * warp / 8, c1 = n * (warp + 1) / 8;  // 16-byte chunks
   const uint4 *x = reinterpret_cast<const uint4 *>(a.X + t * a.ldx);
-  const uint4 *w = reinterpret_cast<const uint4 *>(a.A + ((int64_t)id * a.rank + r) * a.in);
-  float s = 0.0f;
-  for (int64_t k = lane; k < a.in / 8; k += 32) s = dot8(__ldg(x + k), __ldg(w + k), s);
+  const uint4 *w = reinterpret_cast<const uint4 *>(a.A + ((int64_t)id * a.rank + r0) * a.in);
+  float s[kShrinkR];
 #pragma unroll
-  for (int m = 16; m; m >>= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
-  if (lane == 0) a.U[t * a.rank + r] = a.c[id] * s;
+  for (int r = 0; r < kShrinkR; ++r) s[r] = 0.0f;
+#pragma unroll 2
+  for (int k = c0 + lane; k < c1; k += 32) {
+    const uint4 xv = __ldg(x + k);
+    uint4 wv[kShrinkR];
+#pragma unroll
+    for (int r = 0; r < kShrinkR; ++r) wv[r] = __ldg(w + (int64_t)r * n + k);
+#pragma unroll
+    for (int r = 0; r < kShrinkR; ++r) s[r] = dot8(xv, wv[r], s[r]);
+  }
+#pragma unroll
+  for (int r = 0; r < kShrinkR; ++r) {
+#pragma unroll
+    for (int m = 16; m; m >>= 1) s[r] += __shfl_xor_sync(0xffffffffu, s[r], m);
+    if (lane == 0) part[warp][r] = s[r];
+  }
+  __syncthreads();
+  if (threadIdx.x < kShrinkR) {
+    float u = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) u += part[i][threadIdx.x];
+    a.U[t * a.rank + r0 + threadIdx.x] = a.c[id] * u;
+  }
 }
 
 // A cluster of `splits` blocks covers 256 outputs x MAXTOK tokens, each block
@@ -59,18 +85,22 @@ __global__ void __launch_bounds__(256) lora_shrink_kernel(const LoraArgs a) {
 // are A operands straight from global memory, and U (fp32) is an fp16 pair
 // hi + lo of 22 bits under a power of two of its token, so nothing is rounded
 // away and no U overflows.  An adapter's sums are added for its own tokens only.
+constexpr int kFusedU = 64;  // values of U a cluster computes itself, at most
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
 template <Mode M, int NT, int MAXTOK, int STAGES>
 struct LoraShared {
   static constexpr uint32_t kRing = STAGES * stage_bytes<M, MAXTOK>();
   static constexpr uint32_t kRed = (MAXTOK * kRedPitch * 4 + 15) / 16 * 16;  // in the ring, after the product
   static constexpr int kUPitch = 2 * (256 + 8);                               // bytes of a token's hi (lo) row
   static constexpr uint32_t kU = 2 * MAXTOK * kUPitch;                        // behind it
-  static constexpr uint32_t kTail = sizeof(RingBars<STAGES>) + MAXTOK * 12 + 16;
+  static constexpr uint32_t kTail = sizeof(RingBars<STAGES>) + MAXTOK * 12 + 16 + 2 * kFusedU * 4;
   static constexpr uint32_t kBytes = 1024 + kRing + kTail;
   static_assert(kRed + kU <= kRing, "the sums and U reuse the ring");
 };
 
-template <Mode M, int NT, int MAXTOK, int STAGES, int MINB>
+template <Mode M, int NT, int MAXTOK, int STAGES, int MINB, bool FUSED>
 __global__ void __launch_bounds__(kThreads, MINB)
     lora_stream_kernel(const __grid_constant__ LoraArgs a, const __grid_constant__ CUtensorMap map, const int splits) {
   using L = LoraShared<M, NT, MAXTOK, STAGES>;
@@ -83,6 +113,8 @@ __global__ void __launch_bounds__(kThreads, MINB)
   int *list = ids + MAXTOK;                      // the different ones
   float *uscale = reinterpret_cast<float *>(list + MAXTOK);
   int *n_list = reinterpret_cast<int *>(uscale + MAXTOK);
+  float *upart = reinterpret_cast<float *>(n_list + 4);  // FUSED: U over this block's rows, [token][rank row]
+  float *usum = upart + kFusedU;                         // and over all
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = (int)(blockIdx.x % (unsigned)splits);
   const int64_t tile = blockIdx.x / (unsigned)splits;
@@ -101,7 +133,16 @@ __global__ void __launch_bounds__(kThreads, MINB)
                   (int)(tile * 32), (int)(a.out / 8), (int)(tile * 32), (int)(a.out / 8)};
     p.rows(a.X + t0 * a.ldx, a.ldx, n, [](int t) { return t; });
     RingPos pos;
+    if (FUSED) {
+      if (blockIdx.x == 0 && lane == 0) *a.st = DevStatus{};
+      __syncwarp();
+    }
     p.run(pos, smem_u32(ring), bars, k0, k1, a.max_polls, a.st);
+    if (FUSED) {
+      __syncwarp();
+      cluster_arrive();
+      cluster_wait();
+    }
     if (*reinterpret_cast<volatile int *>(&bars->abort)) ring_drain(bars, pos);
   } else {
     RingPos pos;
@@ -124,13 +165,39 @@ __global__ void __launch_bounds__(kThreads, MINB)
       }
       if (lane == 0) *n_list = count;
     }
+    if (FUSED) {  // U over rows [k0, k1), a warp to a value
+      for (int i = warp; i < n * a.rank; i += kConsumers / 32) {
+        const int t = i / a.rank, r = i - t * a.rank, id = ids[t];
+        if (id < 0) continue;
+        const uint4 *x = reinterpret_cast<const uint4 *>(a.X + (t0 + t) * a.ldx);
+        const uint4 *w = reinterpret_cast<const uint4 *>(a.A + ((int64_t)id * a.rank + r) * a.in);
+        float s = 0.0f;
+#pragma unroll 2
+        for (int k = k0 / 8 + lane; k < k1 / 8; k += 32) s = dot8(__ldg(x + k), __ldg(w + k), s);
+#pragma unroll
+        for (int m = 16; m; m >>= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
+        if (lane == 0) upart[i] = a.c[id] * s;
+      }
+      __syncwarp();
+      cluster_arrive();
+    }
     consume<M, NT, MAXTOK, STAGES>(acc, pos, ring, bars, group_shift(a.group), k0, k1, true, a.max_polls, a.st);
-    pdl_wait();  // U and the cleared status word
+    if (FUSED) {
+      cluster_wait();
+      for (int i = tid; i < n * a.rank; i += kConsumers) {
+        float u = 0.0f;
+        if (ids[i / a.rank] >= 0)
+          for (int s = 0; s < splits; ++s) u += cluster.map_shared_rank(upart, s)[i];
+        usum[i] = u;
+      }
+    } else {
+      pdl_wait();  // U and the cleared status word
+    }
     consumer_sync();
-    const int r16 = (a.rank + 15) / 16 * 16;
+    const int r32 = (a.rank + 31) / 32 * 32;
     for (int t = warp; t < MAXTOK; t += kConsumers / 32) {
       const bool on = t < n && ids[t] >= 0;
-      const float *u = a.U + (t0 + t) * a.rank;
+      const float *u = FUSED ? usum + t * a.rank : a.U + (t0 + t) * a.rank;
       float m = 0.0f;
       for (int k = lane; on && k < a.rank; k += 32) m = fmaxf(m, fabsf(u[k]));
 #pragma unroll
@@ -141,7 +208,7 @@ __global__ void __launch_bounds__(kThreads, MINB)
       const float up = scaled ? __uint_as_float((uint32_t)(127 + e) << 23) : 1.0f;
       const float down = scaled ? __uint_as_float((uint32_t)(127 - e) << 23) : 1.0f;
       if (lane == 0) uscale[t] = up;
-      for (int k = lane; k < r16; k += 32) {
+      for (int k = lane; k < r32; k += 32) {
         const float v = on && k < a.rank ? u[k] * down : 0.0f;
         const __half hi = __float2half_rn(v);
         __half *d = reinterpret_cast<__half *>(uhl + t * L::kUPitch) + k;
@@ -154,8 +221,9 @@ __global__ void __launch_bounds__(kThreads, MINB)
     const int64_t o0 = tile * kBoxN + (nw * 8 + g) * 8;
     const int tt = M == Mode::kTok ? half * NT * 8 : 0;  // this warp's first token column
     const int step = M == Mode::kK ? 2 * splits : splits, first = M == Mode::kK ? 2 * rank + half : rank;
-    const uint32_t ua = smem_u32(uhl) + (tt + (NT == 1 ? lane & 7 : (lane >> 4) * 8 + (lane & 7))) * L::kUPitch +
-                        (NT == 1 ? lane >> 3 : (lane >> 3) & 1) * 16;
+    // 32 rank rows a step, a lane's 16 bytes at 8q of a row of B_a (or of U) being
+    // its fragments of two MMAs
+    const uint8_t *ul = uhl + (tt + g) * L::kUPitch + q * 16;
     for (int j = first; j < *n_list; j += step) {
       const int id = list[j];
 #pragma unroll
@@ -164,32 +232,26 @@ __global__ void __launch_bounds__(kThreads, MINB)
         for (int x = 0; x < NT; ++x)
 #pragma unroll
           for (int c = 0; c < 4; ++c) acc.grp[p][x][c] = 0.0f;
-      const __half *bp = a.B + ((int64_t)id * a.out + o0) * a.rank + 2 * q;
+      const __half *bp = a.B + ((int64_t)id * a.out + o0) * a.rank + 8 * q;
       const bool o_ok = o0 < a.out;  // out % 32 == 0: the 8 outputs are all in or all out
-#pragma unroll 2
-      for (int k = 0; k < r16; k += 16) {
-        uint32_t af[4][4];
+#pragma unroll 1
+      for (int k = 0; k < r32; k += 32) {
+        uint4 af[8];
 #pragma unroll
-        for (int p = 0; p < 4; ++p)
+        for (int o = 0; o < 8; ++o)
+          af[o] = o_ok && k + 8 * q < a.rank ? __ldg(reinterpret_cast<const uint4 *>(bp + (int64_t)o * a.rank + k))
+                                             : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int kk = k + 8 * (i >> 1);
-            af[p][i] = o_ok && kk < a.rank
-                           ? __ldg(reinterpret_cast<const uint32_t *>(bp + (int64_t)(p + 4 * (i & 1)) * a.rank + kk))
-                           : 0u;
+        for (int x = 0; x < NT; ++x)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {  // hi, lo
+            const uint4 b = *reinterpret_cast<const uint4 *>(ul + h * (L::kU / 2) + x * 8 * L::kUPitch + k * 2);
+#pragma unroll
+            for (int p = 0; p < 4; ++p) {
+              mma16816(acc.grp[p][x], af[p].x, af[p + 4].x, af[p].y, af[p + 4].y, b.x, b.y);
+              mma16816(acc.grp[p][x], af[p].z, af[p + 4].z, af[p].w, af[p + 4].w, b.z, b.w);
+            }
           }
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {  // hi, lo
-          uint32_t b[(NT + 1) / 2][4];
-#pragma unroll
-          for (int x = 0; x < (NT + 1) / 2; ++x) ldsm4(b[x], ua + h * (L::kU / 2) + x * 16 * L::kUPitch + k * 2);
-#pragma unroll
-          for (int p = 0; p < 4; ++p)
-#pragma unroll
-            for (int x = 0; x < NT; ++x)
-              mma16816(acc.grp[p][x], af[p][0], af[p][1], af[p][2], af[p][3], b[x / 2][2 * (x & 1)],
-                       b[x / 2][2 * (x & 1) + 1]);
-        }
       }
 #pragma unroll
       for (int x = 0; x < NT; ++x)
@@ -207,7 +269,7 @@ __global__ void __launch_bounds__(kThreads, MINB)
     store_sums<M, NT>(acc, red);
   }
   if (blockIdx.x == 0 && warp == kConsumers / 32) {
-    pdl_wait();
+    if (!FUSED) pdl_wait();
     for (int t = lane; t < n; t += 32) {
       const int id = a.ids[t0 + t];
       if (id < -1 || id >= a.adapters) dev_fail(a.st, kDevBadAdapter, 0xE01u);
@@ -230,23 +292,57 @@ __global__ void __launch_bounds__(kThreads, MINB)
   cluster.sync();  // no block leaves while its sums are read
 }
 
-template <Mode M, int NT, int MAXTOK, int STAGES, int MINB>
-cudaError_t launch_stream(const LoraArgs &a, int num_sms, cudaStream_t stream) {
+// The most blocks of a cluster (up to 8) with which `clusters` of them run at
+// once: a second wave costs a whole pass (16 clusters of 8 blocks do not fit the
+// GPCs at one block per SM: 15.5 us for the last to start).
+template <class K>
+int cluster_size(K kernel, size_t smem, int64_t clusters, int64_t most, int (&fit)[64][9]) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 1;
+  for (int s = (int)(most < 8 ? most : 8); s > 1; --s) {
+    if (!fit[dev][s]) {
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3((unsigned)s);
+      cfg.blockDim = dim3(kThreads);
+      cfg.dynamicSmemBytes = smem;
+      cudaLaunchAttribute at[1];
+      at[0].id = cudaLaunchAttributeClusterDimension;
+      at[0].val.clusterDim.x = (unsigned)s;
+      at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+      cfg.attrs = at;
+      cfg.numAttrs = 1;
+      int n = 0;
+      if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
+        (void)cudaGetLastError();
+        n = 0;
+      }
+      fit[dev][s] = n + 1;
+    }
+    if (fit[dev][s] - 1 >= clusters) return s;
+  }
+  return 1;
+}
+
+template <Mode M, int NT, int MAXTOK, int STAGES, int MINB, bool FUSED>
+cudaError_t launch_stream(const LoraArgs &a, int, cudaStream_t stream) {
   static bool done[64];
+  static int fit[64][9];
   constexpr size_t kSmem = LoraShared<M, NT, MAXTOK, STAGES>::kBytes;
   static_assert(MINB * (kSmem + 1024) <= 233472, "resident blocks");
-  auto kernel = lora_stream_kernel<M, NT, MAXTOK, STAGES, MINB>;
+  auto kernel = lora_stream_kernel<M, NT, MAXTOK, STAGES, MINB, FUSED>;
   cudaError_t e = allow_smem(kernel, kSmem, done);
   if (e != cudaSuccess) return e;
   CUtensorMap map;  // the words as pairs of 16-bit values
   e = make_tmap_f16_box(&map, a.qweight, a.in, a.out / 4, a.out / 4, 64, kBoxK);
   if (e != cudaSuccess) return e;
-  const int64_t tiles = (a.out + kBoxN - 1) / kBoxN, ttiles = (a.T + MAXTOK - 1) / MAXTOK;
-  // blocks of a cluster: as many as fill the SMs, a power of two (clusters of 3
-  // or 5 leave SMs of a GPC over: 48 of 3 ran as two waves)
-  const int64_t most = (a.in + 127) / 128;
-  int64_t s = 1;
-  while (s < 8 && 2 * s <= most && 2 * s * tiles * ttiles <= (int64_t)num_sms * MINB) s *= 2;
+  const int64_t tiles = (a.out + kBoxN - 1) / kBoxN;
+  const int s = cluster_size(kernel, kSmem, tiles, (a.in + 127) / 128, fit);
+  if (!FUSED) {
+    const int64_t blocks = a.T * (a.rank / kShrinkR);
+    lora_shrink_kernel<<<(unsigned)blocks, 256, 0, stream>>>(a);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+  }
   cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeClusterDimension;
   at[0].val.clusterDim.x = (unsigned)s;
@@ -254,26 +350,25 @@ cudaError_t launch_stream(const LoraArgs &a, int num_sms, cudaStream_t stream) {
   at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[1].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(tiles * s), (unsigned)ttiles);
+  cfg.gridDim = dim3((unsigned)(tiles * s));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = kSmem;
   cfg.stream = stream;
   cfg.attrs = at;
-  cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, kernel, a, map, (int)s);
+  cfg.numAttrs = FUSED ? 1 : 2;
+  return cudaLaunchKernelEx(&cfg, kernel, a, map, s);
 }
 }  // namespace
 
 cudaError_t launch_lora(const LoraArgs &a, int num_sms, cudaStream_t stream) {
-  const int64_t blocks = (a.T * a.rank + 7) / 8;
-  lora_shrink_kernel<<<(unsigned)blocks, 256, 0, stream>>>(a);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  if (a.T <= 8) return launch_stream<Mode::kK, 1, 8, 4, 2>(a, num_sms, stream);
-  if (a.T <= 16) return launch_stream<Mode::kK, 2, 16, 8, 1>(a, num_sms, stream);
-  if (a.T <= 32) return launch_stream<Mode::kTok, 2, 32, 6, 1>(a, num_sms, stream);
-  if (a.T <= 48) return launch_stream<Mode::kTok, 3, 48, 6, 1>(a, num_sms, stream);
-  return launch_stream<Mode::kTok, 4, 64, 5, 1>(a, num_sms, stream);
+  // on its own up to as many values of U as keep A's part below the words'
+  // (1 token at rank 64: as many bytes of A as of words for a block)
+  if (a.T <= 8 && a.T * a.rank <= 64) return launch_stream<Mode::kK, 1, 8, 4, 2, true>(a, num_sms, stream);
+  if (a.T <= 8) return launch_stream<Mode::kK, 1, 8, 4, 2, false>(a, num_sms, stream);
+  if (a.T <= 16) return launch_stream<Mode::kK, 2, 16, 8, 1, false>(a, num_sms, stream);
+  if (a.T <= 32) return launch_stream<Mode::kTok, 2, 32, 6, 1, false>(a, num_sms, stream);
+  if (a.T <= 48) return launch_stream<Mode::kTok, 3, 48, 6, 1, false>(a, num_sms, stream);
+  return launch_stream<Mode::kTok, 4, 64, 5, 1, false>(a, num_sms, stream);
 }
 
 }  // namespace awq

@@ -323,50 +323,51 @@ __device__ __forceinline__ int h_rows(int n) { return 2 * n <= 8 ? 2 * n : n; }
 
 __device__ __forceinline__ float silu_mul(float g, float u) { return g / (1.0f + expf(-g)) * u; }
 
-// The units of a phase: for each tile, each entry and each 128 input rows, in
-// that order (gate|up: entry, then pair of tiles, then gate, up).  Blocks take
-// even shares of their cost.  `per` units of equal cost follow one another; a
-// run of them is a "stretch": (entry, tile) pairs.
+// The units of a phase in their order: by (entry, tile) pair, a "stretch" of
+// `len` units of 128 input rows, gate|up with the entry outermost (and gate's
+// tile before up's), down with the tile outermost.  Blocks take even shares of
+// the units' cost.  Costs stay below 2^26 (about 300 entries of 5, 256 tiles, 128
+// units; or 32 tiles, 512 units): 32 bits.
 template <int V, bool DOWN>
 struct Work {
   const MoeLists<V> *sh;
-  int n_seg, tiles, len;  // tiles: gate|up 2 x the pairs of tiles, down the tiles; len: units of a stretch
-  int64_t quota;
+  int n_seg, tiles, len;  // tiles: gate|up 2 x the pairs of tiles, down the tiles
+  int stretches, quota;
 
-  __device__ __forceinline__ Work(const MoeLists<V> *l, int tiles_, int len_) : sh(l), n_seg(l->n_seg), tiles(tiles_), len(len_) {
-    const int64_t total = (int64_t)sh->seg_cost[n_seg] * tiles * len;
-    quota = (total + gridDim.x - 1) / gridDim.x;
+  __device__ __forceinline__ Work(const MoeLists<V> *l, int tiles_, int len_)
+      : sh(l), n_seg(l->n_seg), tiles(tiles_), len(len_), stretches(l->n_seg * tiles_) {
+    const int total = sh->seg_cost[n_seg] * tiles * len;
+    quota = (total + (int)gridDim.x - 1) / (int)gridDim.x;
     // at least a unit's cost, so that every block between a stretch's first and last has a unit of it
-    quota = quota < unit_cost(Cfg<V>::kTok) ? unit_cost(Cfg<V>::kTok) : quota;
+    quota = max(quota, unit_cost(Cfg<V>::kTok));
   }
   __device__ __forceinline__ int cost(int seg) const { return sh->seg_cost[seg + 1] - sh->seg_cost[seg]; }
   // stretch = seg * tiles + tile (gate|up), tile * n_seg + seg (down)
   __device__ __forceinline__ int seg_of(int stretch) const { return DOWN ? stretch % n_seg : stretch / tiles; }
   __device__ __forceinline__ int tile_of(int stretch) const { return DOWN ? stretch / n_seg : stretch % tiles; }
-  __device__ __forceinline__ int64_t cost_before(int stretch) const {
+  __device__ __forceinline__ int cost_before(int stretch) const {
     const int seg = seg_of(stretch), tile = tile_of(stretch);
-    const int64_t c = DOWN ? (int64_t)tile * sh->seg_cost[n_seg] + sh->seg_cost[seg]
-                           : (int64_t)sh->seg_cost[seg] * tiles + (int64_t)tile * cost(seg);
-    return c * len;
+    return (DOWN ? tile * sh->seg_cost[n_seg] + sh->seg_cost[seg] : sh->seg_cost[seg] * tiles + tile * cost(seg)) * len;
   }
-  // Units of a stretch that a block takes begin at its first unit whose cost
-  // offset is at least the block's share: first unit of block b in the stretch.
-  __device__ __forceinline__ int first_unit(int stretch, int64_t b) const {
-    const int64_t d = b * quota - cost_before(stretch);
-    const int c = cost(seg_of(stretch));
-    const int64_t u = d <= 0 ? 0 : (d + c - 1) / c;
-    return (int)(u < len ? u : len);
+  // The units of a stretch that block b takes: those whose cost offset lies in
+  // its share [b quota, (b + 1) quota).
+  __device__ __forceinline__ void units(int stretch, int b, int &u0, int &u1) const {
+    const int d = b * quota - cost_before(stretch), c = cost(seg_of(stretch));
+    u0 = d <= 0 ? 0 : min((d + c - 1) / c, len);
+    u1 = d + quota <= 0 ? 0 : min((d + quota + c - 1) / c, len);
   }
-  // The blocks that take units of a stretch: those of its first and last unit.
-  __device__ __forceinline__ int block_of(int stretch, int unit) const {
-    return (int)((cost_before(stretch) + (int64_t)unit * cost(seg_of(stretch))) / quota);
+  // The blocks of a stretch's first and last unit: all that take part in it.
+  __device__ __forceinline__ int2 blocks(int stretch) const {
+    const int at = cost_before(stretch);
+    return make_int2(at / quota, (at + (len - 1) * cost(seg_of(stretch))) / quota);
   }
-  // The stretch that holds cost offset c.
-  __device__ __forceinline__ int find(int64_t c) const {
-    int lo = 0, hi = n_seg * tiles;  // the last stretch with cost_before <= c
+  // The last stretch that begins at or before block b's share.
+  __device__ __forceinline__ int first_of(int b) const {
+    const int at = b * quota;
+    int lo = 0, hi = stretches;
     while (hi - lo > 1) {
       const int m = (lo + hi) / 2;
-      if (cost_before(m) <= c)
+      if (cost_before(m) <= at)
         lo = m;
       else
         hi = m;
@@ -374,6 +375,20 @@ struct Work {
     return lo;
   }
 };
+
+// Block b's stretches of a phase, in order: f(stretch, first unit, end).
+template <class W, class F>
+__device__ __forceinline__ void each_stretch(const W &w, int b, F f) {
+  if (!w.stretches) return;
+  for (int s = w.first_of(b); s < w.stretches; ++s) {
+    int u0, u1;
+    w.units(s, b, u0, u1);
+    if (u0 < u1)
+      f(s, u0, u1);
+    else if (u0 < w.len)
+      break;  // the block's share has ended
+  }
+}
 
 template <int V>
 __global__ void __launch_bounds__(kThreads, Cfg<V>::kBlocks)
@@ -437,7 +452,6 @@ __global__ void __launch_bounds__(kThreads, Cfg<V>::kBlocks)
   const Work<V, false> up(sh, 2 * itiles, kgh);
   const Work<V, true> down(sh, htiles, kgi);
   const int wi = inter / 8, wh = hidden / 8;  // word columns
-  const int64_t up_end = (int64_t)up.n_seg * up.tiles, dn_end = (int64_t)down.n_seg * down.tiles;
   const int64_t pitch_gu = 2 * a.inter;  // a row of the gate|up sums
   // the words of a stretch
   const auto up_weights = [&](int stretch) {
@@ -452,63 +466,47 @@ __global__ void __launch_bounds__(kThreads, Cfg<V>::kBlocks)
     const int64_t groups = (int64_t)e * (inter / a.group);
     return Weights{&dn_map, e * inter, a.dn_z + groups * wh, a.dn_s + groups * hidden, wh, shift, c0, wh, c0 + 32, wh};
   };
-  const int up_first = up_end ? up.find((int64_t)blockIdx.x * up.quota) : 0;
-  const int dn_first = dn_end ? down.find((int64_t)blockIdx.x * down.quota) : 0;
   bool ok = true;
 
   if (tid >= kConsumers) {
     // ------------------------------------------------------------ producer
     RingPos pos;
-    {
-      for (int s = up_first; s < up_end; ++s) {
-        const int u0 = up.first_unit(s, blockIdx.x), u1 = up.first_unit(s, blockIdx.x + 1);
-        if (u0 >= u1) {
-          if (u0 < up.len) break;  // the block's share ended
-          continue;
-        }
-        Producer<Mode::kN, C::kTok> p;
-        p.w = up_weights(s);
-        const int seg = up.seg_of(s), p0 = sh->seg_first[seg];
-        p.rows(a.X, a.ldx, sh->seg_n[seg], [&](int t) { return sh->pair[p0 + t] / a.top_k; });
-        p.template run<C::kStages>(pos, ring_u, bars, u0 * 128, min(u1 * 128, hidden), a.max_polls, st);
-      }
-    }
-    // the first words of a down stretch do not wait for its H
-    const auto words_ahead = [&](const Producer<Mode::kN, C::kTok> &p, int k0, int k1) {
-      RingPos r = pos;
-      const int most = min(num_stages<Mode::kN>(k1 - k0), C::kStages);
-      int n = 0;
-      while (n < most && ring_wait(bars, &bars->empty[r.slot], r.phase ^ 1u, a.max_polls, st, 0xE22u)) {
-        p.issue_words(ring_u + r.slot * C::kStage, &bars->full[r.slot], k0, k1, n++);
-        r.next<C::kStages>();
-      }
-      return n;
-    };
-    bool met = false;
+    each_stretch(up, (int)blockIdx.x, [&](int s, int u0, int u1) {
+      Producer<Mode::kN, C::kTok> p;
+      p.w = up_weights(s);
+      const int seg = up.seg_of(s), p0 = sh->seg_first[seg];
+      p.rows(a.X, a.ldx, sh->seg_n[seg], [&](int t) { return sh->pair[p0 + t] / a.top_k; });
+      p.template run<C::kStages>(pos, ring_u, bars, u0 * 128, min(u1 * 128, hidden), a.max_polls, st);
+    });
+    // the first words of the down product do not wait for H
     int ahead = 0;
-    for (int s = dn_first; s < dn_end && ok; ++s) {
-      const int u0 = down.first_unit(s, blockIdx.x), u1 = down.first_unit(s, blockIdx.x + 1);
-      if (u0 >= u1) {
-        if (u0 < down.len) break;
-        continue;
-      }
+    bool met = false;
+    const auto meet = [&] {
+      met = true;
+      ok = grid_barrier(a.barrier + 1, &sh->flag, st, a.max_polls, 0xE11u);
+      if (V == 1 && ok) asm volatile("bar.sync 2, 288;" ::: "memory");  // H of this block's ranges is there
+    };
+    each_stretch(down, (int)blockIdx.x, [&](int s, int u0, int u1) {
       Producer<Mode::kN, C::kTok> p;
       p.w = down_weights(s);
-      const int seg = down.seg_of(s), p0 = sh->seg_first[seg], n = sh->seg_n[seg], pairs = a.T * a.top_k;
       const int k0 = u0 * 128, k1 = min(u1 * 128, inter);
-      ahead = V == 1 || !met ? words_ahead(p, k0, k1) : 0;
       if (!met) {
-        met = true;
-        ok = grid_barrier(a.barrier + 1, &sh->flag, st, a.max_polls, 0xE11u);
-        if (!ok) break;
+        RingPos r = pos;
+        const int most = min(num_stages<Mode::kN>(k1 - k0), C::kStages);
+        while (ahead < most && ring_wait(bars, &bars->empty[r.slot], r.phase ^ 1u, a.max_polls, st, 0xE22u)) {
+          p.issue_words(ring_u + r.slot * C::kStage, &bars->full[r.slot], k0, k1, ahead++);
+          r.next<C::kStages>();
+        }
+        meet();
       }
-      if (V == 1) asm volatile("bar.sync 2, 288;" ::: "memory");  // H of this range is there
+      if (!ok) return;
+      const int seg = down.seg_of(s), p0 = sh->seg_first[seg], n = sh->seg_n[seg], pairs = a.T * a.top_k;
       p.rows(a.H, inter, h_rows(n),
              [&](int t) { return t < n ? sh->pair[p0 + t] : pairs + sh->pair[p0 + t - n]; });
       p.template run<C::kStages>(pos, ring_u, bars, k0, k1, a.max_polls, st, ahead);
       ahead = 0;
-    }
-    if (!met) ok = grid_barrier(a.barrier + 1, &sh->flag, st, a.max_polls, 0xE11u);
+    });
+    if (!met) meet();
     for (int i = 0; i < ahead; ++i) pos.next<C::kStages>();
     if (!ok || *reinterpret_cast<volatile int *>(&bars->abort)) ring_drain(bars, pos);
   } else {
@@ -548,12 +546,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<V>::kBlocks)
     const auto slot = [&](int64_t b, int which) { return a.partial + (b * 2 + which) * C::kTok * kTile; };
     const auto dn_slot = [&](int64_t b, int which) { return a.dn_partial + (b * 2 + which) * C::kTok * kTile; };
 
-    for (int s = up_first; s < up_end; ++s) {
-      const int u0 = up.first_unit(s, blockIdx.x), u1 = up.first_unit(s, blockIdx.x + 1);
-      if (u0 >= u1) {
-        if (u0 < up.len) break;
-        continue;
-      }
+    each_stretch(up, (int)blockIdx.x, [&](int s, int u0, int u1) {
       const int seg = up.seg_of(s), tile = up.tile_of(s), p0 = sh->seg_first[seg], n = sh->seg_n[seg];
       const int ch = (tile >> 1) * kTile, cols = min(kTile, inter - ch);  // the tile's channels
       const bool whole = u0 == 0 && u1 == up.len;
@@ -562,98 +555,91 @@ __global__ void __launch_bounds__(kThreads, Cfg<V>::kBlocks)
       sums(n, u0 * 128, min(u1 * 128, hidden), cols, [&](int t) {
         return whole ? gu + sh->pair[p0 + t] * pitch_gu : part + t * kTile;
       });
-    }
-    // four channels of H for row t of entry seg: the sums of the blocks that
-    // share gate's and up's tile, silu(g) u, and what its rounding leaves
-    const auto finish = [&](int sg, int t, int c) {
-      const int su = sg + 1, seg = up.seg_of(sg), ch = (up.tile_of(sg) >> 1) * kTile;
-      const int64_t row = sh->pair[sh->seg_first[seg] + t];
-      const auto gather = [&](int stretch, int64_t off) {
-        const int first = up.block_of(stretch, 0), last = up.block_of(stretch, up.len - 1);
-        if (first == last) return __ldcg(reinterpret_cast<const float4 *>(a.sums + row * pitch_gu + off + ch + c));
-        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        for (int b = first; b <= last; ++b) {  // all but the first block enter inside the tile
-          const float4 p = __ldcg(reinterpret_cast<const float4 *>(slot(b, b == first) + t * kTile + c));
-          v.x += p.x;
-          v.y += p.y;
-          v.z += p.z;
-          v.w += p.w;
-        }
-        return v;
-      };
-      const float4 gv = gather(sg, 0), uv = gather(su, a.inter);
-      const float h[4] = {silu_mul(gv.x, uv.x), silu_mul(gv.y, uv.y), silu_mul(gv.z, uv.z), silu_mul(gv.w, uv.w)};
-      __align__(8) __half hi[4], rest[4];
+    });
+    // H of entry seg, channels [c0, c1) of one pair of tiles: the sums of the blocks
+    // that share gate's and up's tile, silu(g) u, and what its rounding leaves
+    const auto finish = [&](int seg, int c0, int c1) {
+      const int ch = c0 / kTile * kTile, sg = seg * up.tiles + 2 * (c0 / kTile);
+      const int n = sh->seg_n[seg], p0 = sh->seg_first[seg], quads = (c1 - c0) / 4;
+      const bool rest_too = h_rows(n) > n;
+      const int2 gb = up.blocks(sg), ub = up.blocks(sg + 1);
+      for (int i = tid; i < n * quads; i += kConsumers) {
+        const int t = i / quads, c = c0 + 4 * (i - t * quads);
+        const int64_t row = sh->pair[p0 + t];
+        const auto gather = [&](int2 b, int64_t off) {
+          if (b.x == b.y) return __ldcg(reinterpret_cast<const float4 *>(a.sums + row * pitch_gu + off + c));
+          float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          for (int k = b.x; k <= b.y; ++k) {  // all but the first block enter inside the tile
+            const float4 p = __ldcg(reinterpret_cast<const float4 *>(slot(k, k == b.x) + t * kTile + c - ch));
+            v.x += p.x;
+            v.y += p.y;
+            v.z += p.z;
+            v.w += p.w;
+          }
+          return v;
+        };
+        const float4 gv = gather(gb, 0), uv = gather(ub, a.inter);
+        const float h[4] = {silu_mul(gv.x, uv.x), silu_mul(gv.y, uv.y), silu_mul(gv.z, uv.z), silu_mul(gv.w, uv.w)};
+        __align__(8) __half hi[4], rest[4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        hi[k] = __float2half_rn(h[k]);
-        rest[k] = __float2half_rn(isfinite(h[k]) ? h[k] - __half2float(hi[k]) : 0.0f);
+        for (int k = 0; k < 4; ++k) {
+          hi[k] = __float2half_rn(h[k]);
+          rest[k] = __float2half_rn(isfinite(h[k]) ? h[k] - __half2float(hi[k]) : 0.0f);
+        }
+        __half *d = a.H + row * inter + c;
+        *reinterpret_cast<uint2 *>(d) = *reinterpret_cast<const uint2 *>(hi);
+        if (rest_too) *reinterpret_cast<uint2 *>(d + (int64_t)a.T * a.top_k * inter) = *reinterpret_cast<const uint2 *>(rest);
       }
-      __half *d = a.H + row * inter + ch + c;
-      *reinterpret_cast<uint2 *>(d) = *reinterpret_cast<const uint2 *>(hi);
-      if (h_rows(sh->seg_n[seg]) > sh->seg_n[seg])
-        *reinterpret_cast<uint2 *>(d + (int64_t)a.T * a.top_k * inter) = *reinterpret_cast<const uint2 *>(rest);
     };
-    if (V != 1) {
+    if (V != 1 && up.stretches) {
       // the last block to arrive at a pair of tiles finishes it
       __threadfence();
       consumer_sync();
-      for (int base = up_first; base < up_end; base += kConsumers) {
+      for (int base = up.first_of((int)blockIdx.x);; base += kConsumers) {
         const int s = base + tid;
-        bool mine = false, more = false;
-        if (s < up_end) {
-          const int u0 = up.first_unit(s, blockIdx.x), u1 = up.first_unit(s, blockIdx.x + 1);
-          mine = u0 < u1;
-          more = mine || u0 >= up.len;
-        }
+        int u0 = 0, u1 = 0;
+        if (s < up.stretches) up.units(s, (int)blockIdx.x, u0, u1);
+        const bool more = s < up.stretches && (u0 < u1 || u0 >= up.len);
         int last = 0;
-        if (mine) {
-          const int sg = s - (up.tile_of(s) & 1), su = sg + 1;
-          const int arrivals = up.block_of(sg, up.len - 1) - up.block_of(sg, 0) + up.block_of(su, up.len - 1) -
-                               up.block_of(su, 0) + 2;
-          last = atomicAdd(a.tile_count + sg / 2, 1) == arrivals - 1;
+        if (u0 < u1) {
+          const int sg = s - (up.tile_of(s) & 1);
+          const int2 gb = up.blocks(sg), ub = up.blocks(sg + 1);
+          last = atomicAdd(a.tile_count + sg / 2, 1) == gb.y - gb.x + ub.y - ub.x + 1;
         }
         sh->last[tid] = (uint8_t)last;
         const int run = consumer_count(more);  // stretches before the block's end, from `base`
         __threadfence();
         for (int j = 0; j < run; ++j) {
           if (!sh->last[j]) continue;
-          const int sg = base + j - (up.tile_of(base + j) & 1), n = sh->seg_n[up.seg_of(sg)];
-          const int quads = min(kTile, inter - (up.tile_of(sg) >> 1) * kTile) / 4;
-          for (int i = tid; i < n * quads; i += kConsumers) finish(sg, i / quads, 4 * (i % quads));
+          const int c0 = (up.tile_of(base + j) >> 1) * kTile;
+          finish(up.seg_of(base + j), c0, min(c0 + kTile, inter));
         }
         consumer_sync();
         if (run < kConsumers) break;
       }
     }
     ok = grid_barrier(a.barrier + 1, &sh->flag, st, a.max_polls, 0xE11u);
-    if (ok) {
-      for (int s = dn_first; s < dn_end; ++s) {
-        const int u0 = down.first_unit(s, blockIdx.x), u1 = down.first_unit(s, blockIdx.x + 1);
-        if (u0 >= u1) {
-          if (u0 < down.len) break;
-          continue;
-        }
+    if (V == 1 && ok) {
+      // the block makes the H it reads: other blocks may write the same values
+      each_stretch(down, (int)blockIdx.x, [&](int s, int u0, int u1) {
+        const int end = min(u1 * 128, inter);
+        for (int c = u0 * 128; c < end; c = c / kTile * kTile + kTile)
+          finish(down.seg_of(s), c, min(c / kTile * kTile + kTile, end));
+      });
+      asm volatile("bar.sync 2, 288;" ::: "memory");  // the producer waits for it
+    }
+    if (ok)
+      each_stretch(down, (int)blockIdx.x, [&](int s, int u0, int u1) {
         const int seg = down.seg_of(s), ch = down.tile_of(s) * kTile, p0 = sh->seg_first[seg], n = sh->seg_n[seg];
         const bool whole = u0 == 0 && u1 == down.len;
         float *part = dn_slot(blockIdx.x, u0 == 0);
         const int rows = h_rows(n), pairs = a.T * a.top_k;
-        if (V == 1) {
-          // the block makes the H it reads: other blocks may write the same values
-          const int k0 = u0 * 128, quads = (min(u1 * 128, inter) - k0) / 4;
-          for (int i = tid; i < n * quads; i += kConsumers) {
-            const int c = k0 + 4 * (i % quads);
-            finish(seg * up.tiles + 2 * (c / kTile), i / quads, c % kTile);
-          }
-          asm volatile("bar.sync 2, 288;" ::: "memory");  // the producer waits for it
-        }
         sums(rows, u0 * 128, min(u1 * 128, inter), min(kTile, hidden - ch), [&](int t) {
           // the remainders' sums have rows of their own
           return whole ? a.dn_sums + (int64_t)(t < n ? sh->pair[p0 + t] : pairs + sh->pair[p0 + t - n]) * hidden + ch
                        : part + t * kTile;
         });
-      }
-    }
+      });
   }
   if (!ok) return;
   if (!grid_barrier(a.barrier + 2, &sh->flag, st, a.max_polls, 0xE12u)) return;
@@ -680,7 +666,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<V>::kBlocks)
         seg = lo;
       }
       const int stretch = tile * down.n_seg + seg, n = sh->seg_n[seg], row = at - sh->seg_first[seg];
-      const int b0 = down.block_of(stretch, 0), b1 = down.block_of(stretch, down.len - 1);
+      const int2 db = down.blocks(stretch);
       const bool two = h_rows(n) > n;
       float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
       const auto add = [&](const float *src) {
@@ -690,12 +676,12 @@ __global__ void __launch_bounds__(kThreads, Cfg<V>::kBlocks)
         v.z += x.z;
         v.w += x.w;
       };
-      if (b0 == b1) {
+      if (db.x == db.y) {
         add(a.dn_sums + (int64_t)p * hidden + o);
         if (two) add(a.dn_sums + (int64_t)(a.T * a.top_k + p) * hidden + o);
       } else {
-        for (int b = b0; b <= b1; ++b) {
-          const float *src = a.dn_partial + ((int64_t)b * 2 + (b == b0)) * C::kTok * kTile + row * kTile + o - tile * kTile;
+        for (int b = db.x; b <= db.y; ++b) {
+          const float *src = a.dn_partial + ((int64_t)b * 2 + (b == db.x)) * C::kTok * kTile + row * kTile + o - tile * kTile;
           add(src);
           if (two) add(src + n * kTile);
         }
