@@ -990,10 +990,10 @@ awq_status awq_w4a16_moe(const void *X, int64_t T, int64_t hidden, int64_t ldx, 
   MoeArgs a = {static_cast<const __half *>(X), ldx, mask, static_cast<const __half *>(router),
                gu_qweight, gu_qzeros, static_cast<const __half *>(gu_scales),
                dn_qweight, dn_qzeros, static_cast<const __half *>(dn_scales),
-               (int)T, n_experts, top_k, cfg->group_size, renormalize, hidden, inter, l.max_seg,
+               (int)T, n_experts, top_k, cfg->group_size, renormalize, hidden, inter,
                static_cast<__half *>(Y), ldy, ids, weights,
                static_cast<DevStatus *>(ws), reinterpret_cast<uint32_t *>(b + 64),
-               reinterpret_cast<int *>(b + 256), reinterpret_cast<double *>(b + l.logits), reinterpret_cast<int *>(b + l.tile_count),
+               reinterpret_cast<int *>(b + 256), reinterpret_cast<double *>(b + l.logits),
                reinterpret_cast<__half *>(b + l.H), reinterpret_cast<float *>(b + l.sums),
                reinterpret_cast<float *>(b + l.dn_sums), reinterpret_cast<float *>(b + l.partial),
                reinterpret_cast<float *>(b + l.dn_partial), poll_cap()};

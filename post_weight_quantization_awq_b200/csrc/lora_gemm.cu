@@ -128,9 +128,8 @@ __global__ void __launch_bounds__(kThreads, MINB)
   const int k0 = (int)(units * rank / splits * unit);
   const int k1 = (int)i64min(units * (rank + 1) / splits * unit, a.in);
   if (tid >= kConsumers) {
-    Producer<M, MAXTOK> p;
-    p.w = Weights{&map, 0, a.qzeros, a.scales, a.out / 8, group_shift(a.group),
-                  (int)(tile * 32), (int)(a.out / 8), (int)(tile * 32), (int)(a.out / 8)};
+    Producer<M, MAXTOK> p(Weights{&map, 0, a.qzeros, a.scales, a.out / 8, group_shift(a.group),
+                  (int)(tile * 32), (int)(a.out / 8), (int)(tile * 32), (int)(a.out / 8)});
     p.rows(a.X + t0 * a.ldx, a.ldx, n, [](int t) { return t; });
     RingPos pos;
     if (FUSED) {

@@ -15,9 +15,12 @@
 //            pieces of rows read HBM at 4.6-5.0 TB/s, 256-byte ones at 6.1-6.6),
 //            gate's and up's of one expert in turn, in units of 128 input rows.
 //            The units are dealt out evenly by cost and in order; fp32 sums go
-//            to L2, and the last block to finish a pair of tiles adds them in
-//            block order and applies silu(g) u.  While the blocks meet, the
-//            producer warps load the first words of the next phase;
+//            to L2.  While the blocks meet, the producer warps load the first
+//            words of the next phase;
+//   H        silu(g) u from the sums of the blocks that share a tile, added in
+//            block order: each block makes what its down units read, or, where
+//            that would be made too many times over, all blocks make all of it
+//            between two barriers;
 //   down     the same over hidden's tiles and all met experts;
 //   combine  a token's experts' sums, weighted with p in fp32, one rounding.
 // Sums are added in an order fixed by the sizes and the routing alone.
@@ -53,6 +56,8 @@ struct Cfg {
 // Where every block computes all logits itself: so many of them, from so many
 // router values (64 KB from L2 in about the time of a barrier).
 constexpr int kAloneLogits = 32, kAloneRouter = 32768;
+constexpr int64_t kOwnH = 2 << 20;
+constexpr int kPieceH = 128;  // channels of H made at a time; divides a tile
 
 template <int V>
 struct MoeLists {
@@ -64,7 +69,6 @@ struct MoeLists {
   int16_t seg_expert[C::kSegs], seg_first[C::kSegs], seg_n[C::kSegs];
   int seg_cost[C::kSegs + 1];  // cost of a unit, summed over the entries before
   double logit[kAloneLogits];
-  uint8_t last[kConsumers];
   int n_seg;
   int flag;
 };
@@ -441,9 +445,6 @@ __global__ void __launch_bounds__(kThreads, Cfg<V>::kBlocks)
                }
              });
   } else {
-    // counters of the pairs of gate|up tiles
-    for (int64_t i = blockIdx.x * (int64_t)kThreads + tid; i < a.max_seg * itiles; i += (int64_t)gridDim.x * kThreads)
-      a.tile_count[i] = 0;
     router(a);
     if (!grid_barrier(a.barrier + 0, &sh->flag, st, a.max_polls, 0xE10u)) return;
   }
@@ -466,14 +467,16 @@ __global__ void __launch_bounds__(kThreads, Cfg<V>::kBlocks)
     const int64_t groups = (int64_t)e * (inter / a.group);
     return Weights{&dn_map, e * inter, a.dn_z + groups * wh, a.dn_s + groups * hidden, wh, shift, c0, wh, c0 + 32, wh};
   };
+  // values of H, each made once for every tile of down, up to which that costs
+  // less than a barrier (1.8 us)
+  const bool own_h = (int64_t)a.T * a.top_k * inter * htiles <= kOwnH;
   bool ok = true;
 
   if (tid >= kConsumers) {
     // ------------------------------------------------------------ producer
     RingPos pos;
     each_stretch(up, (int)blockIdx.x, [&](int s, int u0, int u1) {
-      Producer<Mode::kN, C::kTok> p;
-      p.w = up_weights(s);
+      Producer<Mode::kN, C::kTok> p(up_weights(s));
       const int seg = up.seg_of(s), p0 = sh->seg_first[seg];
       p.rows(a.X, a.ldx, sh->seg_n[seg], [&](int t) { return sh->pair[p0 + t] / a.top_k; });
       p.template run<C::kStages>(pos, ring_u, bars, u0 * 128, min(u1 * 128, hidden), a.max_polls, st);
@@ -484,11 +487,13 @@ __global__ void __launch_bounds__(kThreads, Cfg<V>::kBlocks)
     const auto meet = [&] {
       met = true;
       ok = grid_barrier(a.barrier + 1, &sh->flag, st, a.max_polls, 0xE11u);
-      if (V == 1 && ok) asm volatile("bar.sync 2, 288;" ::: "memory");  // H of this block's ranges is there
+      if (ok && own_h)
+        asm volatile("bar.sync 2, 288;" ::: "memory");  // H of this block's ranges is there
+      else if (ok)
+        ok = grid_barrier(a.barrier + 2, &sh->flag, st, a.max_polls, 0xE13u);
     };
     each_stretch(down, (int)blockIdx.x, [&](int s, int u0, int u1) {
-      Producer<Mode::kN, C::kTok> p;
-      p.w = down_weights(s);
+      Producer<Mode::kN, C::kTok> p(down_weights(s));
       const int k0 = u0 * 128, k1 = min(u1 * 128, inter);
       if (!met) {
         RingPos r = pos;
@@ -591,42 +596,21 @@ __global__ void __launch_bounds__(kThreads, Cfg<V>::kBlocks)
         if (rest_too) *reinterpret_cast<uint2 *>(d + (int64_t)a.T * a.top_k * inter) = *reinterpret_cast<const uint2 *>(rest);
       }
     };
-    if (V != 1 && up.stretches) {
-      // the last block to arrive at a pair of tiles finishes it
-      __threadfence();
-      consumer_sync();
-      for (int base = up.first_of((int)blockIdx.x);; base += kConsumers) {
-        const int s = base + tid;
-        int u0 = 0, u1 = 0;
-        if (s < up.stretches) up.units(s, (int)blockIdx.x, u0, u1);
-        const bool more = s < up.stretches && (u0 < u1 || u0 >= up.len);
-        int last = 0;
-        if (u0 < u1) {
-          const int sg = s - (up.tile_of(s) & 1);
-          const int2 gb = up.blocks(sg), ub = up.blocks(sg + 1);
-          last = atomicAdd(a.tile_count + sg / 2, 1) == gb.y - gb.x + ub.y - ub.x + 1;
-        }
-        sh->last[tid] = (uint8_t)last;
-        const int run = consumer_count(more);  // stretches before the block's end, from `base`
-        __threadfence();
-        for (int j = 0; j < run; ++j) {
-          if (!sh->last[j]) continue;
-          const int c0 = (up.tile_of(base + j) >> 1) * kTile;
-          finish(up.seg_of(base + j), c0, min(c0 + kTile, inter));
-        }
-        consumer_sync();
-        if (run < kConsumers) break;
-      }
-    }
     ok = grid_barrier(a.barrier + 1, &sh->flag, st, a.max_polls, 0xE11u);
-    if (V == 1 && ok) {
-      // the block makes the H it reads: other blocks may write the same values
+    if (ok && own_h) {  // other blocks may write the same values
       each_stretch(down, (int)blockIdx.x, [&](int s, int u0, int u1) {
         const int end = min(u1 * 128, inter);
         for (int c = u0 * 128; c < end; c = c / kTile * kTile + kTile)
           finish(down.seg_of(s), c, min(c / kTile * kTile + kTile, end));
       });
       asm volatile("bar.sync 2, 288;" ::: "memory");  // the producer waits for it
+    } else if (ok) {
+      const int pieces = (inter + kPieceH - 1) / kPieceH;
+      for (int i = blockIdx.x; i < up.n_seg * pieces; i += gridDim.x) {
+        const int c = i % pieces * kPieceH;
+        finish(i / pieces, c, min(c + kPieceH, inter));
+      }
+      ok = grid_barrier(a.barrier + 2, &sh->flag, st, a.max_polls, 0xE13u);
     }
     if (ok)
       each_stretch(down, (int)blockIdx.x, [&](int s, int u0, int u1) {
@@ -642,7 +626,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<V>::kBlocks)
       });
   }
   if (!ok) return;
-  if (!grid_barrier(a.barrier + 2, &sh->flag, st, a.max_polls, 0xE12u)) return;
+  if (!grid_barrier(a.barrier + 3, &sh->flag, st, a.max_polls, 0xE12u)) return;
 
   // ---------------------------------------------------------------- combine
   const int quads = hidden / 4;
@@ -731,13 +715,10 @@ cudaError_t launch_moe(const MoeArgs &a, int num_sms, cudaStream_t stream) {
 MoeLayout moe_layout(int64_t T, int64_t hidden, int64_t inter, int64_t experts, int64_t top_k, int num_sms) {
   MoeLayout l;
   const int64_t pairs = T * top_k;
-  l.max_seg = (experts < pairs ? experts : pairs) + pairs / kCap + 1;
   auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
   size_t off = 512;
   l.logits = off;
   off = up(off + sizeof(double) * (size_t)(T * experts));
-  l.tile_count = off;
-  off = up(off + sizeof(int) * (size_t)(l.max_seg * ((inter + kTile - 1) / kTile)));
   l.H = off;  // and the remainders
   off = up(off + 2 * sizeof(__half) * (size_t)(pairs * inter));
   l.sums = off;  // whole tiles' sums: gate|up, and down (the remainders' apart)

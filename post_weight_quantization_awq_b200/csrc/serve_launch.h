@@ -70,25 +70,23 @@ struct MoeArgs {
   const int32_t *dn_q, *dn_z;
   const __half *dn_s;
   int T, experts, top_k, group, renormalize;
-  int64_t hidden, inter, max_seg;
+  int64_t hidden, inter;
   __half *Y;
   int64_t ldy;
   int32_t *ids;
   float *weights;
   // workspace
   DevStatus *st;           // 512 bytes cleared by the launch: status word,
-  uint32_t *barrier;       // 3 counters,
+  uint32_t *barrier;       // 4 counters,
   int *tok_count;          // [T] logits written
   double *logits;
-  int *tile_count;
   __half *H;
   float *sums, *dn_sums;        // [pairs, 2 inter]; [2 pairs, hidden]
   float *partial, *dn_partial;  // [blocks, 2, rows, 512] each
   uint32_t max_polls;
 };
 struct MoeLayout {
-  size_t logits, tile_count, H, sums, dn_sums, partial, dn_partial, end;
-  int64_t max_seg;
+  size_t logits, H, sums, dn_sums, partial, dn_partial, end;
 };
 __host__ __device__ constexpr int64_t i64max_(int64_t a, int64_t b) { return a > b ? a : b; }
 MoeLayout moe_layout(int64_t T, int64_t hidden, int64_t inter, int64_t experts, int64_t top_k, int num_sms);

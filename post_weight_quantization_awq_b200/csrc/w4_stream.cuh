@@ -79,15 +79,6 @@ __device__ __forceinline__ void tma_load_2d_at(uint32_t dst, const CUtensorMap *
 }
 
 __device__ __forceinline__ void consumer_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
-__device__ __forceinline__ int consumer_count(bool v) {
-  uint32_t r;
-  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.popc.u32 %0, 1, 256, p;\n\t}"
-               : "=r"(r)
-               : "r"((uint32_t)v)
-               : "memory");
-  return (int)r;
-}
-
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                          uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -200,9 +191,34 @@ __device__ __forceinline__ int num_stages(int rows) {  // rows a multiple of 64
 template <Mode M, int MAXTOK>
 struct Producer {
   static constexpr int kX = (MAXTOK + 3) / 4;  // token rows of a lane
-  Weights w;
-  int n;
+  int n, shift, row0, x0, x1;                   // x0, x1: the boxes' columns in the words' tensor map
+  const CUtensorMap *map;
+  // this lane's chunk of either box's steps, and (lanes 0..7, 8..15) of their zero
+  // words, in group 0; bytes between groups
+  const char *sc[2], *zp;
+  uint32_t sc_row, zp_row, zp_at;
+  bool sc_ok[2], zp_ok, box1;
   const char *x[kX];  // 16-byte chunk lane % 8 of rows lane / 8 + 4 j
+
+  __device__ __forceinline__ explicit Producer(const Weights &w) {
+    const int lane = threadIdx.x & 31;
+    map = w.map;
+    row0 = w.row0;
+    shift = w.shift;
+    x0 = w.col0 * 2;
+    x1 = w.col1 * 2;
+    box1 = w.col1 < w.end1;
+    sc_row = (uint32_t)w.words * 16u;
+    zp_row = (uint32_t)w.words * 4u;
+    sc_ok[0] = w.col0 + lane < w.end0;
+    sc_ok[1] = w.col1 + lane < w.end1;
+    sc[0] = reinterpret_cast<const char *>(w.scales) + (sc_ok[0] ? (w.col0 + lane) * 16ll : 0ll);
+    sc[1] = reinterpret_cast<const char *>(w.scales) + (sc_ok[1] ? (w.col1 + lane) * 16ll : 0ll);
+    const int zc = (lane < 8 ? w.col0 : w.col1) + 4 * (lane & 7);
+    zp_ok = zc < (lane < 8 ? w.end0 : w.end1);
+    zp = reinterpret_cast<const char *>(w.qzeros) + (zp_ok ? zc * 4ll : 0ll);
+    zp_at = sz_offset<M, MAXTOK>() + (lane < 8 ? 0u : 2 * kSz) + 512u + (lane & 7) * 16u;
+  }
 
   template <class RowOf>
   __device__ __forceinline__ void rows(const __half *base, int64_t ld, int count, RowOf row) {
@@ -218,26 +234,26 @@ struct Producer {
   // Words, steps and zero words of stage s (and the stage's byte count).
   __device__ __forceinline__ void issue_words(uint32_t st, uint64_t *bar, int k0, int k1, int s) const {
     const int lane = threadIdx.x & 31;
-    const int kb[2] = {box_row<M>(k0, s, 0), box_row<M>(k0, s, 1)};
-    const bool ok[2] = {kb[0] < k1, kb[1] < k1 && w.col1 < w.end1};
-    if (lane == 0) mbar_arrive_expect_tx(bar, (ok[0] ? kBoxBytes : 0u) + (ok[1] ? kBoxBytes : 0u));
+    const int kb0 = box_row<M>(k0, s, 0), kb1 = box_row<M>(k0, s, 1);
+    const bool ok1 = kb1 < k1 && box1;  // kb0 is in the range: a stage has its first box
+    if (lane == 0) {
+      mbar_arrive_expect_tx(bar, ok1 ? 2 * kBoxBytes : kBoxBytes);
+      tma_load_2d_at(st, map, bar, x0, row0 + kb0);
+      if (ok1) tma_load_2d_at(st + kBoxBytes, map, bar, x1, row0 + kb1);
+    }
     __syncwarp();
-    if (lane == 0 && ok[0]) tma_load_2d_at(st, w.map, bar, w.col0 * 2, w.row0 + kb[0]);
-    if (lane == 1 && ok[1]) tma_load_2d_at(st + kBoxBytes, w.map, bar, w.col1 * 2, w.row0 + kb[1]);
-#pragma unroll
-    for (int b = 0; b < 2; ++b) {
-      if (!ok[b] || (w.shift == 7 && (kb[b] & 64))) continue;  // a group of 128: with its first box
-      const int col = b ? w.col1 : w.col0, end = b ? w.end1 : w.end0;
-      for (int gi = 0; gi < (w.shift == 5 ? 2 : 1); ++gi) {
-        const int64_t first = (int64_t)((kb[b] + 32 * gi) >> w.shift) * w.words;
-        const uint32_t d = st + sz_offset<M, MAXTOK>() + (b * 2 + gi) * kSz;
-        const bool in = col + lane < end;  // a word column's 8 steps
-        cp16(d + lane * 16, w.scales + (first + (in ? col + lane : 0)) * 8, in);
-        if (lane < 8) {
-          const bool zin = col + 4 * lane < end;
-          cp16(d + 512 + lane * 16, w.qzeros + first + (zin ? col + 4 * lane : 0), zin);
-        }
-      }
+    const uint32_t d = st + sz_offset<M, MAXTOK>() + lane * 16;
+    const bool first0 = shift != 7 || !(kb0 & 64), first1 = ok1 && (shift != 7 || !(kb1 & 64));
+    // a group of 128 comes with its first box
+    const uint32_t g0 = (uint32_t)kb0 >> shift, g1 = (uint32_t)kb1 >> shift;
+    if (first0) cp16(d, sc[0] + (uint64_t)g0 * sc_row, sc_ok[0]);
+    if (first1) cp16(d + 2 * kSz, sc[1] + (uint64_t)g1 * sc_row, sc_ok[1]);
+    if (lane < 16 && (lane < 8 ? first0 : first1)) cp16(st + zp_at, zp + (uint64_t)(lane < 8 ? g0 : g1) * zp_row, zp_ok);
+    if (shift == 5) {  // and the second groups of 32
+      cp16(d + kSz, sc[0] + (uint64_t)(g0 + 1) * sc_row, sc_ok[0]);
+      if (ok1) cp16(d + 3 * kSz, sc[1] + (uint64_t)(g1 + 1) * sc_row, sc_ok[1]);
+      if (lane < 16 && (lane < 8 || ok1))
+        cp16(st + zp_at + kSz, zp + (uint64_t)((lane < 8 ? g0 : g1) + 1) * zp_row, zp_ok);
     }
   }
 
