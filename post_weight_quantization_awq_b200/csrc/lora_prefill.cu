@@ -4,9 +4,10 @@
 //   Y = X Wd^T + sum over the tile's adapters a of mask_a(U) B_a^T,
 //   Wd = RN16((q - z) scale),  U[t] = RN16( c_a (x_t A_a^T) ),  a = ids[t]
 //
-// Two launches.  lora_prepare_kernel: some blocks dequantise W once (in x out
-// work instead of once per token tile), the others compute U and, for every
-// token tile of the product, the list of the adapters its rows carry.
+// Three launches.  lora_shrink_mma_kernel computes U and, for every token tile of
+// the product, the list of the adapters its rows carry; beside it (programmatic
+// dependent launch) lora_dequant_kernel dequantises W once, in x out work instead
+// of once per token tile.
 // lora_gemm_kernel: the low-rank part is K steps like any other, appended to a
 // tile's K loop for each adapter on its list: A is U's rows, of which the
 // waiting epilogue warps zero those of other adapters in shared memory, B is
@@ -25,9 +26,10 @@ namespace {
 // ---------------------------------------------------------------------------
 // Preparation
 // ---------------------------------------------------------------------------
-constexpr int kShT = 32;   // tokens of a shrink block
-constexpr int kShR = 32;   // rank rows of a pass
-constexpr int kShWarps = 8;
+constexpr int kShT = 16;      // tokens of a shrink block
+constexpr int kShR = 32;      // rank rows of a pass
+constexpr int kShWarps = 16;
+constexpr int kShThreads = kShWarps * 32;
 
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                          uint32_t b0, uint32_t b1) {
@@ -36,15 +38,15 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// The different adapters of n ids (shared memory), in order of appearance, into
-// list; returns how many.  All 256 threads.
+// The different adapters of n <= 256 ids (shared memory), in order of appearance,
+// into list; returns how many.  All threads of the block.
 __device__ int adapter_list(const int *ids, int n, int *list, int *scratch) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int id = tid < n ? ids[tid] : -1;
   bool first = id >= 0;
   for (int s = 0; s < tid && first; ++s) first = ids[s] != id;
   const uint32_t b = __ballot_sync(0xffffffffu, first);
-  if (lane == 0) scratch[warp] = __popc(b);
+  if (lane == 0 && warp < 8) scratch[warp] = __popc(b);
   __syncthreads();
   int at = 0, total = 0;
   for (int w = 0; w < 8; ++w) {
@@ -56,109 +58,130 @@ __device__ int adapter_list(const int *ids, int n, int *list, int *scratch) {
   return total;
 }
 
-// U of 32 tokens: for each adapter among them, X (32 rows) times A_a^T on
-// mma.sync, the 8 warps taking eighths of K.  A lane loads 16 bytes of a row: the
-// 8 columns 8q .. 8q + 7 of a 32-column step are its fragments of two MMAs, the
-// order of k inside a step being free as long as both operands agree.
+// 8 NX rank rows of one adapter: X (16 rows) times A_a^T on mma.sync over this
+// warp's steps of 32 columns, the loads of four steps in flight together.  A lane
+// loads 16 bytes of a row: the 8 columns 8q .. 8q + 7 of a step are its fragments of
+// two MMAs, the order of k inside a step being free as long as both operands agree.
+template <int NX>
+__device__ __forceinline__ void shrink_pass(float (&acc)[4][4], const __half *x0, const __half *x1, const __half *ar,
+                                            int64_t in, int s0, int s1) {
+  for (int s = s0; s < s1; s += 4) {
+    uint4 xa[4], xb[4], av[4][NX];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (s + i < s1) {
+        xa[i] = __ldg(reinterpret_cast<const uint4 *>(x0 + 32 * (s + i)));
+        xb[i] = __ldg(reinterpret_cast<const uint4 *>(x1 + 32 * (s + i)));
+#pragma unroll
+        for (int x = 0; x < NX; ++x) av[i][x] = __ldg(reinterpret_cast<const uint4 *>(ar + 8 * x * in + 32 * (s + i)));
+      } else {
+        xa[i] = xb[i] = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+        for (int x = 0; x < NX; ++x) av[i][x] = make_uint4(0u, 0u, 0u, 0u);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int x = 0; x < NX; ++x) {
+        mma16816(acc[x], xa[i].x, xb[i].x, xa[i].y, xb[i].y, av[i][x].x, av[i][x].y);
+        mma16816(acc[x], xa[i].z, xb[i].z, xa[i].w, xb[i].w, av[i][x].z, av[i][x].w);
+      }
+  }
+}
+
+// U of 16 tokens for each adapter among them.  `split` of the 16 warps share an
+// adapter's K, so that each has at least four steps of it, and the others take
+// other adapters.
 __device__ void shrink_block(const LoraArgs &a, int64_t t0, uint8_t *smem) {
-  float *red = reinterpret_cast<float *>(smem);                          // [8][32][kShR + 1]
-  int *ids = reinterpret_cast<int *>(smem + kShWarps * kShT * (kShR + 1) * 4);  // [32], list [32], scratch [8]
+  float *red = reinterpret_cast<float *>(smem);  // [16][16][kShR + 1]
+  int *ids = reinterpret_cast<int *>(smem + kShWarps * kShT * (kShR + 1) * 4);
   int *list = ids + 256, *scratch = list + 256;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, q = lane & 3;
   const int n = (int)i64min(kShT, a.T - t0);
-  if (tid < 256) {
+  if (tid < kShT) {
     const int id = tid < n ? a.ids[t0 + tid] : -1;
     ids[tid] = id >= 0 && id < a.adapters ? id : -1;
     if (id < -1 || id >= a.adapters) dev_fail(a.st, kDevBadAdapter, 0xE02u);
   }
   __syncthreads();
   const int count = adapter_list(ids, n, list, scratch);
-  const int steps = (int)(a.in / 32), s0 = steps * warp / kShWarps, s1 = steps * (warp + 1) / kShWarps;
-  const __half *xr[4];  // rows g, g + 8, g + 16, g + 24 (the last one again past the end)
-#pragma unroll
-  for (int i = 0; i < 4; ++i) xr[i] = a.X + (t0 + min(g + 8 * i, n - 1)) * a.ldx + 8 * q;
-  for (int j = 0; j < count; ++j) {
-    const int id = list[j];
-    for (int r0 = 0; r0 < a.rank; r0 += kShR) {
-      float acc[2][4][4];
-#pragma unroll
-      for (int m = 0; m < 2; ++m)
-#pragma unroll
-        for (int x = 0; x < 4; ++x)
-#pragma unroll
-          for (int c = 0; c < 4; ++c) acc[m][x][c] = 0.0f;
-      const __half *ar = a.A + ((int64_t)id * a.rank + r0 + g) * a.in + 8 * q;
-#pragma unroll 4
-      for (int s = s0; s < s1; ++s) {
-        uint4 xv[4], av[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) xv[i] = __ldg(reinterpret_cast<const uint4 *>(xr[i] + 32 * s));
+  const int steps = (int)(a.in / 32);
+  int split = kShWarps;
+  while (split > 1 && split * 4 > steps) split /= 2;
+  const int teams = kShWarps / split, team = warp / split, part = warp - team * split;
+  const int s0 = steps * part / split, s1 = steps * (part + 1) / split;
+  // rows g and g + 8 (the last one again past the end)
+  const __half *x0 = a.X + (t0 + min(g, n - 1)) * a.ldx + 8 * q, *x1 = a.X + (t0 + min(g + 8, n - 1)) * a.ldx + 8 * q;
+  for (int j0 = 0; j0 < count; j0 += teams) {
+    const bool works = j0 + team < count;
+    for (int r0 = 0, rows; r0 < a.rank; r0 += rows) {
+      const int left = a.rank - r0;
+      rows = left >= 32 ? 32 : left >= 16 ? 16 : 8;
+      if (works) {
+        float acc[4][4];
 #pragma unroll
         for (int x = 0; x < 4; ++x)
-          av[x] = r0 + 8 * x < a.rank ? __ldg(reinterpret_cast<const uint4 *>(ar + (int64_t)8 * x * a.in + 32 * s))
-                                      : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
-        for (int m = 0; m < 2; ++m)
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            mma16816(acc[m][x], xv[2 * m].x, xv[2 * m + 1].x, xv[2 * m].y, xv[2 * m + 1].y, av[x].x, av[x].y);
-            mma16816(acc[m][x], xv[2 * m].z, xv[2 * m + 1].z, xv[2 * m].w, xv[2 * m + 1].w, av[x].z, av[x].w);
-          }
-      }
-#pragma unroll
-      for (int m = 0; m < 2; ++m)
+          for (int c = 0; c < 4; ++c) acc[x][c] = 0.0f;
+        const __half *ar = a.A + ((int64_t)list[j0 + team] * a.rank + r0 + g) * a.in + 8 * q;
+        if (rows == 32)
+          shrink_pass<4>(acc, x0, x1, ar, a.in, s0, s1);
+        else if (rows == 16)
+          shrink_pass<2>(acc, x0, x1, ar, a.in, s0, s1);
+        else
+          shrink_pass<1>(acc, x0, x1, ar, a.in, s0, s1);
 #pragma unroll
         for (int x = 0; x < 4; ++x)
 #pragma unroll
           for (int c = 0; c < 4; ++c)
-            red[(warp * kShT + 16 * m + g + 8 * (c >> 1)) * (kShR + 1) + 8 * x + 2 * q + (c & 1)] = acc[m][x][c];
+            red[(warp * kShT + g + 8 * (c >> 1)) * (kShR + 1) + 8 * x + 2 * q + (c & 1)] = acc[x][c];
+      }
       __syncthreads();
-      for (int i = tid; i < kShT * kShR; i += 256) {
-        const int t = i / kShR, r = i % kShR;
-        if (t < n && ids[t] == id && r0 + r < a.rank) {
-          float v = 0.0f;
-#pragma unroll
-          for (int w = 0; w < kShWarps; ++w) v += red[(w * kShT + t) * (kShR + 1) + r];
-          reinterpret_cast<__half *>(a.U)[(t0 + t) * a.rank + r0 + r] = __float2half_rn(a.c[id] * v);
-        }
+      for (int i = tid; i < min(teams, count - j0) * kShT * rows; i += kShThreads) {
+        const int m = i / (kShT * rows), t = i / rows % kShT, r = i % rows, id = list[j0 + m];
+        if (t >= n || ids[t] != id) continue;
+        float v = 0.0f;
+        for (int w = 0; w < split; ++w) v += red[((m * split + w) * kShT + t) * (kShR + 1) + r];
+        reinterpret_cast<__half *>(a.U)[(t0 + t) * a.rank + r0 + r] = __float2half_rn(a.c[id] * v);
       }
       __syncthreads();
     }
   }
 }
 
-constexpr int kPrepSmem = kShWarps * kShT * (kShR + 1) * 4 + (256 + 256 + 16) * 4;
+constexpr int kShrinkSmem = kShWarps * kShT * (kShR + 1) * 4 + (256 + 256 + 16) * 4;
 
-// Blocks [0, n_shrink): U; [n_shrink, n_shrink + n_lists): the lists of `bm`-row
-// tiles, lists[tile][bm + 1] = count, ids; the rest: one dequantised tile each.
-__global__ void __launch_bounds__(256) lora_prepare_kernel(const LoraArgs a, int n_shrink, int n_lists, int bm,
-                                                           int *lists, __half *Wd) {
-  __shared__ __align__(16) uint8_t smem[kPrepSmem];
+// Blocks [0, n_shrink): U; the rest: the lists of `bm`-row tiles,
+// lists[tile][bm + 1] = count, ids.
+__global__ void __launch_bounds__(kShThreads) lora_shrink_mma_kernel(const LoraArgs a, int n_shrink, int bm, int *lists) {
+  __shared__ __align__(16) uint8_t smem[kShrinkSmem];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   int64_t b = blockIdx.x;
   if (b < n_shrink) {
     shrink_block(a, b * kShT, smem);
     return;
   }
   b -= n_shrink;
-  if (b < n_lists) {
-    int *ids = reinterpret_cast<int *>(smem), *list = ids + 256, *scratch = list + 256;
-    const int64_t t0 = b * bm;
-    const int n = (int)i64min(bm, a.T - t0), tid = threadIdx.x;
-    const int id = tid < n ? a.ids[t0 + tid] : -1;
-    ids[tid] = id >= 0 && id < a.adapters ? id : -1;
-    __syncthreads();
-    const int count = adapter_list(ids, n, list, scratch);
-    int *dst = lists + b * (bm + 1);
-    if (tid == 0) dst[0] = count;
-    if (tid < count) dst[1 + tid] = list[tid];
-    return;
-  }
-  b -= n_lists;
-  const int64_t tiles_o = (a.out + kDeqOut - 1) / kDeqOut;
-  dequant_tile(reinterpret_cast<__half *>(smem), a.qweight, a.qzeros, a.scales, a.in, a.out, a.group,
-               b % tiles_o * kDeqOut, b / tiles_o * kDeqIn, Wd);
+  int *ids = reinterpret_cast<int *>(smem), *list = ids + 256, *scratch = list + 256;
+  const int64_t t0 = b * bm;
+  const int n = (int)i64min(bm, a.T - t0), tid = threadIdx.x;
+  const int id = tid < n ? a.ids[t0 + tid] : -1;
+  if (tid < 256) ids[tid] = id >= 0 && id < a.adapters ? id : -1;
+  __syncthreads();
+  const int count = adapter_list(ids, n, list, scratch);
+  int *dst = lists + b * (bm + 1);
+  if (tid == 0) dst[0] = count;
+  if (tid < count) dst[1 + tid] = list[tid];
 }
-static_assert(kPrepSmem >= kDeqIn * kDeqOut * 2, "dequantised tile");
+
+__global__ void __launch_bounds__(256) lora_dequant_kernel(const LoraArgs a, __half *Wd) {
+  __shared__ __align__(16) __half tile[kWideIn * kWideOut];
+  const int64_t tiles_o = (a.out + kWideOut - 1) / kWideOut, b = blockIdx.x;
+  dequant_wide(tile, a.qweight, a.qzeros, a.scales, a.in, a.out, a.group, b % tiles_o * kWideOut,
+               b / tiles_o * kWideIn, Wd);
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // its end is the shrink product's too
+}
 
 // ---------------------------------------------------------------------------
 // Product.  One block per SM, persistent over BM x BN tiles: warp 0 TMA, warp 1
@@ -296,6 +319,7 @@ __global__ void __launch_bounds__(320, 1)
   } else if (warp == 1) {
     if (lane == 0) {
       uint32_t step = 0, fphase = 0, mphase = 0;  // phases per stage
+      constexpr uint32_t idesc = idesc_f16_f32(128, BN);
       int it = 0;
       bool ok = true, issued = false;
       for (int tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x, ++it) {
@@ -333,7 +357,7 @@ __global__ void __launch_bounds__(320, 1)
             const uint64_t bd = smem_desc_k_sw128(sb + kk * 32);
 #pragma unroll
             for (int h = 0; h < C::kMT; ++h)
-              tc_mma_f16(d + h * BN, smem_desc_k_sw128(sa + h * 128 * PK * 2 + kk * 32), bd, idesc_f16_f32(128, BN),
+              tc_mma_f16(d + h * BN, smem_desc_k_sw128(sa + h * 128 * PK * 2 + kk * 32), bd, idesc,
                          (k | kk) != 0 ? 1u : 0u);
           }
           issued = true;
@@ -471,11 +495,20 @@ cudaError_t launch_lora_prefill(const LoraArgs &a, int num_sms, cudaStream_t str
   cudaError_t e = cudaMemsetAsync(a.st, 0, sizeof(DevStatus), stream);
   if (e != cudaSuccess) return e;
   const int64_t n_shrink = (a.T + kShT - 1) / kShT, n_lists = (a.T + bm - 1) / bm;
-  const int64_t n_deq = ((a.out + kDeqOut - 1) / kDeqOut) * ((a.in + kDeqIn - 1) / kDeqIn);
-  if (n_shrink + n_lists + n_deq > INT32_MAX) return cudaErrorInvalidValue;
-  lora_prepare_kernel<<<(unsigned)(n_shrink + n_lists + n_deq), 256, 0, stream>>>(a, (int)n_shrink, (int)n_lists, bm,
-                                                                                  lists, Wd);
+  const int64_t n_deq = ((a.out + kWideOut - 1) / kWideOut) * (a.in / kWideIn);
+  if (n_shrink + n_lists > INT32_MAX || n_deq > INT32_MAX) return cudaErrorInvalidValue;
+  lora_shrink_mma_kernel<<<(unsigned)(n_shrink + n_lists), kShThreads, 0, stream>>>(a, (int)n_shrink, bm, lists);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)n_deq);
+  cfg.blockDim = dim3(256);
+  cfg.stream = stream;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  if ((e = cudaLaunchKernelEx(&cfg, lora_dequant_kernel, a, Wd)) != cudaSuccess) return e;
   return bm == 256 ? launch_product<256, 256>(a, lists, Wd, num_sms, stream)
                    : launch_product<128, 128>(a, lists, Wd, num_sms, stream);
 }

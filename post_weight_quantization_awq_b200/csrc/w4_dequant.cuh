@@ -101,5 +101,54 @@ __device__ __forceinline__ void dequant_tile(__half *tile, const int32_t *__rest
   }
 }
 
+// The same with 256-output tiles of 64 inputs: 128 bytes of a row of words and of a
+// row of weights at a time, which HBM reads and writes faster than 32 bytes.  The
+// 16-byte chunks of an output's 64 weights are XOR-swizzled by its word column, and
+// the 4-byte pairs inside a chunk by the column's upper bits, so that a warp's
+// writes (32 word columns, one input pair) fall in different banks.
+constexpr int kWideIn = 64, kWideOut = 256;
+
+__device__ __forceinline__ void dequant_wide(__half *tile, const int32_t *__restrict__ qweight,
+                                             const int32_t *__restrict__ qzeros, const __half *__restrict__ scales,
+                                             int64_t in, int64_t out, int group, int64_t o0, int64_t j0,
+                                             __half *__restrict__ Wd) {
+  const int64_t words = out / 8;
+  const int ow = threadIdx.x & 31, jw = threadIdx.x >> 5;  // word column; inputs 8 jw .. 8 jw + 7 (one group)
+  const int64_t wc = o0 / 8 + ow, j = j0 + 8 * jw;
+  uint32_t wv[8];
+  __half2 zp[4], sp[4];
+  const bool ok = wc < words && j < in;  // in % 64 == 0
+  if (ok) {
+    const int64_t gi = j / group;
+#pragma unroll
+    for (int r = 0; r < 8; ++r) wv[r] = (uint32_t)__ldg(qweight + (j + r) * words + wc);
+    nib_pairs((uint32_t)__ldg(qzeros + gi * words + wc), zp);
+    scale_pairs(__ldg(reinterpret_cast<const uint4 *>(scales + gi * out + 8 * wc)), sp);
+    uint32_t *t = reinterpret_cast<uint32_t *>(tile) + 8 * ow * (kWideIn / 2) + ((jw ^ (ow & 7)) << 2);
+#pragma unroll
+    for (int r = 0; r < 8; r += 2) {
+      const uint4 v0 = dequant_word(wv[r], zp, sp), v1 = dequant_word(wv[r + 1], zp, sp);
+      const uint32_t h0[4] = {v0.x, v0.y, v0.z, v0.w}, h1[4] = {v1.x, v1.y, v1.z, v1.w};
+      const int at = (r >> 1) ^ (ow >> 3);
+#pragma unroll
+      for (int p = 0; p < 4; ++p) {  // output p: low halves of the two rows; p + 4: the high halves
+        t[p * (kWideIn / 2) + at] = __byte_perm(h0[p], h1[p], 0x5410u);
+        t[(p + 4) * (kWideIn / 2) + at] = __byte_perm(h0[p], h1[p], 0x7632u);
+      }
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kWideOut * (kWideIn / 8) / 256; ++i) {
+    const int c = threadIdx.x + 256 * i, oo = c >> 3, jc = c & 7;  // output, 8-input chunk
+    const int64_t o = o0 + oo, jj = j0 + 8 * jc;
+    if (o >= out || jj >= in) continue;
+    const uint4 v = *reinterpret_cast<const uint4 *>(tile + oo * kWideIn + 8 * (jc ^ ((oo >> 3) & 7)));
+    const int x = oo >> 6;  // undo the pairs' swizzle: pair i lies at i ^ x
+    const uint32_t a = (x & 1) ? v.y : v.x, b = (x & 1) ? v.x : v.y, e = (x & 1) ? v.w : v.z, f = (x & 1) ? v.z : v.w;
+    *reinterpret_cast<uint4 *>(Wd + o * in + jj) = (x & 2) ? make_uint4(e, f, a, b) : make_uint4(a, b, e, f);
+  }
+}
+
 }  // namespace
 }  // namespace awq
