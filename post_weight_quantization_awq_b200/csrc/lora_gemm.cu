@@ -95,7 +95,7 @@ struct LoraShared {
   static constexpr uint32_t kRed = (MAXTOK * kRedPitch * 4 + 15) / 16 * 16;  // in the ring, after the product
   static constexpr int kUPitch = 2 * (256 + 8);                               // bytes of a token's hi (lo) row
   static constexpr uint32_t kU = 2 * MAXTOK * kUPitch;                        // behind it
-  static constexpr uint32_t kTail = sizeof(RingBars<STAGES>) + MAXTOK * 12 + 16 + 2 * kFusedU * 4;
+  static constexpr uint32_t kTail = sizeof(RingBars<STAGES>) + MAXTOK * 16 + 16 + 2 * kFusedU * 4;
   static constexpr uint32_t kBytes = 1024 + kRing + kTail;
   static_assert(kRed + kU <= kRing, "the sums and U reuse the ring");
 };
@@ -109,12 +109,16 @@ __global__ void __launch_bounds__(kThreads, MINB)
   float *red = reinterpret_cast<float *>(ring);
   uint8_t *uhl = ring + L::kRed;
   auto *bars = reinterpret_cast<RingBars<STAGES> *>(ring + L::kRing);
-  int *ids = reinterpret_cast<int *>(bars + 1);  // the tokens' adapters, -1: none
-  int *list = ids + MAXTOK;                      // the different ones
+  // the block's tokens stand in the order of their adapters, so that one's tokens
+  // fill whole token tiles
+  int *ids = reinterpret_cast<int *>(bars + 1);  // adapter of the token at a place, -1: none
+  int *perm = ids + MAXTOK;                      // its row of X
+  int *list = perm + MAXTOK;                     // the different adapters' first place | end << 16
   float *uscale = reinterpret_cast<float *>(list + MAXTOK);
   int *n_list = reinterpret_cast<int *>(uscale + MAXTOK);
   float *upart = reinterpret_cast<float *>(n_list + 4);  // FUSED: U over this block's rows, [token][rank row]
-  float *usum = upart + kFusedU;                         // and over all
+  float *usum = upart + kFusedU;                         // and over all (16-byte aligned, like all before it)
+  static_assert(sizeof(RingBars<STAGES>) % 16 == 0 && MAXTOK % 4 == 0 && kFusedU % 4 == 0, "alignment");
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = (int)(blockIdx.x % (unsigned)splits);
   const int64_t tile = blockIdx.x / (unsigned)splits;
@@ -130,13 +134,18 @@ __global__ void __launch_bounds__(kThreads, MINB)
   if (tid >= kConsumers) {
     Producer<M, MAXTOK> p(Weights{&map, 0, a.qzeros, a.scales, a.out / 8, group_shift(a.group),
                   (int)(tile * 32), (int)(a.out / 8), (int)(tile * 32), (int)(a.out / 8)});
-    p.rows(a.X + t0 * a.ldx, a.ldx, n, [](int t) { return t; });
     RingPos pos;
     if (FUSED) {
       if (blockIdx.x == 0 && lane == 0) *a.st = DevStatus{};
       __syncwarp();
     }
-    p.run(pos, smem_u32(ring), bars, k0, k1, a.max_polls, a.st);
+    // the first words do not wait for the tokens' order
+    const int ahead = min(num_stages<M>(max(k1 - k0, 0)), STAGES);
+    for (int s = 0; s < ahead; ++s)
+      p.issue_words(smem_u32(ring) + s * stage_bytes<M, MAXTOK>(), &bars->full[s], k0, k1, s);
+    asm volatile("bar.sync 2, 288;" ::: "memory");
+    p.rows(a.X + t0 * a.ldx, a.ldx, n, [&](int t) { return perm[t]; });
+    p.run(pos, smem_u32(ring), bars, k0, k1, a.max_polls, a.st, ahead);
     if (FUSED) {
       __syncwarp();
       cluster_arrive();
@@ -146,20 +155,33 @@ __global__ void __launch_bounds__(kThreads, MINB)
   } else {
     RingPos pos;
     Acc<NT> acc;
-    // the tokens' adapters, while the first words travel
+    // the tokens' order, while the first words travel
     for (int t = tid; t < MAXTOK; t += kConsumers) {
       const int id = t < n ? __ldg(a.ids + t0 + t) : -1;
-      ids[t] = id >= 0 && id < a.adapters ? id : -1;
+      list[t] = id >= 0 && id < a.adapters ? id : -1;
     }
     consumer_sync();
-    if (warp == 0) {  // the first token of each adapter lists it
+    if (tid < n) {
+      const int id = list[tid];
+      int at = 0;
+      for (int s = 0; s < n; ++s) at += list[s] < id || (list[s] == id && s < tid);
+      ids[at] = id;
+      perm[at] = tid;
+    } else if (tid < MAXTOK) {
+      ids[tid] = -1;
+    }
+    asm volatile("bar.sync 2, 288;" ::: "memory");
+    if (warp == 0) {
       int count = 0;
       for (int c = 0; c < n; c += 32) {
         const int t = c + lane, id = t < n ? ids[t] : -1;
-        bool first = id >= 0;
-        for (int s = 0; s < t && first; ++s) first = ids[s] != id;
+        const bool first = id >= 0 && (t == 0 || ids[t - 1] != id);
         const uint32_t b = __ballot_sync(0xffffffffu, first);
-        if (first) list[count + __popc(b & ((1u << lane) - 1u))] = id;
+        if (first) {
+          int end = t + 1;
+          while (end < n && ids[end] == id) ++end;
+          list[count + __popc(b & ((1u << lane) - 1u))] = t | end << 16;
+        }
         count += __popc(b);
       }
       if (lane == 0) *n_list = count;
@@ -168,7 +190,7 @@ __global__ void __launch_bounds__(kThreads, MINB)
       for (int i = warp; i < n * a.rank; i += kConsumers / 32) {
         const int t = i / a.rank, r = i - t * a.rank, id = ids[t];
         if (id < 0) continue;
-        const uint4 *x = reinterpret_cast<const uint4 *>(a.X + (t0 + t) * a.ldx);
+        const uint4 *x = reinterpret_cast<const uint4 *>(a.X + (t0 + perm[t]) * a.ldx);
         const uint4 *w = reinterpret_cast<const uint4 *>(a.A + ((int64_t)id * a.rank + r) * a.in);
         float s = 0.0f;
 #pragma unroll 2
@@ -194,25 +216,37 @@ __global__ void __launch_bounds__(kThreads, MINB)
     }
     consumer_sync();
     const int r32 = (a.rank + 31) / 32 * 32;
-    for (int t = warp; t < MAXTOK; t += kConsumers / 32) {
+    {  // a team of threads to a token, all tokens at once
+      constexpr int kTeam = MAXTOK <= 8 ? 32 : MAXTOK <= 16 ? 16 : MAXTOK <= 32 ? 8 : 4;
+      const int t = tid / kTeam, part = tid % kTeam;
       const bool on = t < n && ids[t] >= 0;
-      const float *u = FUSED ? usum + t * a.rank : a.U + (t0 + t) * a.rank;
+      const float4 *u = reinterpret_cast<const float4 *>(FUSED ? usum + t * a.rank : a.U + (t0 + (on ? perm[t] : 0)) * a.rank);
       float m = 0.0f;
-      for (int k = lane; on && k < a.rank; k += 32) m = fmaxf(m, fabsf(u[k]));
+#pragma unroll 4
+      for (int k = part; k < a.rank / 4; k += kTeam)
+        if (on) m = fmaxf(m, fmaxf(fmaxf(fabsf(u[k].x), fabsf(u[k].y)), fmaxf(fabsf(u[k].z), fabsf(u[k].w))));
 #pragma unroll
-      for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+      for (int d = kTeam / 2; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
       // 2^e with |u| / 2^e in [1, 2) at most; not for 0, infinities and the ends of the range
       const int e = (int)(__float_as_uint(m) >> 23) - 127;
       const bool scaled = e > -120 && e < 120;
       const float up = scaled ? __uint_as_float((uint32_t)(127 + e) << 23) : 1.0f;
       const float down = scaled ? __uint_as_float((uint32_t)(127 - e) << 23) : 1.0f;
-      if (lane == 0) uscale[t] = up;
-      for (int k = lane; k < r32; k += 32) {
-        const float v = on && k < a.rank ? u[k] * down : 0.0f;
-        const __half hi = __float2half_rn(v);
-        __half *d = reinterpret_cast<__half *>(uhl + t * L::kUPitch) + k;
-        *d = hi;
-        d[L::kU / 4] = __float2half_rn(isfinite(__half2float(hi)) ? v - __half2float(hi) : 0.0f);
+      if (t < MAXTOK) {
+        if (part == 0) uscale[t] = up;
+        __half2 *d = reinterpret_cast<__half2 *>(uhl + t * L::kUPitch);
+#pragma unroll 4
+        for (int k = part; k < r32 / 4; k += kTeam) {
+          const float4 v = on && 4 * k < a.rank ? u[k] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          const float w[4] = {v.x * down, v.y * down, v.z * down, v.w * down};
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const __half2 hi = __floats2half2_rn(w[2 * i], w[2 * i + 1]);
+            const float2 f = __half22float2(hi);
+            d[2 * k + i] = hi;
+            d[2 * k + i + L::kU / 8] = __floats2half2_rn(isfinite(f.x) ? w[2 * i] - f.x : 0.0f, isfinite(f.y) ? w[2 * i + 1] - f.y : 0.0f);
+          }
+        }
       }
     }
     consumer_sync();
@@ -224,7 +258,8 @@ __global__ void __launch_bounds__(kThreads, MINB)
     // its fragments of two MMAs
     const uint8_t *ul = uhl + (tt + g) * L::kUPitch + q * 16;
     for (int j = first; j < *n_list; j += step) {
-      const int id = list[j];
+      const int lo = list[j] & 0xffff, hi = list[j] >> 16, id = ids[lo];
+      if (hi <= tt || lo >= tt + 8 * NT) continue;  // none of this warp's tokens
 #pragma unroll
       for (int p = 0; p < 4; ++p)
 #pragma unroll
@@ -241,7 +276,8 @@ __global__ void __launch_bounds__(kThreads, MINB)
           af[o] = o_ok && k + 8 * q < a.rank ? __ldg(reinterpret_cast<const uint4 *>(bp + (int64_t)o * a.rank + k))
                                              : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
-        for (int x = 0; x < NT; ++x)
+        for (int x = 0; x < NT; ++x) {
+          if (hi <= tt + 8 * x || lo >= tt + 8 * x + 8) continue;
 #pragma unroll
           for (int h = 0; h < 2; ++h) {  // hi, lo
             const uint4 b = *reinterpret_cast<const uint4 *>(ul + h * (L::kU / 2) + x * 8 * L::kUPitch + k * 2);
@@ -251,13 +287,14 @@ __global__ void __launch_bounds__(kThreads, MINB)
               mma16816(acc.grp[p][x], af[p].z, af[p + 4].z, af[p].w, af[p + 4].w, b.z, b.w);
             }
           }
+        }
       }
 #pragma unroll
       for (int x = 0; x < NT; ++x)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const int t = tt + x * 8 + 2 * q + e;
-          if (ids[t] != id) continue;
+          if (t < lo || t >= hi) continue;
           const float sc = uscale[t];
 #pragma unroll
           for (int p = 0; p < 4; ++p)
@@ -286,7 +323,7 @@ __global__ void __launch_bounds__(kThreads, MINB)
       s0 += p[0];
       s1 += p[1];
     }
-    *reinterpret_cast<__half2 *>(a.Y + (t0 + t) * a.ldy + o) = __floats2half2_rn(s0, s1);
+    *reinterpret_cast<__half2 *>(a.Y + (t0 + perm[t]) * a.ldy + o) = __floats2half2_rn(s0, s1);
   }
   cluster.sync();  // no block leaves while its sums are read
 }

@@ -101,7 +101,7 @@ __device__ __forceinline__ uint32_t sub2(uint32_t a, uint32_t b) {
 
 // The barriers of a ring and whether a wait ran out.
 template <int STAGES>
-struct __align__(8) RingBars {
+struct __align__(16) RingBars {
   uint64_t full[STAGES], empty[STAGES];
   int abort;
 };
