@@ -370,7 +370,7 @@ size_t awq_w4a16_workspace_size(int64_t T, int64_t in, int64_t out, const awq_co
  *   U[t][r] = sum_j X[t][j] A_a[r][j],  W[o][j] = (q - z) scale,  a = adapter[t];
  * a token whose adapter is -1 gets the first sum alone.  Rows may carry their
  * adapters in any order.
- *   X, qweight, qzeros, scales, Y, cfg  as in awq_w4a16_gemm
+ *   X, qweight, qzeros, scales, Y, cfg  as in awq_w4a16_gemm; Y is not X
  *   A        device fp16 [n_adapters, rank, in]
  *   B        device fp16 [n_adapters, out, rank] (an adapter of lower rank is
  *            padded with zeros)

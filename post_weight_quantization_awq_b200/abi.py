@@ -331,16 +331,46 @@ def awq_w4a16_workspace_size(T: int, inn: int, out: int, cfg: AwqConfig) -> int:
     return int(n)
 
 
+def _refuse(func: str, what) -> None:
+    """Refuses a serving call for the first of its tensors that is on another device
+    than the current one or is not laid out as the call reads it; each of `what` is
+    (name, tensor or None, dtype or None for any, whether its rows may be strided)."""
+    import torch
+    dev = torch._C._cuda_getDevice()
+    for name, t, dtype, strided in what:
+        if t is None:
+            continue
+        if t.get_device() != dev:
+            raise AwqError(func, 1, f"{name} is on {t.device}, the current device is cuda:{dev}")
+        if dtype is not None and t.dtype is not dtype:
+            raise AwqError(func, 1, f"{name} is {t.dtype}, {dtype} is needed")
+        if not (t.stride(-1) == 1 if strided else t.is_contiguous()):
+            raise AwqError(func, 1, f"{name} has strides {t.stride()}: its rows must be contiguous"
+                           if strided else f"{name} must be contiguous")
+
+
 def awq_w4a16_lora_gemm(X, qweight, qzeros, scales, cfg: AwqConfig, A, B, c, adapter, Y, ws,
                         stream=None) -> None:
     """Y [T, out] fp16 = X times the packed weights, plus for each token its
     adapter's c_a (X A_a^T) B_a^T: A fp16 [n, rank, in], B fp16 [n, out, rank],
     c fp32 [n], adapter int32 [T] (-1: none)."""
-    n, rank, _ = A.shape
+    import torch
+    f16, i32 = torch.float16, torch.int32
+    T, inn = X.shape
+    n, rank, a_in = A.shape
+    out = Y.shape[1]
+    _refuse("awq_w4a16_lora_gemm", (
+        ("X", X, f16, True), ("qweight", qweight, i32, False), ("qzeros", qzeros, i32, False),
+        ("scales", scales, f16, False), ("A", A, f16, False), ("B", B, f16, False),
+        ("c", c, torch.float32, False), ("adapter", adapter, i32, False), ("Y", Y, f16, True),
+        ("ws", ws, None, False)))
+    if (a_in != inn or B.shape != (n, out, rank) or c.shape != (n,) or adapter.shape != (T,) or Y.shape[0] != T
+            or qweight.shape != (inn, out // 8) or scales.shape[1] != out):
+        raise AwqError("awq_w4a16_lora_gemm", 1, "the shapes of X, the packed weights, A, B, c, adapter and Y disagree")
     _check("awq_w4a16_lora_gemm", LIB.awq_w4a16_lora_gemm(
-        _ptr(X), X.shape[0], X.shape[1], X.stride(0), _ptr(qweight), _ptr(qzeros), _ptr(scales),
-        Y.shape[1], ctypes.byref(cfg), _ptr(A), _ptr(B), _ptr(c), n, rank, _ptr(adapter), _ptr(Y),
-        Y.stride(0), _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)))
+        X.data_ptr(), T, inn, X.stride(0), qweight.data_ptr(), qzeros.data_ptr(), scales.data_ptr(),
+        out, ctypes.byref(cfg), A.data_ptr(), B.data_ptr(), c.data_ptr(), n, rank, adapter.data_ptr(),
+        Y.data_ptr(), Y.stride(0), ws.data_ptr(), ws.numel() * ws.element_size(), _stream(stream)))
 
 
 def awq_w4a16_lora_workspace_size(T: int, inn: int, out: int, rank: int, cfg: AwqConfig) -> int:
@@ -356,12 +386,26 @@ def awq_w4a16_moe(X, router, gate_up, down, cfg: AwqConfig, renormalize: bool, m
     fp16 [E, hidden], gate_up and down (qweight, qzeros, scales) with a leading
     expert axis, mask uint8 [T] or None; outputs Y [T, hidden] fp16, ids int32
     and weights fp32 [T, top_k]."""
+    import torch
+    f16, i32 = torch.float16, torch.int32
     gq, gz, gs = gate_up
     dq, dz, ds = down
+    T, hidden = X.shape
+    E, inter, top_k = router.shape[0], dq.shape[1], ids.shape[1]
+    _refuse("awq_w4a16_moe", (
+        ("X", X, f16, True), ("router", router, f16, False), ("gate_up qweight", gq, i32, False),
+        ("gate_up qzeros", gz, i32, False), ("gate_up scales", gs, f16, False), ("down qweight", dq, i32, False),
+        ("down qzeros", dz, i32, False), ("down scales", ds, f16, False), ("mask", mask, torch.uint8, False),
+        ("Y", Y, f16, True), ("ids", ids, i32, False), ("weights", weights, torch.float32, False),
+        ("ws", ws, None, False)))
+    if (router.shape[1] != hidden or gq.shape != (E, hidden, inter // 4) or dq.shape != (E, inter, hidden // 8)
+            or gs.shape[2] != 2 * inter or ds.shape[2] != hidden or Y.shape != (T, hidden) or ids.shape[0] != T
+            or weights.shape != (T, top_k) or (mask is not None and mask.shape != (T,))):
+        raise AwqError("awq_w4a16_moe", 1, "the shapes of X, router, the experts and the outputs disagree")
     _check("awq_w4a16_moe", LIB.awq_w4a16_moe(
-        _ptr(X), X.shape[0], X.shape[1], X.stride(0), _ptr(mask), _ptr(router), router.shape[0], ids.shape[1],
-        1 if renormalize else 0, _ptr(gq), _ptr(gz), _ptr(gs), dq.shape[1], _ptr(dq), _ptr(dz), _ptr(ds),
-        ctypes.byref(cfg), _ptr(Y), Y.stride(0), _ptr(ids), _ptr(weights), _ptr(ws),
+        X.data_ptr(), T, hidden, X.stride(0), _ptr(mask), router.data_ptr(), E, top_k, 1 if renormalize else 0,
+        gq.data_ptr(), gz.data_ptr(), gs.data_ptr(), inter, dq.data_ptr(), dz.data_ptr(), ds.data_ptr(),
+        ctypes.byref(cfg), Y.data_ptr(), Y.stride(0), ids.data_ptr(), weights.data_ptr(), ws.data_ptr(),
         ws.numel() * ws.element_size(), _stream(stream)))
 
 
@@ -377,12 +421,21 @@ def awq_block_norm(R, V, post, gate, c: float, pre, eps: float, R_out, N_out, st
     """R_out = R + c gate rmsnorm(V) post and N_out = rmsnorm(R_out) pre over
     fp16 rows [T, d]; V, post, gate ([T, d] or [d]), pre and one of the outputs
     may be None."""
+    import torch
+    f16 = torch.float16
     T, d = R.shape
+    _refuse("awq_block_norm", (
+        ("R", R, f16, True), ("V", V, f16, True), ("post", post, f16, False), ("gate", gate, f16, True),
+        ("pre", pre, f16, False), ("R_out", R_out, f16, True), ("N_out", N_out, f16, True)))
+    ldg = gate.stride(0) if gate is not None and gate.dim() == 2 else 0
+    if any(t is not None and t.shape != (T, d) for t in (V, R_out, N_out)) or any(
+            t is not None and t.shape != (d,) for t in (post, pre)) or (
+            gate is not None and gate.shape != ((T, d) if gate.dim() == 2 else (d,))):
+        raise AwqError("awq_block_norm", 1, "the shapes of R, V, post, gate, pre and the outputs disagree")
     _check("awq_block_norm", LIB.awq_block_norm(
-        _ptr(R), R.stride(0), _ptr(V), 0 if V is None else V.stride(0), T, d, _ptr(post), _ptr(gate),
-        gate.stride(0) if gate is not None and gate.dim() == 2 else 0, c, _ptr(pre), eps, _ptr(R_out),
-        0 if R_out is None else R_out.stride(0), _ptr(N_out), 0 if N_out is None else N_out.stride(0),
-        _stream(stream)))
+        R.data_ptr(), R.stride(0), _ptr(V), 0 if V is None else V.stride(0), T, d, _ptr(post), _ptr(gate), ldg,
+        c, _ptr(pre), eps, _ptr(R_out), 0 if R_out is None else R_out.stride(0), _ptr(N_out),
+        0 if N_out is None else N_out.stride(0), _stream(stream)))
 
 
 def awq_device_status(ws, stream=None) -> None:

@@ -908,6 +908,7 @@ awq_status awq_w4a16_lora_gemm(const void *X, int64_t T, int64_t in, int64_t ldx
   if (!c || !adapter || !aligned(c, 4) || !aligned(adapter, 4))
     return fail(AWQ_ERR_INVALID_ARG, "c and adapter must be non-NULL and 4-byte aligned");
   if (!Y || !aligned(Y, 16)) return fail(AWQ_ERR_INVALID_ARG, "Y is NULL or not 16-byte aligned");
+  if (Y == X) return fail(AWQ_ERR_INVALID_ARG, "Y and X are the same buffer");
   if (ldy < out || ldy % 8 != 0)
     return fail(AWQ_ERR_INVALID_ARG, "ldy=%lld must be >= out and a multiple of 8", (long long)ldy);
   if ((st = check_ws(ws, ws_bytes, lora_ws_bytes(T, in, out, rank))) != AWQ_OK) return st;

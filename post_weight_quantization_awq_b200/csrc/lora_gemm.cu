@@ -332,11 +332,12 @@ __global__ void __launch_bounds__(kThreads, MINB)
 // once: a second wave costs a whole pass (16 clusters of 8 blocks do not fit the
 // GPCs at one block per SM: 15.5 us for the last to start).
 template <class K>
-int cluster_size(K kernel, size_t smem, int64_t clusters, int64_t most, int (&fit)[64][9]) {
+int cluster_size(K kernel, size_t smem, int64_t clusters, int64_t most, std::atomic<int> (&fit)[64][9]) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 1;
   for (int s = (int)(most < 8 ? most : 8); s > 1; --s) {
-    if (!fit[dev][s]) {
+    int known = fit[dev][s];  // 0: not asked yet
+    if (!known) {
       cudaLaunchConfig_t cfg = {};
       cfg.gridDim = dim3((unsigned)s);
       cfg.blockDim = dim3(kThreads);
@@ -352,17 +353,17 @@ int cluster_size(K kernel, size_t smem, int64_t clusters, int64_t most, int (&fi
         (void)cudaGetLastError();
         n = 0;
       }
-      fit[dev][s] = n + 1;
+      fit[dev][s] = known = n + 1;
     }
-    if (fit[dev][s] - 1 >= clusters) return s;
+    if (known > clusters) return s;
   }
   return 1;
 }
 
 template <Mode M, int NT, int MAXTOK, int STAGES, int MINB, bool FUSED>
 cudaError_t launch_stream(const LoraArgs &a, int, cudaStream_t stream) {
-  static bool done[64];
-  static int fit[64][9];
+  static std::atomic<bool> done[64];
+  static std::atomic<int> fit[64][9];
   constexpr size_t kSmem = LoraShared<M, NT, MAXTOK, STAGES>::kBytes;
   static_assert(MINB * (kSmem + 1024) <= 233472, "resident blocks");
   auto kernel = lora_stream_kernel<M, NT, MAXTOK, STAGES, MINB, FUSED>;

@@ -457,7 +457,7 @@ __global__ void __launch_bounds__(320, 1)
 template <int BM, int BN>
 cudaError_t launch_product(const LoraArgs &a, const int *lists, const __half *Wd, int num_sms, cudaStream_t stream) {
   using C = PCfg<BM, BN>;
-  static bool done[64];
+  static std::atomic<bool> done[64];
   static_assert(sizeof(PTail<C::kStages>) <= 512 && C::kBytes <= 232448, "shared memory");
   cudaError_t e = allow_smem(lora_gemm_kernel<BM, BN>, C::kBytes, done);
   if (e != cudaSuccess) return e;

@@ -684,7 +684,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<V>::kBlocks)
 
 template <int V>
 cudaError_t go(const MoeArgs &a, int num_sms, cudaStream_t stream) {
-  static bool done[64];
+  static std::atomic<bool> done[64];
   cudaError_t e = allow_smem(moe_kernel<V>, moe_smem<V>(), done);
   if (e != cudaSuccess) return e;
   CUtensorMap gu, dn;  // the words of all experts as pairs of 16-bit values

@@ -6,6 +6,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "awq_device.cuh"
 
 namespace awq {
@@ -13,9 +15,10 @@ namespace awq {
 // DevStatus flag: an adapter id outside [-1, n_adapters) (beside awq_device.cuh's kDev* bits)
 constexpr uint32_t kDevBadAdapter = 1u << 4;
 
-// Sets a kernel's dynamic shared memory limit once per device.
+// Sets a kernel's dynamic shared memory limit once per device (two threads that
+// come first both set it).
 template <class K>
-inline cudaError_t allow_smem(K kernel, size_t bytes, bool (&done)[64]) {
+inline cudaError_t allow_smem(K kernel, size_t bytes, std::atomic<bool> (&done)[64]) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;

@@ -142,3 +142,34 @@ def test_norm_captured_and_on_another_stream():
     awq.awq_block_norm(r, v, *args, ro, no, stream=s.cuda_stream)
     s.synchronize()
     assert torch.equal(no, want)
+
+
+def test_norm_tensors_the_call_cannot_read_are_refused():
+    T, d = 3, 64
+    h = lambda *s: torch.zeros(s, dtype=torch.float16, device="cuda")  # noqa: E731
+    ok = dict(R=h(T, d), V=h(T, d), post=h(d), gate=h(d), pre=h(d), ro=h(T, d), no=h(T, d))
+    for name, bad in (("R", ok["R"].float()), ("R", ok["R"].cpu()), ("V", h(d, T).T), ("V", h(T, 128)),
+                      ("post", h(d + 8)), ("post", h(2 * d)[::2]), ("gate", h(T + 1, d)), ("gate", h(8)),
+                      ("pre", h(d).bfloat16()), ("ro", h(T + 1, d)), ("no", h(T, d).cpu())):
+        a = dict(ok, **{name: bad})
+        with pytest.raises(awq.AwqError) as e:
+            awq.awq_block_norm(a["R"], a["V"], a["post"], a["gate"], 1.0, a["pre"], 1e-6, a["ro"], a["no"])
+        assert e.value.status_name == "AWQ_ERR_INVALID_ARG", name
+
+
+def test_norm_rows_past_two_to_the_31():
+    """Rows whose values begin past 2^31 values of R and of the outputs."""
+    d = 32768
+    T = (1 << 31) // d + 3
+    R = torch.zeros((T, d), dtype=torch.float16, device="cuda")
+    rng = np.random.default_rng(2)
+    rows = [0, 65535, 65536, T - 1]
+    Rn = rng.standard_normal((len(rows), d)).astype(np.float16)
+    for r, v in zip(rows, Rn):
+        R[r] = _dev(v)
+    pre = rng.standard_normal(d).astype(np.float16)
+    no = torch.full((T, d), 3.0, dtype=torch.float16, device="cuda")
+    awq.awq_block_norm(R, None, None, None, 1.0, _dev(pre), 1e-6, None, no)
+    got = np.stack([no[r].cpu().numpy() for r in rows])
+    _check((None, got), Rn, None, None, None, 1.0, pre, 1e-6, d)
+    assert not bool(no[1].any())

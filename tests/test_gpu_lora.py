@@ -168,3 +168,90 @@ def test_lora_captured_and_replayed_with_new_inputs():
             got = Y.cpu().numpy()
             assert np.array_equal(got.view(np.uint16), _run(XX, packed, 128, A, B, c, ii).view(np.uint16))
         del g
+
+
+@pytest.mark.parametrize("T", [5, 100])
+def test_lora_two_at_once_with_a_workspace_each(T):
+    """The same weights and adapters, two batches, two streams, interleaved."""
+    X, packed, A, B, c, ids = _case(T, 1024, 544, 16, 4, 128, T)
+    X2, _, _, _, _, ids2 = _case(T, 1024, 544, 16, 4, 128, T + 1)
+    cfg = awq.AwqConfig.make()
+    d = lambda a: torch.from_numpy(np.ascontiguousarray(a)).cuda()  # noqa: E731
+    w, ad = [d(p) for p in packed], [d(A), d(B), d(c)]
+    calls, want = [], [_run(XX, packed, 128, A, B, c, ii) for XX, ii in ((X, ids), (X2, ids2))]
+    for XX, ii in ((X, ids), (X2, ids2)):
+        n = awq.awq_w4a16_lora_workspace_size(T, 1024, 544, 16, cfg)
+        calls.append((d(XX), d(ii), torch.zeros((T, 544), dtype=torch.float16, device="cuda"),
+                      torch.empty(n, dtype=torch.uint8, device="cuda"), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for x, i, Y, ws, s in calls:
+            awq.awq_w4a16_lora_gemm(x, *w, cfg, *ad, i, Y, ws, s.cuda_stream)
+    for (x, i, Y, ws, s), y in zip(calls, want):
+        awq.awq_device_status(ws, s.cuda_stream)
+        assert np.array_equal(Y.cpu().numpy().view(np.uint16), y.view(np.uint16))
+
+
+@pytest.mark.parametrize("T,rank", [(5, 8), (6, 64), (12, 16), (40, 64), (100, 16)])
+def test_lora_wait_that_runs_out_is_reported(monkeypatch, T, rank):
+    """Every bounded wait gives up after one poll; whether one does depends on how
+    soon the copies land, so the call either names the timeout or is right, and
+    the next call is right."""
+    X, packed, A, B, c, ids = _case(T, 4096, 1056, rank, 4, 128, T)
+    want = _run(X, packed, 128, A, B, c, ids)
+    monkeypatch.setenv("AWQ_FAULT", "timeout")
+    try:
+        got = _run(X, packed, 128, A, B, c, ids)
+        assert np.array_equal(got.view(np.uint16), want.view(np.uint16))
+    except awq.AwqError as e:
+        assert e.status_name == "AWQ_ERR_TIMEOUT"
+    monkeypatch.delenv("AWQ_FAULT")
+    assert np.array_equal(_run(X, packed, 128, A, B, c, ids).view(np.uint16), want.view(np.uint16))
+
+
+@pytest.mark.parametrize("T", [1, 40, 300])
+def test_lora_adapters_past_two_to_the_31(T):
+    """An adapter's rows that begin past 2^31 bytes, and past 2^31 values."""
+    n, rank, inn, out = 2100, 256, 4096, 64
+    rng = np.random.default_rng(T)
+    packed = random_packed(inn, out, 128, rng)
+    X = rng.standard_normal((T, inn)).astype(np.float16)
+    ids = np.array([0, 1, n // 2, n - 1, -1])[rng.integers(0, 5, T)].astype(np.int32)
+    ids[0] = n - 1
+    d = lambda a: torch.from_numpy(np.ascontiguousarray(a)).cuda()  # noqa: E731
+    A = torch.zeros((n, rank, inn), dtype=torch.float16, device="cuda")
+    B, c = np.zeros((n, out, rank), np.float16), np.ones(n, np.float32)
+    few = sorted(set(ids) - {-1})
+    An = {a: (rng.standard_normal((rank, inn)) / 64).astype(np.float16) for a in few}
+    for a in few:
+        A[a] = d(An[a])
+        B[a] = rng.standard_normal((out, rank)) * 0.1
+    cfg = awq.AwqConfig.make()
+    Y = torch.empty((T, out), dtype=torch.float16, device="cuda")
+    ws = torch.empty(awq.awq_w4a16_lora_workspace_size(T, inn, out, rank, cfg), dtype=torch.uint8, device="cuda")
+    awq.awq_w4a16_lora_gemm(d(X), *map(d, packed), cfg, A, d(B), d(c), d(ids), Y, ws)
+    awq.awq_device_status(ws)
+    short = np.array([few.index(a) if a >= 0 else -1 for a in ids])
+    Yo, mags = lora(X, packed, 128, np.stack([An[a] for a in few]), np.stack([B[a] for a in few]),
+                    np.ones(len(few)), short)
+    err = np.abs(Y.cpu().numpy().astype(np.float64) - Yo)
+    assert np.all(err <= lora_tolerance(Yo, mags, inn, rank, T > 64)), err.max()
+
+
+def test_lora_tensors_the_call_cannot_read_are_refused():
+    X, packed, A, B, c, ids = _case(4, 256, 96, 16, 3, 64, 1)
+    cfg = awq.AwqConfig.make(group_size=64)
+    d = lambda a: torch.from_numpy(np.ascontiguousarray(a)).cuda()  # noqa: E731
+    ok = dict(X=d(X), q=d(packed[0]), z=d(packed[1]), s=d(packed[2]), A=d(A), B=d(B), c=d(c), ids=d(ids),
+              Y=torch.full((4, 96), 7.0, dtype=torch.float16, device="cuda"),
+              ws=torch.empty(1 << 20, dtype=torch.uint8, device="cuda"))
+    for name, bad in (("X", ok["X"].double()), ("X", ok["X"].cpu()), ("X", d(X.T).T), ("q", ok["q"].T),
+                      ("q", ok["q"][:128]), ("s", ok["s"].float()), ("A", ok["A"].transpose(1, 2)),
+                      ("B", ok["B"][:2]), ("c", ok["c"].half()), ("ids", ok["ids"].long()), ("ids", ok["ids"][:3]),
+                      ("Y", ok["Y"][:3]), ("Y", ok["Y"].bfloat16()), ("ws", ok["ws"].cpu())):
+        a = dict(ok, **{name: bad})
+        with pytest.raises(awq.AwqError) as e:
+            awq.awq_w4a16_lora_gemm(a["X"], a["q"], a["z"], a["s"], cfg, a["A"], a["B"], a["c"], a["ids"], a["Y"],
+                                    a["ws"])
+        assert e.value.status_name == "AWQ_ERR_INVALID_ARG", name
+    assert bool((ok["Y"] == 7.0).all())

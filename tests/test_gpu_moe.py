@@ -72,7 +72,9 @@ def _check(got, X, router, gu, dn, group, k, ren, mask=None):
     (9, 256, 512, 6, 3, 64, True), (16, 576, 320, 3, 2, 32, False), (17, 512, 128, 16, 16, 128, True),
     (33, 384, 704, 2, 1, 64, True), (37, 1024, 256, 40, 4, 128, False), (64, 512, 384, 8, 2, 128, True),
     (64, 192, 64, 256, 8, 64, False), (64, 128, 128, 20, 16, 32, True), (7, 8192, 64, 4, 2, 64, True),
-    (4, 64, 8192, 4, 2, 64, True)])
+    (4, 64, 8192, 4, 2, 64, True),
+    # so many pairs, channels and tiles of hidden that every value of H is made once for all blocks
+    (8, 64, 16448, 16, 16, 64, True), (64, 576, 1088, 20, 16, 64, False), (64, 1088, 704, 18, 16, 32, True)])
 def test_moe_parity(T, hidden, inter, E, k, group, ren):
     X, router, gu, dn = _case(T, hidden, inter, E, group, T + hidden + E)
     got = _Layer(X, router, gu, dn, group, k, ren).run()
@@ -205,3 +207,35 @@ def test_moe_barrier_that_runs_out_is_reported(monkeypatch):
     monkeypatch.delenv("AWQ_FAULT")
     for p, q in zip(want, a.run()):
         assert np.array_equal(p, q)
+
+
+@pytest.mark.parametrize("T,hidden,inter,E,k", [(8, 64, 16448, 16, 16), (64, 576, 1088, 20, 16)])
+def test_moe_shared_h_timeout_is_reported(monkeypatch, T, hidden, inter, E, k):
+    """The same where H is made between two barriers."""
+    X, router, gu, dn = _case(T, hidden, inter, E, 64, 5)
+    a = _Layer(X, router, gu, dn, 64, k, True)
+    want = a.run()
+    monkeypatch.setenv("AWQ_FAULT", "timeout")
+    with pytest.raises(awq.AwqError) as e:
+        a.run()
+    assert e.value.status_name == "AWQ_ERR_TIMEOUT"
+    monkeypatch.delenv("AWQ_FAULT")
+    for p, q in zip(want, a.run()):
+        assert np.array_equal(p, q)
+
+
+def test_moe_tensors_the_call_cannot_read_are_refused():
+    X, router, gu, dn = _case(3, 128, 64, 4, 64, 9)
+    for change in (dict(x=_dev(X).float()), dict(x=_dev(X).T), dict(router=_dev(router).cpu()),
+                   dict(Y=torch.empty((3, 64), dtype=torch.float16, device="cuda")),
+                   dict(ids=torch.empty((3, 2), dtype=torch.int64, device="cuda")),
+                   dict(wt=torch.empty((2, 2), dtype=torch.float32, device="cuda")),
+                   dict(mask=torch.ones(3, dtype=torch.bool, device="cuda")),
+                   dict(ws=torch.empty(1 << 20, dtype=torch.uint8))):
+        a = _Layer(X, router, gu, dn, 64, 2, True)
+        for k, v in change.items():
+            setattr(a, k, v)
+        with pytest.raises(awq.AwqError) as e:
+            a.call()
+        assert e.value.status_name == "AWQ_ERR_INVALID_ARG", change
+        assert bool((a.Y == 7.0).all()) or "Y" in change

@@ -17,7 +17,7 @@ def _name(st):
 
 def _lora(cfg=CFG, **kw):
     a = dict(X=16, T=4, inn=512, ldx=512, qw=16, qz=16, sc=16, out=256, A=16, B=16, c=16, n=2, rank=16, ids=16,
-             Y=16, ldy=256, ws=256, nbytes=1 << 30)
+             Y=32, ldy=256, ws=256, nbytes=1 << 30)
     a.update(kw)
     return abi.LIB.awq_w4a16_lora_gemm(a["X"], a["T"], a["inn"], a["ldx"], a["qw"], a["qz"], a["sc"], a["out"],
                                        ctypes.byref(cfg), a["A"], a["B"], a["c"], a["n"], a["rank"], a["ids"],
@@ -35,6 +35,7 @@ def _lora(cfg=CFG, **kw):
     (dict(sc=None), "AWQ_ERR_INVALID_ARG"), (dict(A=None), "AWQ_ERR_INVALID_ARG"),
     (dict(B=24), "AWQ_ERR_INVALID_ARG"), (dict(c=None), "AWQ_ERR_INVALID_ARG"),
     (dict(ids=18), "AWQ_ERR_INVALID_ARG"), (dict(Y=None), "AWQ_ERR_INVALID_ARG"),
+    (dict(Y=16), "AWQ_ERR_INVALID_ARG"), (dict(n=65536, out=32768, ldy=32768), "AWQ_ERR_UNSUPPORTED"),
     (dict(n=0), "AWQ_ERR_INVALID_ARG"), (dict(n=65537), "AWQ_ERR_INVALID_ARG"),
     (dict(rank=0), "AWQ_ERR_INVALID_ARG"), (dict(rank=12), "AWQ_ERR_UNSUPPORTED"),
     (dict(rank=264), "AWQ_ERR_UNSUPPORTED"),
