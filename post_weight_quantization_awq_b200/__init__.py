@@ -1,6 +1,6 @@
 """AWQ per-layer activation-aware scale search on B200 (sm_100a).
 
-Public API: the C-ABI calls of include/awq.h under the same names
+Public API: the C-ABI calls of include/awq.h and awq_serving.h under the same names
 (``awq_act_stats``, ``awq_search_scale``, ``awq_search_clip``,
 ``awq_quant_pack``, ...) taking torch CUDA tensors, plus ``quantize_layer``,
 which runs the four calls for one linear (or one group of linears that share

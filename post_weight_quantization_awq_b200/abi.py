@@ -1,8 +1,9 @@
-"""ctypes binding of libawq.so (declared in include/awq.h).
+"""ctypes binding of libawq.so (declared in include/awq.h and awq_serving.h).
 
 Argument marshalling only: every function here passes device pointers,
 sizes and the current CUDA stream to the C ABI of the same name and raises
-AwqError on a non-zero status.  Every step of the search runs in the
+AwqError on a non-zero status; the serving calls also refuse tensors of another
+device, type or layout than they read.  Every step of the search runs in the
 library's sm_100a kernels; there is no fallback.  If the library is missing
 the import of this module fails with a message saying how to build it.
 """
@@ -21,6 +22,7 @@ PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG_DIR, "libawq_debug.so" if os.environ.get("AWQ_LIB") == "debug"
                         else "libawq.so")
 HEADER_PATH = os.path.join(os.path.dirname(PKG_DIR), "include", "awq.h")
+SERVING_HEADER_PATH = os.path.join(os.path.dirname(PKG_DIR), "include", "awq_serving.h")
 
 STATUS = {
     0: "AWQ_OK",
@@ -168,7 +170,7 @@ LIB = _Lib()
 
 
 def header_functions(path: str = HEADER_PATH):
-    """Names of the functions include/awq.h declares."""
+    """Names of the functions a header (include/awq.h) declares."""
     with open(path) as f:
         text = f.read()
     text = re.sub(r"/\*.*?\*/", "", text, flags=re.S)
@@ -331,22 +333,24 @@ def awq_w4a16_workspace_size(T: int, inn: int, out: int, cfg: AwqConfig) -> int:
     return int(n)
 
 
-def _refuse(func: str, what) -> None:
-    """Refuses a serving call for the first of its tensors that is on another device
-    than the current one or is not laid out as the call reads it; each of `what` is
-    (name, tensor or None, dtype or None for any, whether its rows may be strided)."""
-    import torch
-    dev = torch._C._cuda_getDevice()
-    for name, t, dtype, strided in what:
+def _refuse(func: str, dev: int, rows, dense) -> None:
+    """Names the tensor for which a serving call was refused: rows and dense are
+    (name, tensor or None, dtype, shape), the first with rows that may lie apart."""
+    for name, t, dtype, shape in rows + dense:
         if t is None:
             continue
         if t.get_device() != dev:
             raise AwqError(func, 1, f"{name} is on {t.device}, the current device is cuda:{dev}")
-        if dtype is not None and t.dtype is not dtype:
+        if t.dtype is not dtype:
             raise AwqError(func, 1, f"{name} is {t.dtype}, {dtype} is needed")
-        if not (t.stride(-1) == 1 if strided else t.is_contiguous()):
-            raise AwqError(func, 1, f"{name} has strides {t.stride()}: its rows must be contiguous"
-                           if strided else f"{name} must be contiguous")
+        if t.shape != shape:
+            raise AwqError(func, 1, f"{name} is {tuple(t.shape)}, {tuple(shape)} is needed")
+    for name, t, _, _ in rows:
+        if t is not None and t.stride(-1) != 1:
+            raise AwqError(func, 1, f"the values of a row of {name} must be contiguous")
+    for name, t, _, _ in dense:
+        if t is not None and not t.is_contiguous():
+            raise AwqError(func, 1, f"{name} must be contiguous")
 
 
 def awq_w4a16_lora_gemm(X, qweight, qzeros, scales, cfg: AwqConfig, A, B, c, adapter, Y, ws,
@@ -355,22 +359,31 @@ def awq_w4a16_lora_gemm(X, qweight, qzeros, scales, cfg: AwqConfig, A, B, c, ada
     adapter's c_a (X A_a^T) B_a^T: A fp16 [n, rank, in], B fp16 [n, out, rank],
     c fp32 [n], adapter int32 [T] (-1: none)."""
     import torch
-    f16, i32 = torch.float16, torch.int32
+    f16, i32, f32 = torch.float16, torch.int32, torch.float32
+    dev = torch._C._cuda_getDevice()
     T, inn = X.shape
-    n, rank, a_in = A.shape
-    out = Y.shape[1]
-    _refuse("awq_w4a16_lora_gemm", (
-        ("X", X, f16, True), ("qweight", qweight, i32, False), ("qzeros", qzeros, i32, False),
-        ("scales", scales, f16, False), ("A", A, f16, False), ("B", B, f16, False),
-        ("c", c, torch.float32, False), ("adapter", adapter, i32, False), ("Y", Y, f16, True),
-        ("ws", ws, None, False)))
-    if (a_in != inn or B.shape != (n, out, rank) or c.shape != (n,) or adapter.shape != (T,) or Y.shape[0] != T
-            or qweight.shape != (inn, out // 8) or scales.shape[1] != out):
-        raise AwqError("awq_w4a16_lora_gemm", 1, "the shapes of X, the packed weights, A, B, c, adapter and Y disagree")
+    n, rank, _ = A.shape
+    out, g = Y.shape[-1], cfg.group_size
+    xs, ys = X.stride(), Y.stride()
+    if not (dev == X.get_device() == qweight.get_device() == qzeros.get_device() == scales.get_device()
+            == A.get_device() == B.get_device() == c.get_device() == adapter.get_device() == Y.get_device()
+            == ws.get_device()
+            and f16 is X.dtype is scales.dtype is A.dtype is B.dtype is Y.dtype
+            and i32 is qweight.dtype is qzeros.dtype is adapter.dtype and c.dtype is f32
+            and xs[1] == 1 and ys[1] == 1 and qweight.is_contiguous() and qzeros.is_contiguous()
+            and scales.is_contiguous() and A.is_contiguous() and B.is_contiguous() and c.is_contiguous()
+            and adapter.is_contiguous() and A.numel() == n * rank * inn and B.numel() == n * out * rank
+            and c.numel() == n and adapter.numel() == T and Y.numel() == T * out
+            and qweight.numel() * 8 == inn * out and scales.numel() == inn // g * out
+            and qzeros.numel() == inn // g * (out // 8)):
+        _refuse("awq_w4a16_lora_gemm", dev, (("X", X, f16, (T, inn)), ("Y", Y, f16, (T, out))), (
+            ("qweight", qweight, i32, (inn, out // 8)), ("qzeros", qzeros, i32, (inn // g, out // 8)),
+            ("scales", scales, f16, (inn // g, out)), ("A", A, f16, (n, rank, inn)), ("B", B, f16, (n, out, rank)),
+            ("c", c, f32, (n,)), ("adapter", adapter, i32, (T,)), ("ws", ws, ws.dtype, ws.shape)))
     _check("awq_w4a16_lora_gemm", LIB.awq_w4a16_lora_gemm(
-        X.data_ptr(), T, inn, X.stride(0), qweight.data_ptr(), qzeros.data_ptr(), scales.data_ptr(),
+        X.data_ptr(), T, inn, xs[0], qweight.data_ptr(), qzeros.data_ptr(), scales.data_ptr(),
         out, ctypes.byref(cfg), A.data_ptr(), B.data_ptr(), c.data_ptr(), n, rank, adapter.data_ptr(),
-        Y.data_ptr(), Y.stride(0), ws.data_ptr(), ws.numel() * ws.element_size(), _stream(stream)))
+        Y.data_ptr(), ys[0], ws.data_ptr(), ws.numel() * ws.element_size(), _stream(stream)))
 
 
 def awq_w4a16_lora_workspace_size(T: int, inn: int, out: int, rank: int, cfg: AwqConfig) -> int:
@@ -387,25 +400,41 @@ def awq_w4a16_moe(X, router, gate_up, down, cfg: AwqConfig, renormalize: bool, m
     expert axis, mask uint8 [T] or None; outputs Y [T, hidden] fp16, ids int32
     and weights fp32 [T, top_k]."""
     import torch
-    f16, i32 = torch.float16, torch.int32
+    f16, i32, f32 = torch.float16, torch.int32, torch.float32
+    dev = torch._C._cuda_getDevice()
     gq, gz, gs = gate_up
     dq, dz, ds = down
     T, hidden = X.shape
-    E, inter, top_k = router.shape[0], dq.shape[1], ids.shape[1]
-    _refuse("awq_w4a16_moe", (
-        ("X", X, f16, True), ("router", router, f16, False), ("gate_up qweight", gq, i32, False),
-        ("gate_up qzeros", gz, i32, False), ("gate_up scales", gs, f16, False), ("down qweight", dq, i32, False),
-        ("down qzeros", dz, i32, False), ("down scales", ds, f16, False), ("mask", mask, torch.uint8, False),
-        ("Y", Y, f16, True), ("ids", ids, i32, False), ("weights", weights, torch.float32, False),
-        ("ws", ws, None, False)))
-    if (router.shape[1] != hidden or gq.shape != (E, hidden, inter // 4) or dq.shape != (E, inter, hidden // 8)
-            or gs.shape[2] != 2 * inter or ds.shape[2] != hidden or Y.shape != (T, hidden) or ids.shape[0] != T
-            or weights.shape != (T, top_k) or (mask is not None and mask.shape != (T,))):
-        raise AwqError("awq_w4a16_moe", 1, "the shapes of X, router, the experts and the outputs disagree")
+    E, inter, _ = dq.shape
+    top_k, g = ids.shape[-1], cfg.group_size
+    xs, ys = X.stride(), Y.stride()
+    if not (dev == X.get_device() == router.get_device() == gq.get_device() == gz.get_device() == gs.get_device()
+            == dq.get_device() == dz.get_device() == ds.get_device() == Y.get_device() == ids.get_device()
+            == weights.get_device() == ws.get_device()
+            and f16 is X.dtype is router.dtype is gs.dtype is ds.dtype is Y.dtype
+            and i32 is gq.dtype is gz.dtype is dq.dtype is dz.dtype is ids.dtype and weights.dtype is f32
+            and xs[1] == 1 and ys[1] == 1 and router.is_contiguous() and gq.is_contiguous() and gz.is_contiguous()
+            and gs.is_contiguous() and dq.is_contiguous() and dz.is_contiguous() and ds.is_contiguous()
+            and ids.is_contiguous() and weights.is_contiguous()
+            and router.numel() == E * hidden and gq.numel() * 4 == E * hidden * inter
+            and dq.numel() * 8 == E * hidden * inter and gs.numel() == E * (hidden // g) * 2 * inter
+            and gz.numel() * 4 == E * (hidden // g) * inter and ds.numel() == E * (inter // g) * hidden
+            and dz.numel() * 8 == E * (inter // g) * hidden and Y.numel() == T * hidden
+            and ids.numel() == T * top_k and weights.numel() == T * top_k
+            and (mask is None or (mask.get_device() == dev and mask.dtype is torch.uint8 and mask.is_contiguous()
+                                  and mask.numel() == T))):
+        _refuse("awq_w4a16_moe", dev, (("X", X, f16, (T, hidden)), ("Y", Y, f16, (T, hidden))), (
+            ("router", router, f16, (E, hidden)),
+            ("gate_up qweight", gq, i32, (E, hidden, inter // 4)),
+            ("gate_up qzeros", gz, i32, (E, hidden // g, inter // 4)),
+            ("gate_up scales", gs, f16, (E, hidden // g, 2 * inter)),
+            ("down qweight", dq, i32, (E, inter, hidden // 8)), ("down qzeros", dz, i32, (E, inter // g, hidden // 8)),
+            ("down scales", ds, f16, (E, inter // g, hidden)), ("mask", mask, torch.uint8, (T,)),
+            ("ids", ids, i32, (T, top_k)), ("weights", weights, f32, (T, top_k)), ("ws", ws, ws.dtype, ws.shape)))
     _check("awq_w4a16_moe", LIB.awq_w4a16_moe(
-        X.data_ptr(), T, hidden, X.stride(0), _ptr(mask), router.data_ptr(), E, top_k, 1 if renormalize else 0,
-        gq.data_ptr(), gz.data_ptr(), gs.data_ptr(), inter, dq.data_ptr(), dz.data_ptr(), ds.data_ptr(),
-        ctypes.byref(cfg), Y.data_ptr(), Y.stride(0), ids.data_ptr(), weights.data_ptr(), ws.data_ptr(),
+        X.data_ptr(), T, hidden, xs[0], None if mask is None else mask.data_ptr(), router.data_ptr(), E, top_k,
+        1 if renormalize else 0, gq.data_ptr(), gz.data_ptr(), gs.data_ptr(), inter, dq.data_ptr(), dz.data_ptr(),
+        ds.data_ptr(), ctypes.byref(cfg), Y.data_ptr(), ys[0], ids.data_ptr(), weights.data_ptr(), ws.data_ptr(),
         ws.numel() * ws.element_size(), _stream(stream)))
 
 
@@ -422,20 +451,34 @@ def awq_block_norm(R, V, post, gate, c: float, pre, eps: float, R_out, N_out, st
     fp16 rows [T, d]; V, post, gate ([T, d] or [d]), pre and one of the outputs
     may be None."""
     import torch
-    f16 = torch.float16
-    T, d = R.shape
-    _refuse("awq_block_norm", (
-        ("R", R, f16, True), ("V", V, f16, True), ("post", post, f16, False), ("gate", gate, f16, True),
-        ("pre", pre, f16, False), ("R_out", R_out, f16, True), ("N_out", N_out, f16, True)))
-    ldg = gate.stride(0) if gate is not None and gate.dim() == 2 else 0
-    if any(t is not None and t.shape != (T, d) for t in (V, R_out, N_out)) or any(
-            t is not None and t.shape != (d,) for t in (post, pre)) or (
-            gate is not None and gate.shape != ((T, d) if gate.dim() == 2 else (d,))):
-        raise AwqError("awq_block_norm", 1, "the shapes of R, V, post, gate, pre and the outputs disagree")
+    f16, dev, none = torch.float16, torch._C._cuda_getDevice(), (0, 1)
+    shape = T, d = R.shape
+    by_token = gate is not None and gate.dim() == 2
+    ldr, r1 = R.stride()
+    ldv, v1 = none if V is None else V.stride()
+    ldro, ro1 = none if R_out is None else R_out.stride()
+    ldno, no1 = none if N_out is None else N_out.stride()
+    ldg, g1 = gate.stride() if by_token else none
+    if not (r1 == v1 == ro1 == no1 == g1 == 1 and R.dtype is f16 and R.get_device() == dev
+            and (V is None or (V.dtype is f16 and V.get_device() == dev and V.shape == shape))
+            and (R_out is None or (R_out.dtype is f16 and R_out.get_device() == dev and R_out.shape == shape))
+            and (N_out is None or (N_out.dtype is f16 and N_out.get_device() == dev and N_out.shape == shape))
+            and (pre is None or (pre.dtype is f16 and pre.get_device() == dev and pre.numel() == d
+                                 and pre.is_contiguous()))
+            and (post is None or (post.dtype is f16 and post.get_device() == dev and post.numel() == d
+                                  and post.is_contiguous()))
+            and (gate is None or (gate.dtype is f16 and gate.get_device() == dev
+                                  and (gate.shape == shape if by_token else gate.numel() == d
+                                       and gate.is_contiguous())))):
+        rows = [("R", R, f16, shape), ("V", V, f16, shape), ("R_out", R_out, f16, shape), ("N_out", N_out, f16, shape)]
+        dense = [("post", post, f16, (d,)), ("pre", pre, f16, (d,))]
+        (rows if by_token else dense).append(("gate", gate, f16, shape if by_token else (d,)))
+        _refuse("awq_block_norm", dev, rows, dense)
     _check("awq_block_norm", LIB.awq_block_norm(
-        R.data_ptr(), R.stride(0), _ptr(V), 0 if V is None else V.stride(0), T, d, _ptr(post), _ptr(gate), ldg,
-        c, _ptr(pre), eps, _ptr(R_out), 0 if R_out is None else R_out.stride(0), _ptr(N_out),
-        0 if N_out is None else N_out.stride(0), _stream(stream)))
+        R.data_ptr(), ldr, None if V is None else V.data_ptr(), ldv, T, d, None if post is None else post.data_ptr(),
+        None if gate is None else gate.data_ptr(), ldg, c, None if pre is None else pre.data_ptr(), eps,
+        None if R_out is None else R_out.data_ptr(), ldro, None if N_out is None else N_out.data_ptr(), ldno,
+        _stream(stream)))
 
 
 def awq_device_status(ws, stream=None) -> None:

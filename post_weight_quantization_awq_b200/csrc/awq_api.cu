@@ -1,4 +1,4 @@
-// Host implementation of the C ABI declared in include/awq.h: argument
+// Host implementation of the C ABI declared in include/awq.h and awq_serving.h: argument
 // checks, workspace carving, kernel launches, per-thread error messages and
 // optional per-kernel event timing.
 #include <cuda_runtime.h>
@@ -14,6 +14,7 @@
 #include <nvtx3/nvToolsExt.h>
 
 #include "awq.h"
+#include "awq_serving.h"
 #include "awq_launch.h"
 #include "serve_launch.h"
 
@@ -1035,6 +1036,13 @@ awq_status awq_block_norm(const void *R, int64_t ldr, const void *V, int64_t ldv
   if (N_out && (st = check_rows("N_out", N_out, ldno, d)) != AWQ_OK) return st;
   if (pre && !N_out) return fail(AWQ_ERR_INVALID_ARG, "pre needs N_out");
   if (R_out && R_out == N_out) return fail(AWQ_ERR_INVALID_ARG, "R_out and N_out are the same buffer");
+  if (T > 1) {  // in place: an output's row must lie over its own input row
+    const struct { const void *p; int64_t ld; } in[2] = {{R, ldr}, {V, ldv}}, out[2] = {{R_out, ldro}, {N_out, ldno}};
+    for (const auto &o : out)
+      for (const auto &i : in)
+        if (o.p && o.p == i.p && o.ld != i.ld)
+          return fail(AWQ_ERR_INVALID_ARG, "an output in place of R or V has another row stride");
+  }
   AWQ_LAUNCH_GATE();
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
   const NormArgs a = {static_cast<const __half *>(R), static_cast<const __half *>(V),

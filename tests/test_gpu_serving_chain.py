@@ -151,3 +151,12 @@ def test_block_captured_by_its_first_call(T):
     r = subprocess.run([sys.executable, "-c", CAPTURE_FIRST.format(T=T)], env=env, capture_output=True, text=True,
                        timeout=300)
     assert r.returncode == 0 and "same" in r.stdout, r.stdout + r.stderr
+
+
+@pytest.mark.parametrize("args", [
+    "--op lora --tokens 3 --in 512 --out 256 --adapters 2", "--op lora --tokens 100 --in 512 --out 288 --rank 24",
+    "--op moe --tokens 5 --in 256 --out 384 --experts 4 --top-k 3", "--op norm --tokens 70 --in 4096"])
+def test_run_case_serving_ops(args, capsys):
+    from post_weight_quantization_awq_b200 import run_case
+    assert run_case.main(args.split() + ["--repeat", "2"]) == 0
+    assert args.split()[1] + ": T=" in capsys.readouterr().out

@@ -71,6 +71,7 @@ def _norm(**kw):
     (dict(d=0), "AWQ_ERR_INVALID_ARG"), (dict(d=60), "AWQ_ERR_INVALID_ARG"),
     (dict(d=32776, ldr=32776, ldv=32776, ldro=32776, ldno=32776), "AWQ_ERR_UNSUPPORTED"),
     (dict(R=None), "AWQ_ERR_INVALID_ARG"), (dict(R=24), "AWQ_ERR_INVALID_ARG"),
+    (dict(Ro=16, ldr=64, ldro=72), "AWQ_ERR_INVALID_ARG"), (dict(V=80, No=80, ldno=72), "AWQ_ERR_INVALID_ARG"),
     (dict(ldr=56), "AWQ_ERR_INVALID_ARG"), (dict(ldv=68), "AWQ_ERR_INVALID_ARG"),
     (dict(V=None, post=16), "AWQ_ERR_INVALID_ARG"), (dict(V=None, gate=16), "AWQ_ERR_INVALID_ARG"),
     (dict(gate=16, ldg=32), "AWQ_ERR_INVALID_ARG"), (dict(gate=20), "AWQ_ERR_INVALID_ARG"),
@@ -136,3 +137,26 @@ def test_injected_launch_failure_reaches_the_moe_call(monkeypatch):
     assert _name(_moe()) == "AWQ_ERR_CUDA"
     monkeypatch.setenv("AWQ_FAULT", "alloc")
     assert _name(_moe()) == "AWQ_ERR_WORKSPACE"
+
+
+def test_library_exports_and_gates_every_serving_call(monkeypatch):
+    names = set(abi.header_functions(abi.SERVING_HEADER_PATH)) - set(abi.header_functions())
+    sizes = {n for n in names if n.endswith("_workspace_size")}
+    assert names - sizes == {"awq_w4a16_lora_gemm", "awq_w4a16_moe", "awq_block_norm"}
+    for n in names:
+        assert abi.LIB[n] is not None and callable(getattr(awq, n))
+    monkeypatch.setenv("AWQ_FAULT", "launch")
+    for call in (_lora, _moe, _norm):
+        assert _name(call()) == "AWQ_ERR_CUDA" and "injected launch failure" in awq.last_error()
+
+
+def test_serving_header_is_plain_c(tmp_path):
+    import os
+    import shutil
+    import subprocess
+    if shutil.which("gcc") is None:
+        pytest.skip("no C compiler")
+    src = tmp_path / "h.c"
+    src.write_text('#include "awq_serving.h"\nint main(void) { return awq_block_norm == 0; }\n')
+    subprocess.run(["gcc", "-std=c11", "-Wall", "-Wextra", "-Werror", "-Wno-address", "-fsyntax-only", "-I",
+                    os.path.dirname(abi.SERVING_HEADER_PATH), str(src)], check=True)
