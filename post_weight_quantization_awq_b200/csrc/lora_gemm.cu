@@ -100,7 +100,7 @@ struct LoraShared {
   static_assert(kRed + kU <= kRing, "the sums and U reuse the ring");
 };
 
-template <Mode M, int NT, int MAXTOK, int STAGES, int MINB, bool FUSED>
+template <Mode M, int NT, int MAXTOK, int STAGES, int MINB, bool FUSED, int SHIFT>
 __global__ void __launch_bounds__(kThreads, MINB)
     lora_stream_kernel(const __grid_constant__ LoraArgs a, const __grid_constant__ CUtensorMap map, const int splits) {
   using L = LoraShared<M, NT, MAXTOK, STAGES>;
@@ -132,7 +132,7 @@ __global__ void __launch_bounds__(kThreads, MINB)
   const int k0 = (int)(units * rank / splits * unit);
   const int k1 = (int)i64min(units * (rank + 1) / splits * unit, a.in);
   if (tid >= kConsumers) {
-    Producer<M, MAXTOK> p(Weights{&map, 0, a.qzeros, a.scales, a.out / 8, group_shift(a.group),
+    Producer<M, MAXTOK> p(Weights{&map, 0, a.qzeros, a.scales, a.out / 8, SHIFT,
                   (int)(tile * 32), (int)(a.out / 8), (int)(tile * 32), (int)(a.out / 8)});
     RingPos pos;
     if (FUSED) {
@@ -202,7 +202,7 @@ __global__ void __launch_bounds__(kThreads, MINB)
       __syncwarp();
       cluster_arrive();
     }
-    consume<M, NT, MAXTOK, STAGES>(acc, pos, ring, bars, group_shift(a.group), k0, k1, true, a.max_polls, a.st);
+    consume<M, NT, MAXTOK, STAGES, SHIFT>(acc, pos, ring, bars, k0, k1, true, a.max_polls, a.st);
     if (FUSED) {
       cluster_wait();
       for (int i = tid; i < n * a.rank; i += kConsumers) {
@@ -360,13 +360,13 @@ int cluster_size(K kernel, size_t smem, int64_t clusters, int64_t most, std::ato
   return 1;
 }
 
-template <Mode M, int NT, int MAXTOK, int STAGES, int MINB, bool FUSED>
-cudaError_t launch_stream(const LoraArgs &a, int, cudaStream_t stream) {
+template <Mode M, int NT, int MAXTOK, int STAGES, int MINB, bool FUSED, int SHIFT>
+cudaError_t launch_stream(const LoraArgs &a, cudaStream_t stream) {
   static std::atomic<bool> done[64];
   static std::atomic<int> fit[64][9];
   constexpr size_t kSmem = LoraShared<M, NT, MAXTOK, STAGES>::kBytes;
   static_assert(MINB * (kSmem + 1024) <= 233472, "resident blocks");
-  auto kernel = lora_stream_kernel<M, NT, MAXTOK, STAGES, MINB, FUSED>;
+  auto kernel = lora_stream_kernel<M, NT, MAXTOK, STAGES, MINB, FUSED, SHIFT>;
   cudaError_t e = allow_smem(kernel, kSmem, done);
   if (e != cudaSuccess) return e;
   CUtensorMap map;  // the words as pairs of 16-bit values
@@ -395,17 +395,21 @@ cudaError_t launch_stream(const LoraArgs &a, int, cudaStream_t stream) {
   cfg.numAttrs = FUSED ? 1 : 2;
   return cudaLaunchKernelEx(&cfg, kernel, a, map, s);
 }
-}  // namespace
-
-cudaError_t launch_lora(const LoraArgs &a, int num_sms, cudaStream_t stream) {
+template <int SHIFT>
+cudaError_t launch_group(const LoraArgs &a, cudaStream_t stream) {
   // on its own up to as many values of U as keep A's part below the words'
   // (1 token at rank 64: as many bytes of A as of words for a block)
-  if (a.T <= 8 && a.T * a.rank <= 64) return launch_stream<Mode::kK, 1, 8, 4, 2, true>(a, num_sms, stream);
-  if (a.T <= 8) return launch_stream<Mode::kK, 1, 8, 4, 2, false>(a, num_sms, stream);
-  if (a.T <= 16) return launch_stream<Mode::kK, 2, 16, 8, 1, false>(a, num_sms, stream);
-  if (a.T <= 32) return launch_stream<Mode::kTok, 2, 32, 6, 1, false>(a, num_sms, stream);
-  if (a.T <= 48) return launch_stream<Mode::kTok, 3, 48, 6, 1, false>(a, num_sms, stream);
-  return launch_stream<Mode::kTok, 4, 64, 5, 1, false>(a, num_sms, stream);
+  if (a.T <= 8 && a.T * a.rank <= kFusedU) return launch_stream<Mode::kK, 1, 8, 4, 2, true, SHIFT>(a, stream);
+  if (a.T <= 8) return launch_stream<Mode::kK, 1, 8, 4, 2, false, SHIFT>(a, stream);
+  if (a.T <= 16) return launch_stream<Mode::kK, 2, 16, 8, 1, false, SHIFT>(a, stream);
+  if (a.T <= 32) return launch_stream<Mode::kTok, 2, 32, 6, 1, false, SHIFT>(a, stream);
+  if (a.T <= 48) return launch_stream<Mode::kTok, 3, 48, 6, 1, false, SHIFT>(a, stream);
+  return launch_stream<Mode::kTok, 4, 64, 5, 1, false, SHIFT>(a, stream);
+}
+}  // namespace
+
+cudaError_t launch_lora(const LoraArgs &a, cudaStream_t stream) {
+  return a.group == 128 ? launch_group<7>(a, stream) : a.group == 64 ? launch_group<6>(a, stream) : launch_group<5>(a, stream);
 }
 
 }  // namespace awq

@@ -394,7 +394,7 @@ __device__ __forceinline__ void each_stretch(const W &w, int b, F f) {
   }
 }
 
-template <int V>
+template <int V, int SHIFT>
 __global__ void __launch_bounds__(kThreads, Cfg<V>::kBlocks)
     moe_kernel(const __grid_constant__ MoeArgs a, const __grid_constant__ CUtensorMap gu_map,
                const __grid_constant__ CUtensorMap dn_map) {
@@ -406,7 +406,6 @@ __global__ void __launch_bounds__(kThreads, Cfg<V>::kBlocks)
   const uint32_t ring_u = smem_u32(ring);
   const int tid = threadIdx.x;
   DevStatus *st = a.st;
-  const int shift = group_shift(a.group);
   const int hidden = (int)a.hidden, inter = (int)a.inter;
   const int itiles = (inter + kTile - 1) / kTile, htiles = (hidden + kTile - 1) / kTile;
   const int kgh = (hidden + 127) / 128, kgi = (inter + 127) / 128;
@@ -459,13 +458,13 @@ __global__ void __launch_bounds__(kThreads, Cfg<V>::kBlocks)
     const int e = sh->seg_expert[up.seg_of(stretch)], tile = up.tile_of(stretch);
     const int64_t groups = (int64_t)e * (hidden / a.group);
     const int c0 = (tile & 1) * wi + (tile >> 1) * 64, end = (tile & 1) ? 2 * wi : wi;
-    return Weights{&gu_map, e * hidden, a.gu_z + groups * 2 * wi, a.gu_s + groups * 2 * inter, 2 * wi, shift,
+    return Weights{&gu_map, e * hidden, a.gu_z + groups * 2 * wi, a.gu_s + groups * 2 * inter, 2 * wi, SHIFT,
                    c0, end, c0 + 32, end};
   };
   const auto down_weights = [&](int stretch) {
     const int e = sh->seg_expert[down.seg_of(stretch)], c0 = down.tile_of(stretch) * 64;
     const int64_t groups = (int64_t)e * (inter / a.group);
-    return Weights{&dn_map, e * inter, a.dn_z + groups * wh, a.dn_s + groups * hidden, wh, shift, c0, wh, c0 + 32, wh};
+    return Weights{&dn_map, e * inter, a.dn_z + groups * wh, a.dn_s + groups * hidden, wh, SHIFT, c0, wh, c0 + 32, wh};
   };
   // values of H, each made once for every tile of down, up to which that costs
   // less than a barrier (1.8 us)
@@ -524,7 +523,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<V>::kBlocks)
       const auto run = [&](auto nt) {
         constexpr int NT = decltype(nt)::value;
         Acc<NT> acc;
-        consume<Mode::kN, NT, C::kTok, C::kStages>(acc, pos, ring, bars, shift, k0, k1, cols > kBoxN, a.max_polls, st);
+        consume<Mode::kN, NT, C::kTok, C::kStages, SHIFT>(acc, pos, ring, bars, k0, k1, cols > kBoxN, a.max_polls, st);
         if (lane_col >= cols) return;
 #pragma unroll
         for (int n = 0; n < NT; ++n)
@@ -682,10 +681,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<V>::kBlocks)
   }
 }
 
-template <int V>
+template <int V, int SHIFT>
 cudaError_t go(const MoeArgs &a, int num_sms, cudaStream_t stream) {
   static std::atomic<bool> done[64];
-  cudaError_t e = allow_smem(moe_kernel<V>, moe_smem<V>(), done);
+  cudaError_t e = allow_smem(moe_kernel<V, SHIFT>, moe_smem<V>(), done);
   if (e != cudaSuccess) return e;
   CUtensorMap gu, dn;  // the words of all experts as pairs of 16-bit values
   e = make_tmap_f16_box(&gu, a.gu_q, a.experts * a.hidden, a.inter / 2, a.inter / 2, 64, kBoxK);
@@ -702,14 +701,20 @@ cudaError_t go(const MoeArgs &a, int num_sms, cudaStream_t stream) {
   cfg.stream = stream;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, moe_kernel<V>, a, gu, dn);
+  return cudaLaunchKernelEx(&cfg, moe_kernel<V, SHIFT>, a, gu, dn);
+}
+template <int V>
+cudaError_t go_group(const MoeArgs &a, int num_sms, cudaStream_t stream) {
+  return a.group == 128  ? go<V, 7>(a, num_sms, stream)
+         : a.group == 64 ? go<V, 6>(a, num_sms, stream)
+                         : go<V, 5>(a, num_sms, stream);
 }
 }  // namespace
 
 cudaError_t launch_moe(const MoeArgs &a, int num_sms, cudaStream_t stream) {
   cudaError_t e = cudaMemsetAsync(a.st, 0, 512, stream);  // status word and counters
   if (e != cudaSuccess) return e;
-  return a.T <= 8 ? go<1>(a, num_sms, stream) : go<2>(a, num_sms, stream);
+  return a.T <= 8 ? go_group<1>(a, num_sms, stream) : go_group<2>(a, num_sms, stream);
 }
 
 MoeLayout moe_layout(int64_t T, int64_t hidden, int64_t inter, int64_t experts, int64_t top_k, int num_sms) {

@@ -59,7 +59,6 @@ __host__ __device__ constexpr uint32_t stage_bytes() {
   return (sz_offset<M, MAXTOK>() + 4 * kSz + 1023) / 1024 * 1024;
 }
 
-__device__ __forceinline__ int group_shift(int group) { return group == 32 ? 5 : group == 64 ? 6 : 7; }
 
 __device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool ok) {
   const uint32_t n = ok ? 16u : 0u;  // 0: zero-filled, nothing is read
@@ -76,6 +75,19 @@ __device__ __forceinline__ void tma_load_2d_at(uint32_t dst, const CUtensorMap *
       " [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y)
       : "memory");
+}
+
+// Whether the phase of `bar` has completed; does not wait.
+__device__ __forceinline__ bool mbar_test(uint64_t *bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
 }
 
 __device__ __forceinline__ void consumer_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
@@ -363,43 +375,47 @@ __device__ __forceinline__ void close_group(Acc<NT> &a) {
   for (int c = 0; c < 4; ++c) a.sx[c] = 0.0f;
 }
 
-// One box: four 16-row steps, each step's words and token fragments loaded one
-// step ahead.  w0 / w1: this lane's word addresses of rows 2q and 2q + 1; xa:
-// this lane's ldmatrix address.
+// Words and token fragments of two 16-row steps: the one at work and the next.
 template <int NT>
-__device__ __forceinline__ void box(Acc<NT> &a, const uint8_t *w0, const uint8_t *w1, uint32_t xa, const uint8_t *sz,
-                                    int wcol, int shift, bool upper) {
-  if (!(shift == 7 && upper)) open_group<NT>(a, sz, wcol);
-  constexpr int NB = (NT + 1) / 2;
-  uint32_t w[2][4], b[2][NB][4];
-  auto load_w = [&](uint32_t(&d)[4], int ks) {
-    d[0] = lds32(w0 + ks * 2048);
-    d[1] = lds32(w1 + ks * 2048);
-    d[2] = lds32(w0 + ks * 2048 + 1024);
-    d[3] = lds32(w1 + ks * 2048 + 1024);
-  };
-  auto load_x = [&](uint32_t(&d)[NB][4], int ks) {
-    if (NT == 1) {  // both steps of a half at once
-      ldsm4(d[0], xa + (ks >> 1) * 64);
-    } else {
+struct Frags {
+  static constexpr int kB = (NT + 1) / 2;
+  uint32_t w[2][4], b[2][kB][4];
+};
+
+// The words (this lane's rows 2q, 2q + 1, 2q + 8, 2q + 9) and token fragments of step
+// ks of a box; w0 / w1: the word addresses of rows 2q and 2q + 1; xa: the ldmatrix
+// address.  One token tile takes the fragments of two steps at once.
+template <int NT>
+__device__ __forceinline__ void load_step(Frags<NT> &f, const uint8_t *w0, const uint8_t *w1, uint32_t xa, int ks) {
+  uint32_t(&d)[4] = f.w[ks & 1];
+  d[0] = lds32(w0 + ks * 2048);
+  d[1] = lds32(w1 + ks * 2048);
+  d[2] = lds32(w0 + ks * 2048 + 1024);
+  d[3] = lds32(w1 + ks * 2048 + 1024);
+  if (NT == 1) {
+    if (!(ks & 1)) ldsm4(f.b[ks >> 1][0], xa + (ks >> 1) * 64);
+  } else {
 #pragma unroll
-      for (int n = 0; n < NB; ++n) ldsm4(d[n], xa + n * 16 * kXPitch + ks * 32);
-    }
-  };
-  load_w(w[0], 0);
-  load_x(b[0], 0);
+    for (int n = 0; n < Frags<NT>::kB; ++n) ldsm4(f.b[ks & 1][n], xa + n * 16 * kXPitch + ks * 32);
+  }
+}
+
+// One box: four 16-row steps, each step's words and fragments loaded one step
+// ahead.  Its first step is loaded already; next() loads the first step of the box
+// that follows, while this one's last step is at work.
+template <int NT, int SHIFT, class Next>
+__device__ __forceinline__ void box(Acc<NT> &a, Frags<NT> &f, const uint8_t *w0, const uint8_t *w1, uint32_t xa,
+                                    const uint8_t *sz, int wcol, bool upper, Next next) {
+  if (!(SHIFT == 7 && upper)) open_group<NT>(a, sz, wcol);
 #pragma unroll
   for (int ks = 0; ks < 4; ++ks) {
-    if (ks < 3) {
-      load_w(w[(ks + 1) & 1], ks + 1);
-      if (NT > 1)
-        load_x(b[(ks + 1) & 1], ks + 1);
-      else if (ks == 1)
-        load_x(b[1], 2);
-    }
-    const uint32_t(&c)[4] = w[ks & 1];
+    const uint32_t(&c)[4] = f.w[ks & 1];
     uint32_t v[4] = {__byte_perm(c[0], c[1], 0x5410), __byte_perm(c[0], c[1], 0x7632),
                      __byte_perm(c[2], c[3], 0x5410), __byte_perm(c[2], c[3], 0x7632)};
+    if (ks < 3)
+      load_step<NT>(f, w0, w1, xa, ks + 1);
+    else
+      next();
 #pragma unroll
     for (int p = 0; p < 4; ++p) {
       const uint32_t m = (p & 1) ? 0x00F000F0u : 0x000F000Fu;
@@ -416,26 +432,26 @@ __device__ __forceinline__ void box(Acc<NT> &a, const uint8_t *w0, const uint8_t
       }
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        const uint32_t b0 = NT == 1 ? b[ks >> 1][0][2 * (ks & 1)] : b[ks & 1][n / 2][2 * (n & 1)];
-        const uint32_t b1 = NT == 1 ? b[ks >> 1][0][2 * (ks & 1) + 1] : b[ks & 1][n / 2][2 * (n & 1) + 1];
+        const uint32_t b0 = NT == 1 ? f.b[ks >> 1][0][2 * (ks & 1)] : f.b[ks & 1][n / 2][2 * (n & 1)];
+        const uint32_t b1 = NT == 1 ? f.b[ks >> 1][0][2 * (ks & 1) + 1] : f.b[ks & 1][n / 2][2 * (n & 1) + 1];
         mma16816(a.grp[p][n], a0, a1, a2, a3, b0, b1);
         if (Acc<NT>::kSumX && p == 3)
           mma16816(a.sx, 0x00010001u, 0x00010001u, 0x00010001u, 0x00010001u, b0, b1);
       }
     }
-    if (ks == 1 && shift == 5) {
+    if (ks == 1 && SHIFT == 5) {
       close_group<NT>(a);
       open_group<NT>(a, sz + kSz, wcol);
     }
   }
-  if (shift != 7 || upper) close_group<NT>(a);
+  if (SHIFT != 7 || upper) close_group<NT>(a);
 }
 
 // The consumers' side of a product over rows [k0, k1) (multiples of 64; of 128
 // when g = 128).
-template <Mode M, int NT, int MAXTOK, int STAGES>
-__device__ __forceinline__ void consume(Acc<NT> &a, RingPos &pos, uint8_t *ring, RingBars<STAGES> *bars, int shift,
-                                        int k0, int k1, bool box1, uint32_t max_polls, DevStatus *st) {
+template <Mode M, int NT, int MAXTOK, int STAGES, int SHIFT>
+__device__ __forceinline__ void consume(Acc<NT> &a, RingPos &pos, uint8_t *ring, RingBars<STAGES> *bars, int k0, int k1,
+                                        bool box1, uint32_t max_polls, DevStatus *st) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int nw = warp & 3, half = warp >> 2, g = lane >> 2, q = lane & 3;
   const int wcol = nw * 8 + g, chunk = wcol >> 2;
@@ -446,25 +462,53 @@ __device__ __forceinline__ void consume(Acc<NT> &a, RingPos &pos, uint8_t *ring,
   const uint32_t xl = NT == 1 ? (lane & 7) * kXPitch + (lane >> 3) * 16
                               : ((lane >> 4) * 8 + (lane & 7)) * kXPitch + ((lane >> 3) & 1) * 16;
   const uint32_t xt = M == Mode::kTok ? half * NT * 8 * kXPitch : 0;
-  const int ns = num_stages<M>(k1 - k0);
   acc_zero<NT>(a);
-#pragma unroll 1
-  for (int s = 0; s < ns; ++s) {
-    if (!ring_wait(bars, &bars->full[pos.slot], pos.phase, max_polls, st, 0xE21u)) break;
+  // This warp's boxes; in modes kN and kK one of each stage, but for the last stages
+  // of a range that end before its half.
+  const int ns = num_stages<M>(k1 - k0), rows = k1 - k0, rem = rows % 256;
+  const int boxes = M == Mode::kN     ? (half == 0 || box1 ? ns : 0)
+                    : M == Mode::kTok ? rows / 64
+                    : half == 0       ? rows / 256 * 2 + min(rem / 64, 2)
+                                      : rows / 256 * 2 + (rem == 192);
+  Frags<NT> f;
+  const uint32_t w_at = M == Mode::kTok ? 0 : half * kBoxBytes;
+  const uint32_t x_at = x_offset() + (M == Mode::kK ? half * MAXTOK * kXPitch : 0) + xl + xt;
+  const uint32_t sz_at = sz_offset<M, MAXTOK>() + (M == Mode::kTok ? 0 : half * 2 * kSz);
+  const auto load = [&](int b, int ks) {
     const uint8_t *sp = ring + pos.slot * stage_bytes<M, MAXTOK>();
-#pragma unroll 1
-    for (int i = 0; i < (M == Mode::kTok ? 2 : 1); ++i) {
-      const int b = M == Mode::kTok ? i : half;
-      const int kb = box_row<M>(k0, s, b);
-      if (kb < k1 && (M != Mode::kN || b == 0 || box1)) {
-        const int xb = M == Mode::kN ? 0 : b;
-        box<NT>(a, sp + b * kBoxBytes + o0, sp + b * kBoxBytes + o1,
-                smem_u32(sp) + x_offset() + xb * MAXTOK * kXPitch + xl + xt,
-                sp + sz_offset<M, MAXTOK>() + b * 2 * kSz, wcol, shift, (kb & 64) != 0);
-      }
+    load_step<NT>(f, sp + w_at + b * kBoxBytes + o0, sp + w_at + b * kBoxBytes + o1,
+                  smem_u32(sp) + x_at + b * MAXTOK * kXPitch, ks);
+  };
+  bool ready = false, ok = true;
+  // A group of 128 is two boxes, one after the other (their count is even)
+  constexpr int kUnroll = SHIFT == 5 || NT == 4 ? 1 : 2;
+#pragma unroll kUnroll
+  for (int i = 0; i < boxes; ++i) {
+    const int b = M == Mode::kTok ? i & 1 : 0;  // box of the stage
+    // The first step was loaded while the box before was at work, and counts if the
+    // stage had landed.  There is no branch but this one: instructions of two boxes
+    // do not overlap across branches
+    if (!__all_sync(0xffffffffu, ready)) {
+      ok = ring_wait(bars, &bars->full[pos.slot], pos.phase, max_polls, st, 0xE21u);
+      if (!ok) break;
+      load(b, 0);
     }
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&bars->empty[pos.slot]);
+    const bool leaves = M != Mode::kTok || b == 1 || i == boxes - 1;
+    RingPos nx = pos;
+    nx.next<STAGES>();
+    ready = !leaves || mbar_test(&bars->full[nx.slot], nx.phase);
+    const uint8_t *sp = ring + pos.slot * stage_bytes<M, MAXTOK>();
+    box<NT, SHIFT>(a, f, sp + w_at + b * kBoxBytes + o0, sp + w_at + b * kBoxBytes + o1,
+                   smem_u32(sp) + x_at + b * MAXTOK * kXPitch, sp + sz_at + b * 2 * kSz, wcol, (i & 1) != 0, [&] {
+                     __syncwarp();  // every load from the box has been issued
+                     if (leaves && lane == 0) mbar_arrive(&bars->empty[pos.slot]);
+                     if (leaves) pos = nx;
+                     load(M == Mode::kTok && !leaves ? 1 : 0, 0);
+                   });
+  }
+  for (int s = M == Mode::kTok ? ns : boxes; ok && s < ns; ++s) {
+    ok = ring_wait(bars, &bars->full[pos.slot], pos.phase, max_polls, st, 0xE21u);
+    if (ok && lane == 0) mbar_arrive(&bars->empty[pos.slot]);
     pos.next<STAGES>();
   }
 #pragma unroll
