@@ -80,12 +80,12 @@ constexpr uint32_t moe_smem() {
   return n;
 }
 
-// All blocks meet (counter from 0 to gridDim.x); false when the wait ran out.
+// All blocks meet (counter from 0 to gridDim.x); false when the wait ran out.  The
+// release and the acquire cover the block's other threads through its barriers.
 __device__ __forceinline__ bool grid_barrier(uint32_t *counter, int *flag, DevStatus *st, uint32_t max_polls,
                                              uint32_t site) {
   __syncthreads();
   if (threadIdx.x == 0) {
-    __threadfence();
     uint32_t v;
     asm volatile("atom.add.release.gpu.global.u32 %0, [%1], 1;" : "=r"(v) : "l"(counter) : "memory");
     const uint64_t t0 = global_ns(), limit = (uint64_t)max_polls * 64u;
@@ -99,7 +99,6 @@ __device__ __forceinline__ bool grid_barrier(uint32_t *counter, int *flag, DevSt
         break;
       }
     }
-    __threadfence();
     *flag = ok;
   }
   __syncthreads();
@@ -327,70 +326,111 @@ __device__ __forceinline__ int h_rows(int n) { return 2 * n <= 8 ? 2 * n : n; }
 
 __device__ __forceinline__ float silu_mul(float g, float u) { return g / (1.0f + expf(-g)) * u; }
 
+// ceil(x / c) for a unit's cost c, x >= 0
+__device__ __forceinline__ int units_of(int x, int c) { return c == 3 ? (x + 2) / 3 : c == 4 ? (x + 3) / 4 : (x + 4) / 5; }
+
 // The units of a phase in their order: by (entry, tile) pair, a "stretch" of
 // `len` units of 128 input rows, gate|up with the entry outermost (and gate's
 // tile before up's), down with the tile outermost.  Blocks take even shares of
 // the units' cost.  Costs stay below 2^26 (about 300 entries of 5, 256 tiles, 128
 // units; or 32 tiles, 512 units): 32 bits.
+struct Stretch {
+  int seg, tile;
+  int before;  // the cost of all units before it
+};
+
 template <int V, bool DOWN>
 struct Work {
   const MoeLists<V> *sh;
   int n_seg, tiles, len;  // tiles: gate|up 2 x the pairs of tiles, down the tiles
-  int stretches, quota;
+  int quota;
 
   __device__ __forceinline__ Work(const MoeLists<V> *l, int tiles_, int len_)
-      : sh(l), n_seg(l->n_seg), tiles(tiles_), len(len_), stretches(l->n_seg * tiles_) {
+      : sh(l), n_seg(l->n_seg), tiles(tiles_), len(len_) {
     const int total = sh->seg_cost[n_seg] * tiles * len;
     quota = (total + (int)gridDim.x - 1) / (int)gridDim.x;
     // at least a unit's cost, so that every block between a stretch's first and last has a unit of it
     quota = max(quota, unit_cost(Cfg<V>::kTok));
   }
   __device__ __forceinline__ int cost(int seg) const { return sh->seg_cost[seg + 1] - sh->seg_cost[seg]; }
-  // stretch = seg * tiles + tile (gate|up), tile * n_seg + seg (down)
-  __device__ __forceinline__ int seg_of(int stretch) const { return DOWN ? stretch % n_seg : stretch / tiles; }
-  __device__ __forceinline__ int tile_of(int stretch) const { return DOWN ? stretch / n_seg : stretch % tiles; }
-  __device__ __forceinline__ int cost_before(int stretch) const {
-    const int seg = seg_of(stretch), tile = tile_of(stretch);
-    return (DOWN ? tile * sh->seg_cost[n_seg] + sh->seg_cost[seg] : sh->seg_cost[seg] * tiles + tile * cost(seg)) * len;
+  __device__ __forceinline__ Stretch at(int seg, int tile) const {
+    const int c = sh->seg_cost[seg];
+    return {seg, tile, (DOWN ? tile * sh->seg_cost[n_seg] + c : c * tiles + tile * cost(seg)) * len};
   }
   // The units of a stretch that block b takes: those whose cost offset lies in
   // its share [b quota, (b + 1) quota).
-  __device__ __forceinline__ void units(int stretch, int b, int &u0, int &u1) const {
-    const int d = b * quota - cost_before(stretch), c = cost(seg_of(stretch));
-    u0 = d <= 0 ? 0 : min((d + c - 1) / c, len);
-    u1 = d + quota <= 0 ? 0 : min((d + quota + c - 1) / c, len);
+  __device__ __forceinline__ void units(const Stretch &s, int b, int &u0, int &u1) const {
+    const int d = b * quota - s.before, c = cost(s.seg);
+    u0 = d <= 0 ? 0 : min(units_of(d, c), len);
+    u1 = d + quota <= 0 ? 0 : min(units_of(d + quota, c), len);
   }
   // The blocks of a stretch's first and last unit: all that take part in it.
-  __device__ __forceinline__ int2 blocks(int stretch) const {
-    const int at = cost_before(stretch);
-    return make_int2(at / quota, (at + (len - 1) * cost(seg_of(stretch))) / quota);
+  __device__ __forceinline__ int2 blocks(const Stretch &s) const {
+    return make_int2(s.before / quota, (s.before + (len - 1) * cost(s.seg)) / quota);
   }
   // The last stretch that begins at or before block b's share.
-  __device__ __forceinline__ int first_of(int b) const {
-    const int at = b * quota;
-    int lo = 0, hi = stretches;
+  __device__ __forceinline__ Stretch first_of(int b) const {
+    const int at_cost = b * quota, scale = DOWN ? len : tiles * len;
+    const int per_tile = sh->seg_cost[n_seg] * len, tile = DOWN ? min(at_cost / per_tile, tiles - 1) : 0;
+    const int rest = at_cost - tile * per_tile;
+    int lo = 0, hi = n_seg;
     while (hi - lo > 1) {
       const int m = (lo + hi) / 2;
-      if (cost_before(m) <= at)
+      if (sh->seg_cost[m] * scale <= rest)
         lo = m;
       else
         hi = m;
     }
-    return lo;
+    return at(lo, DOWN ? tile : min((rest - sh->seg_cost[lo] * scale) / (cost(lo) * len), tiles - 1));
+  }
+  __device__ __forceinline__ bool next(Stretch &s) const {  // false behind the last one
+    s.before += cost(s.seg) * len;
+    int &inner = DOWN ? s.seg : s.tile, &outer = DOWN ? s.tile : s.seg;
+    if (++inner < (DOWN ? n_seg : tiles)) return true;
+    inner = 0;
+    return ++outer < (DOWN ? tiles : n_seg);
   }
 };
 
 // Block b's stretches of a phase, in order: f(stretch, first unit, end).
 template <class W, class F>
 __device__ __forceinline__ void each_stretch(const W &w, int b, F f) {
-  if (!w.stretches) return;
-  for (int s = w.first_of(b); s < w.stretches; ++s) {
+  if (!w.n_seg) return;
+  Stretch s = w.first_of(b);
+  do {
     int u0, u1;
     w.units(s, b, u0, u1);
     if (u0 < u1)
       f(s, u0, u1);
     else if (u0 < w.len)
       break;  // the block's share has ended
+  } while (w.next(s));
+}
+
+// Sums of n0 and n1 parts, each in its parts' order, the loads of four of each in
+// flight together: p0(i) and p1(i) point at part i.
+template <class P0, class P1>
+__device__ __forceinline__ void sum_parts(int n0, P0 p0, int n1, P1 p1, float4 &s0, float4 &s1) {
+  s0 = s1 = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  const auto add = [](float4 &s, const float4 &v) {
+    s.x += v.x;
+    s.y += v.y;
+    s.z += v.z;
+    s.w += v.w;
+  };
+  for (int k = 0; k < n0 || k < n1; k += 4) {
+    float4 v[4], w[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      v[j] = w[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (k + j < n0) v[j] = __ldcg(reinterpret_cast<const float4 *>(p0(k + j)));
+      if (k + j < n1) w[j] = __ldcg(reinterpret_cast<const float4 *>(p1(k + j)));
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      add(s0, v[j]);
+      add(s1, w[j]);
+    }
   }
 }
 
@@ -454,15 +494,15 @@ __global__ void __launch_bounds__(kThreads, Cfg<V>::kBlocks)
   const int wi = inter / 8, wh = hidden / 8;  // word columns
   const int64_t pitch_gu = 2 * a.inter;  // a row of the gate|up sums
   // the words of a stretch
-  const auto up_weights = [&](int stretch) {
-    const int e = sh->seg_expert[up.seg_of(stretch)], tile = up.tile_of(stretch);
+  const auto up_weights = [&](const Stretch &s) {
+    const int e = sh->seg_expert[s.seg], tile = s.tile;
     const int64_t groups = (int64_t)e * (hidden / a.group);
     const int c0 = (tile & 1) * wi + (tile >> 1) * 64, end = (tile & 1) ? 2 * wi : wi;
     return Weights{&gu_map, e * hidden, a.gu_z + groups * 2 * wi, a.gu_s + groups * 2 * inter, 2 * wi, SHIFT,
                    c0, end, c0 + 32, end};
   };
-  const auto down_weights = [&](int stretch) {
-    const int e = sh->seg_expert[down.seg_of(stretch)], c0 = down.tile_of(stretch) * 64;
+  const auto down_weights = [&](const Stretch &s) {
+    const int e = sh->seg_expert[s.seg], c0 = s.tile * 64;
     const int64_t groups = (int64_t)e * (inter / a.group);
     return Weights{&dn_map, e * inter, a.dn_z + groups * wh, a.dn_s + groups * hidden, wh, SHIFT, c0, wh, c0 + 32, wh};
   };
@@ -474,9 +514,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<V>::kBlocks)
   if (tid >= kConsumers) {
     // ------------------------------------------------------------ producer
     RingPos pos;
-    each_stretch(up, (int)blockIdx.x, [&](int s, int u0, int u1) {
+    each_stretch(up, (int)blockIdx.x, [&](const Stretch &s, int u0, int u1) {
       Producer<Mode::kN, C::kTok> p(up_weights(s));
-      const int seg = up.seg_of(s), p0 = sh->seg_first[seg];
+      const int seg = s.seg, p0 = sh->seg_first[seg];
       p.rows(a.X, a.ldx, sh->seg_n[seg], [&](int t) { return sh->pair[p0 + t] / a.top_k; });
       p.template run<C::kStages>(pos, ring_u, bars, u0 * 128, min(u1 * 128, hidden), a.max_polls, st);
     });
@@ -491,7 +531,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<V>::kBlocks)
       else if (ok)
         ok = grid_barrier(a.barrier + 2, &sh->flag, st, a.max_polls, 0xE13u);
     };
-    each_stretch(down, (int)blockIdx.x, [&](int s, int u0, int u1) {
+    each_stretch(down, (int)blockIdx.x, [&](const Stretch &s, int u0, int u1) {
       Producer<Mode::kN, C::kTok> p(down_weights(s));
       const int k0 = u0 * 128, k1 = min(u1 * 128, inter);
       if (!met) {
@@ -504,7 +544,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<V>::kBlocks)
         meet();
       }
       if (!ok) return;
-      const int seg = down.seg_of(s), p0 = sh->seg_first[seg], n = sh->seg_n[seg], pairs = a.T * a.top_k;
+      const int seg = s.seg, p0 = sh->seg_first[seg], n = sh->seg_n[seg], pairs = a.T * a.top_k;
       p.rows(a.H, inter, h_rows(n),
              [&](int t) { return t < n ? sh->pair[p0 + t] : pairs + sh->pair[p0 + t - n]; });
       p.template run<C::kStages>(pos, ring_u, bars, k0, k1, a.max_polls, st, ahead);
@@ -550,8 +590,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<V>::kBlocks)
     const auto slot = [&](int64_t b, int which) { return a.partial + (b * 2 + which) * C::kTok * kTile; };
     const auto dn_slot = [&](int64_t b, int which) { return a.dn_partial + (b * 2 + which) * C::kTok * kTile; };
 
-    each_stretch(up, (int)blockIdx.x, [&](int s, int u0, int u1) {
-      const int seg = up.seg_of(s), tile = up.tile_of(s), p0 = sh->seg_first[seg], n = sh->seg_n[seg];
+    each_stretch(up, (int)blockIdx.x, [&](const Stretch &s, int u0, int u1) {
+      const int seg = s.seg, tile = s.tile, p0 = sh->seg_first[seg], n = sh->seg_n[seg];
       const int ch = (tile >> 1) * kTile, cols = min(kTile, inter - ch);  // the tile's channels
       const bool whole = u0 == 0 && u1 == up.len;
       float *part = slot(blockIdx.x, u0 == 0);
@@ -563,26 +603,21 @@ __global__ void __launch_bounds__(kThreads, Cfg<V>::kBlocks)
     // H of entry seg, channels [c0, c1) of one pair of tiles: the sums of the blocks
     // that share gate's and up's tile, silu(g) u, and what its rounding leaves
     const auto finish = [&](int seg, int c0, int c1) {
-      const int ch = c0 / kTile * kTile, sg = seg * up.tiles + 2 * (c0 / kTile);
+      const int ch = c0 / kTile * kTile, tile = 2 * (c0 / kTile);
       const int n = sh->seg_n[seg], p0 = sh->seg_first[seg], quads = (c1 - c0) / 4;
       const bool rest_too = h_rows(n) > n;
-      const int2 gb = up.blocks(sg), ub = up.blocks(sg + 1);
+      const int2 gb = up.blocks(up.at(seg, tile)), ub = up.blocks(up.at(seg, tile + 1));
       for (int i = tid; i < n * quads; i += kConsumers) {
         const int t = i / quads, c = c0 + 4 * (i - t * quads);
         const int64_t row = sh->pair[p0 + t];
-        const auto gather = [&](int2 b, int64_t off) {
-          if (b.x == b.y) return __ldcg(reinterpret_cast<const float4 *>(a.sums + row * pitch_gu + off + c));
-          float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-          for (int k = b.x; k <= b.y; ++k) {  // all but the first block enter inside the tile
-            const float4 p = __ldcg(reinterpret_cast<const float4 *>(slot(k, k == b.x) + t * kTile + c - ch));
-            v.x += p.x;
-            v.y += p.y;
-            v.z += p.z;
-            v.w += p.w;
-          }
-          return v;
+        // part j: a whole tile's sums, or those of the j-th of its blocks, which but for the first enter inside it
+        const auto part = [&](int2 b, int64_t off) {
+          return [=](int j) {
+            return b.x == b.y ? a.sums + row * pitch_gu + off + c : slot(b.x + j, j == 0) + t * kTile + c - ch;
+          };
         };
-        const float4 gv = gather(gb, 0), uv = gather(ub, a.inter);
+        float4 gv, uv;
+        sum_parts(gb.y - gb.x + 1, part(gb, 0), ub.y - ub.x + 1, part(ub, a.inter), gv, uv);
         const float h[4] = {silu_mul(gv.x, uv.x), silu_mul(gv.y, uv.y), silu_mul(gv.z, uv.z), silu_mul(gv.w, uv.w)};
         __align__(8) __half hi[4], rest[4];
 #pragma unroll
@@ -597,10 +632,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<V>::kBlocks)
     };
     ok = grid_barrier(a.barrier + 1, &sh->flag, st, a.max_polls, 0xE11u);
     if (ok && own_h) {  // other blocks may write the same values
-      each_stretch(down, (int)blockIdx.x, [&](int s, int u0, int u1) {
+      each_stretch(down, (int)blockIdx.x, [&](const Stretch &s, int u0, int u1) {
         const int end = min(u1 * 128, inter);
         for (int c = u0 * 128; c < end; c = c / kTile * kTile + kTile)
-          finish(down.seg_of(s), c, min(c / kTile * kTile + kTile, end));
+          finish(s.seg, c, min(c / kTile * kTile + kTile, end));
       });
       asm volatile("bar.sync 2, 288;" ::: "memory");  // the producer waits for it
     } else if (ok) {
@@ -612,8 +647,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<V>::kBlocks)
       ok = grid_barrier(a.barrier + 2, &sh->flag, st, a.max_polls, 0xE13u);
     }
     if (ok)
-      each_stretch(down, (int)blockIdx.x, [&](int s, int u0, int u1) {
-        const int seg = down.seg_of(s), ch = down.tile_of(s) * kTile, p0 = sh->seg_first[seg], n = sh->seg_n[seg];
+      each_stretch(down, (int)blockIdx.x, [&](const Stretch &s, int u0, int u1) {
+        const int seg = s.seg, ch = s.tile * kTile, p0 = sh->seg_first[seg], n = sh->seg_n[seg];
         const bool whole = u0 == 0 && u1 == down.len;
         float *part = dn_slot(blockIdx.x, u0 == 0);
         const int rows = h_rows(n), pairs = a.T * a.top_k;
@@ -628,58 +663,53 @@ __global__ void __launch_bounds__(kThreads, Cfg<V>::kBlocks)
   if (!grid_barrier(a.barrier + 3, &sh->flag, st, a.max_polls, 0xE12u)) return;
 
   // ---------------------------------------------------------------- combine
-  const int quads = hidden / 4;
-  for (int i = blockIdx.x * kThreads + tid; i < a.T * quads; i += gridDim.x * kThreads) {
-    const int t = i / quads, o = 4 * (i - t * quads), tile = o / kTile;
+  // A warp takes 32 / kp quads of four outputs, kp lanes to a quad: a token's choices
+  // side by side (their sums meet in a fixed tree)
+  int kp = 1;
+  while (kp < a.top_k) kp *= 2;
+  const int quads = hidden / 4, qw = 32 / kp, groups = (quads + qw - 1) / qw;
+  const int lane = tid & 31, k = lane / qw;
+  for (int i = blockIdx.x + gridDim.x * (tid >> 5); i < a.T * groups; i += gridDim.x * (kThreads / 32)) {
+    const int t = i / groups, quad = (i - t * groups) * qw + lane % qw, o = 4 * quad;
+    const int p = t * a.top_k + k, at = quad < quads && k < a.top_k ? sh->where[p] : -1;  // -1: a masked row
     float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    for (int k = 0; k < a.top_k; ++k) {
-      const int p = t * a.top_k + k;
-      const int at = sh->where[p];
-      if (at < 0) continue;  // a masked row
-      int seg = 0;  // the entry that holds position `at`
-      {
-        int lo = 0, hi = down.n_seg;
-        while (hi - lo > 1) {
-          const int m = (lo + hi) / 2;
-          if (sh->seg_first[m] <= at)
-            lo = m;
-          else
-            hi = m;
-        }
-        seg = lo;
+    if (at >= 0) {
+      int seg = 0, hi = down.n_seg;  // the entry that holds position `at`
+      while (hi - seg > 1) {
+        const int m = (seg + hi) / 2;
+        if (sh->seg_first[m] <= at)
+          seg = m;
+        else
+          hi = m;
       }
-      const int stretch = tile * down.n_seg + seg, n = sh->seg_n[seg], row = at - sh->seg_first[seg];
-      const int2 db = down.blocks(stretch);
-      const bool two = h_rows(n) > n;
-      float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      const auto add = [&](const float *src) {
-        const float4 x = __ldcg(reinterpret_cast<const float4 *>(src));
-        v.x += x.x;
-        v.y += x.y;
-        v.z += x.z;
-        v.w += x.w;
+      const int n = sh->seg_n[seg], row = at - sh->seg_first[seg];
+      const int2 db = down.blocks(down.at(seg, o / kTile));
+      const int parts = db.y - db.x + 1, w = o % kTile;
+      const auto part = [&](int j, int rest) -> const float * {
+        return parts == 1 ? a.dn_sums + (int64_t)(rest * a.T * a.top_k + p) * hidden + o
+                          : a.dn_partial + (((int64_t)db.x + j) * 2 + (j == 0)) * C::kTok * kTile + (rest * n + row) * kTile + w;
       };
-      if (db.x == db.y) {
-        add(a.dn_sums + (int64_t)p * hidden + o);
-        if (two) add(a.dn_sums + (int64_t)(a.T * a.top_k + p) * hidden + o);
-      } else {
-        for (int b = db.x; b <= db.y; ++b) {
-          const float *src = a.dn_partial + ((int64_t)b * 2 + (b == db.x)) * C::kTok * kTile + row * kTile + o - tile * kTile;
-          add(src);
-          if (two) add(src + n * kTile);
-        }
-      }
-      const float w = sh->wt[p];
-      y.x = fmaf(w, v.x, y.x);
-      y.y = fmaf(w, v.y, y.y);
-      y.z = fmaf(w, v.z, y.z);
-      y.w = fmaf(w, v.w, y.w);
+      float4 v, r;
+      sum_parts(parts, [&](int j) { return part(j, 0); }, h_rows(n) > n ? parts : 0, [&](int j) { return part(j, 1); }, v, r);
+      const float pw = sh->wt[p];
+      y = make_float4(pw * (v.x + r.x), pw * (v.y + r.y), pw * (v.z + r.z), pw * (v.w + r.w));
     }
-    const __half2 h0 = __floats2half2_rn(y.x, y.y), h1 = __floats2half2_rn(y.z, y.w);
-    *reinterpret_cast<uint2 *>(a.Y + t * a.ldy + o) =
-        make_uint2(*reinterpret_cast<const uint32_t *>(&h0), *reinterpret_cast<const uint32_t *>(&h1));
+    for (int d = qw; d < 32; d *= 2) {
+      y.x += __shfl_xor_sync(0xffffffffu, y.x, d);
+      y.y += __shfl_xor_sync(0xffffffffu, y.y, d);
+      y.z += __shfl_xor_sync(0xffffffffu, y.z, d);
+      y.w += __shfl_xor_sync(0xffffffffu, y.w, d);
+    }
+    if (k == 0 && quad < quads) {
+      const __half2 h0 = __floats2half2_rn(y.x, y.y), h1 = __floats2half2_rn(y.z, y.w);
+      *reinterpret_cast<uint2 *>(a.Y + t * a.ldy + o) =
+          make_uint2(*reinterpret_cast<const uint32_t *>(&h0), *reinterpret_cast<const uint32_t *>(&h1));
+    }
   }
 }
+
+// The status word and the counters, 512 bytes
+__global__ void moe_clear_kernel(uint4 *ws) { ws[threadIdx.x] = make_uint4(0u, 0u, 0u, 0u); }
 
 template <int V, int SHIFT>
 cudaError_t go(const MoeArgs &a, int num_sms, cudaStream_t stream) {
@@ -712,7 +742,8 @@ cudaError_t go_group(const MoeArgs &a, int num_sms, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t launch_moe(const MoeArgs &a, int num_sms, cudaStream_t stream) {
-  cudaError_t e = cudaMemsetAsync(a.st, 0, 512, stream);  // status word and counters
+  moe_clear_kernel<<<1, 32, 0, stream>>>(reinterpret_cast<uint4 *>(a.st));
+  const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   return a.T <= 8 ? go_group<1>(a, num_sms, stream) : go_group<2>(a, num_sms, stream);
 }
