@@ -920,7 +920,7 @@ awq_status awq_w4a16_lora_gemm(const void *X, int64_t T, int64_t in, int64_t ldx
                 rank, n_adapters, static_cast<__half *>(Y), ldy,
                 reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + kHeader), static_cast<DevStatus *>(ws), poll_cap()};
   ProfScope p("w4a16_lora", cs);
-  AWQ_TRY_CUDA(T <= kLoraStreamT ? launch_lora(a, cs) : launch_lora_prefill(a, num_sms_current(), cs),
+  AWQ_TRY_CUDA(T <= kLoraStreamT ? launch_lora(a, num_sms_current(), cs) : launch_lora_prefill(a, num_sms_current(), cs),
                "w4a16_lora launch");
   return AWQ_OK;
 }

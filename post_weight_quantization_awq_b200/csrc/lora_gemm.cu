@@ -109,8 +109,8 @@ __global__ void __launch_bounds__(kThreads, MINB)
   float *red = reinterpret_cast<float *>(ring);
   uint8_t *uhl = ring + L::kRed;
   auto *bars = reinterpret_cast<RingBars<STAGES> *>(ring + L::kRing);
-  // the block's tokens stand in the order of their adapters, so that one's tokens
-  // fill whole token tiles
+  // the tokens stand in the order of their adapters, so that one's tokens fill whole
+  // token tiles; this block's are the places [t0, t0 + n)
   int *ids = reinterpret_cast<int *>(bars + 1);  // adapter of the token at a place, -1: none
   int *perm = ids + MAXTOK;                      // its row of X
   int *list = perm + MAXTOK;                     // the different adapters' first place | end << 16
@@ -118,7 +118,9 @@ __global__ void __launch_bounds__(kThreads, MINB)
   int *n_list = reinterpret_cast<int *>(uscale + MAXTOK);
   float *upart = reinterpret_cast<float *>(n_list + 4);  // FUSED: U over this block's rows, [token][rank row]
   float *usum = upart + kFusedU;                         // and over all (16-byte aligned, like all before it)
+  int *all_ids = reinterpret_cast<int *>(upart);         // before that: all tokens' adapters
   static_assert(sizeof(RingBars<STAGES>) % 16 == 0 && MAXTOK % 4 == 0 && kFusedU % 4 == 0, "alignment");
+  static_assert(kFusedU >= kLoraStreamT, "all tokens' adapters");
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = (int)(blockIdx.x % (unsigned)splits);
   const int64_t tile = blockIdx.x / (unsigned)splits;
@@ -144,7 +146,7 @@ __global__ void __launch_bounds__(kThreads, MINB)
     for (int s = 0; s < ahead; ++s)
       p.issue_words(smem_u32(ring) + s * stage_bytes<M, MAXTOK>(), &bars->full[s], k0, k1, s);
     asm volatile("bar.sync 2, 288;" ::: "memory");
-    p.rows(a.X + t0 * a.ldx, a.ldx, n, [&](int t) { return perm[t]; });
+    p.rows(a.X, a.ldx, n, [&](int t) { return perm[t]; });
     p.run(pos, smem_u32(ring), bars, k0, k1, a.max_polls, a.st, ahead);
     if (FUSED) {
       __syncwarp();
@@ -156,19 +158,20 @@ __global__ void __launch_bounds__(kThreads, MINB)
     RingPos pos;
     Acc<NT> acc;
     // the tokens' order, while the first words travel
-    for (int t = tid; t < MAXTOK; t += kConsumers) {
-      const int id = t < n ? __ldg(a.ids + t0 + t) : -1;
-      list[t] = id >= 0 && id < a.adapters ? id : -1;
+    if (tid < a.T) {
+      const int id = __ldg(a.ids + tid);
+      all_ids[tid] = id >= 0 && id < a.adapters ? id : -1;
     }
+    if (tid < MAXTOK) ids[tid] = -1;
     consumer_sync();
-    if (tid < n) {
-      const int id = list[tid];
-      int at = 0;
-      for (int s = 0; s < n; ++s) at += list[s] < id || (list[s] == id && s < tid);
-      ids[at] = id;
-      perm[at] = tid;
-    } else if (tid < MAXTOK) {
-      ids[tid] = -1;
+    if (tid < a.T) {
+      const int id = all_ids[tid];
+      int at = -(int)t0;
+      for (int s = 0; s < a.T; ++s) at += all_ids[s] < id || (all_ids[s] == id && s < tid);
+      if (at >= 0 && at < n) {
+        ids[at] = id;
+        perm[at] = tid;
+      }
     }
     asm volatile("bar.sync 2, 288;" ::: "memory");
     if (warp == 0) {
@@ -190,7 +193,7 @@ __global__ void __launch_bounds__(kThreads, MINB)
       for (int i = warp; i < n * a.rank; i += kConsumers / 32) {
         const int t = i / a.rank, r = i - t * a.rank, id = ids[t];
         if (id < 0) continue;
-        const uint4 *x = reinterpret_cast<const uint4 *>(a.X + (t0 + perm[t]) * a.ldx);
+        const uint4 *x = reinterpret_cast<const uint4 *>(a.X + perm[t] * a.ldx);
         const uint4 *w = reinterpret_cast<const uint4 *>(a.A + ((int64_t)id * a.rank + r) * a.in);
         float s = 0.0f;
 #pragma unroll 2
@@ -220,7 +223,7 @@ __global__ void __launch_bounds__(kThreads, MINB)
       constexpr int kTeam = MAXTOK <= 8 ? 32 : MAXTOK <= 16 ? 16 : MAXTOK <= 32 ? 8 : 4;
       const int t = tid / kTeam, part = tid % kTeam;
       const bool on = t < n && ids[t] >= 0;
-      const float4 *u = reinterpret_cast<const float4 *>(FUSED ? usum + t * a.rank : a.U + (t0 + (on ? perm[t] : 0)) * a.rank);
+      const float4 *u = reinterpret_cast<const float4 *>(FUSED ? usum + t * a.rank : a.U + (on ? perm[t] : 0) * a.rank);
       float m = 0.0f;
 #pragma unroll 4
       for (int k = part; k < a.rank / 4; k += kTeam)
@@ -304,10 +307,10 @@ __global__ void __launch_bounds__(kThreads, MINB)
     }
     store_sums<M, NT>(acc, red);
   }
-  if (blockIdx.x == 0 && warp == kConsumers / 32) {
+  if (blockIdx.x == 0 && blockIdx.y == 0 && warp == kConsumers / 32) {
     if (!FUSED) pdl_wait();
-    for (int t = lane; t < n; t += 32) {
-      const int id = a.ids[t0 + t];
+    for (int t = lane; t < a.T; t += 32) {
+      const int id = a.ids[t];
       if (id < -1 || id >= a.adapters) dev_fail(a.st, kDevBadAdapter, 0xE01u);
     }
   }
@@ -323,7 +326,7 @@ __global__ void __launch_bounds__(kThreads, MINB)
       s0 += p[0];
       s1 += p[1];
     }
-    *reinterpret_cast<__half2 *>(a.Y + (t0 + perm[t]) * a.ldy + o) = __floats2half2_rn(s0, s1);
+    *reinterpret_cast<__half2 *>(a.Y + perm[t] * a.ldy + o) = __floats2half2_rn(s0, s1);
   }
   cluster.sync();  // no block leaves while its sums are read
 }
@@ -360,56 +363,94 @@ int cluster_size(K kernel, size_t smem, int64_t clusters, int64_t most, std::ato
   return 1;
 }
 
+// The blocks that share a tile (and a group of MAXTOK tokens), and the time of the
+// whole in cycles of its steps, measured: 252, 313 and 400 for 2, 3 and 4 token tiles.
+struct Split {
+  int s;
+  int64_t groups, cycles;
+};
 template <Mode M, int NT, int MAXTOK, int STAGES, int MINB, bool FUSED, int SHIFT>
-cudaError_t launch_stream(const LoraArgs &a, cudaStream_t stream) {
-  static std::atomic<bool> done[64];
-  static std::atomic<int> fit[64][9];
-  constexpr size_t kSmem = LoraShared<M, NT, MAXTOK, STAGES>::kBytes;
+struct Stream {
+  static constexpr size_t kSmem = LoraShared<M, NT, MAXTOK, STAGES>::kBytes;
   static_assert(MINB * (kSmem + 1024) <= 233472, "resident blocks");
-  auto kernel = lora_stream_kernel<M, NT, MAXTOK, STAGES, MINB, FUSED, SHIFT>;
-  cudaError_t e = allow_smem(kernel, kSmem, done);
-  if (e != cudaSuccess) return e;
-  CUtensorMap map;  // the words as pairs of 16-bit values
-  e = make_tmap_f16_box(&map, a.qweight, a.in, a.out / 4, a.out / 4, 64, kBoxK);
-  if (e != cudaSuccess) return e;
-  const int64_t tiles = (a.out + kBoxN - 1) / kBoxN;
-  const int s = cluster_size(kernel, kSmem, tiles, (a.in + 127) / 128, fit);
-  if (!FUSED) {
-    const int64_t blocks = a.T * (a.rank / kShrinkR);
-    lora_shrink_kernel<<<(unsigned)blocks, 256, 0, stream>>>(a);
-    e = cudaGetLastError();
+  static constexpr auto kernel = lora_stream_kernel<M, NT, MAXTOK, STAGES, MINB, FUSED, SHIFT>;
+
+  static cudaError_t split(const LoraArgs &a, int num_sms, Split &p) {
+    static std::atomic<bool> done[64];
+    static std::atomic<int> fit[64][9];
+    const cudaError_t e = allow_smem(kernel, kSmem, done);
     if (e != cudaSuccess) return e;
+    p.groups = (a.T + MAXTOK - 1) / MAXTOK;
+    const int64_t clusters = (a.out + kBoxN - 1) / kBoxN * p.groups;
+    p.s = cluster_size(kernel, kSmem, clusters, (a.in + 127) / 128, fit);
+    const int64_t waves = (clusters * p.s + num_sms * MINB - 1) / (num_sms * MINB);
+    p.cycles = waves * ((a.in + p.s - 1) / p.s) / (M == Mode::kTok ? 16 : 32) * (NT <= 2 ? 252 : NT == 3 ? 313 : 400);
+    return cudaSuccess;
   }
-  cudaLaunchAttribute at[2];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = (unsigned)s;
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[1].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(tiles * s));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = kSmem;
-  cfg.stream = stream;
-  cfg.attrs = at;
-  cfg.numAttrs = FUSED ? 1 : 2;
-  return cudaLaunchKernelEx(&cfg, kernel, a, map, s);
+
+  static cudaError_t launch(const LoraArgs &a, const Split &p, cudaStream_t stream) {
+    CUtensorMap map;  // the words as pairs of 16-bit values
+    cudaError_t e = make_tmap_f16_box(&map, a.qweight, a.in, a.out / 4, a.out / 4, 64, kBoxK);
+    if (e != cudaSuccess) return e;
+    if (!FUSED) {
+      const int64_t blocks = a.T * (a.rank / kShrinkR);
+      lora_shrink_kernel<<<(unsigned)blocks, 256, 0, stream>>>(a);
+      e = cudaGetLastError();
+      if (e != cudaSuccess) return e;
+    }
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = (unsigned)p.s;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[1].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((a.out + kBoxN - 1) / kBoxN * p.s), (unsigned)p.groups);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmem;
+    cfg.stream = stream;
+    cfg.attrs = at;
+    cfg.numAttrs = FUSED ? 1 : 2;
+    return cudaLaunchKernelEx(&cfg, kernel, a, map, p.s);
+  }
+
+  static cudaError_t run(const LoraArgs &a, int num_sms, cudaStream_t stream) {
+    Split p;
+    const cudaError_t e = split(a, num_sms, p);
+    return e != cudaSuccess ? e : launch(a, p, stream);
+  }
+};
+
+// 17 tokens and more: all of them in one block, or 16 in each of several blocks of a
+// tile, whichever fills the SMs better (45 tokens on 4096 x 12288: 45 us in 48 clusters
+// of 2, since 48 of 3 do not fit, 37 us in 3 groups of 16).
+template <class Whole, class Groups>
+cudaError_t launch_wide(const LoraArgs &a, int num_sms, cudaStream_t stream) {
+  Split w, g;
+  cudaError_t e = Whole::split(a, num_sms, w);
+  if (e == cudaSuccess) e = Groups::split(a, num_sms, g);
+  if (e != cudaSuccess) return e;
+  return g.cycles < w.cycles ? Groups::launch(a, g, stream) : Whole::launch(a, w, stream);
 }
+
 template <int SHIFT>
-cudaError_t launch_group(const LoraArgs &a, cudaStream_t stream) {
+cudaError_t launch_group(const LoraArgs &a, int num_sms, cudaStream_t stream) {
   // on its own up to as many values of U as keep A's part below the words'
   // (1 token at rank 64: as many bytes of A as of words for a block)
-  if (a.T <= 8 && a.T * a.rank <= kFusedU) return launch_stream<Mode::kK, 1, 8, 4, 2, true, SHIFT>(a, stream);
-  if (a.T <= 8) return launch_stream<Mode::kK, 1, 8, 4, 2, false, SHIFT>(a, stream);
-  if (a.T <= 16) return launch_stream<Mode::kK, 2, 16, 8, 1, false, SHIFT>(a, stream);
-  if (a.T <= 32) return launch_stream<Mode::kTok, 2, 32, 6, 1, false, SHIFT>(a, stream);
-  if (a.T <= 48) return launch_stream<Mode::kTok, 3, 48, 6, 1, false, SHIFT>(a, stream);
-  return launch_stream<Mode::kTok, 4, 64, 5, 1, false, SHIFT>(a, stream);
+  if (a.T <= 8 && a.T * a.rank <= kFusedU) return Stream<Mode::kK, 1, 8, 4, 2, true, SHIFT>::run(a, num_sms, stream);
+  if (a.T <= 8) return Stream<Mode::kK, 1, 8, 4, 2, false, SHIFT>::run(a, num_sms, stream);
+  using Groups = Stream<Mode::kK, 2, 16, 8, 1, false, SHIFT>;
+  if (a.T <= 16) return Groups::run(a, num_sms, stream);
+  if (a.T <= 32) return launch_wide<Stream<Mode::kTok, 2, 32, 6, 1, false, SHIFT>, Groups>(a, num_sms, stream);
+  if (a.T <= 48) return launch_wide<Stream<Mode::kTok, 3, 48, 6, 1, false, SHIFT>, Groups>(a, num_sms, stream);
+  return launch_wide<Stream<Mode::kTok, 4, 64, 5, 1, false, SHIFT>, Groups>(a, num_sms, stream);
 }
 }  // namespace
 
-cudaError_t launch_lora(const LoraArgs &a, cudaStream_t stream) {
-  return a.group == 128 ? launch_group<7>(a, stream) : a.group == 64 ? launch_group<6>(a, stream) : launch_group<5>(a, stream);
+cudaError_t launch_lora(const LoraArgs &a, int num_sms, cudaStream_t stream) {
+  return a.group == 128  ? launch_group<7>(a, num_sms, stream)
+         : a.group == 64 ? launch_group<6>(a, num_sms, stream)
+                         : launch_group<5>(a, num_sms, stream);
 }
 
 }  // namespace awq

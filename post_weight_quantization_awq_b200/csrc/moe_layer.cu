@@ -56,7 +56,7 @@ struct Cfg {
 // Where every block computes all logits itself: so many of them, from so many
 // router values (64 KB from L2 in about the time of a barrier).
 constexpr int kAloneLogits = 32, kAloneRouter = 32768;
-constexpr int64_t kOwnH = 2 << 20;
+constexpr int64_t kOwnH = 1 << 19;
 constexpr int kPieceH = 128;  // channels of H made at a time; divides a tile
 
 template <int V>
@@ -506,8 +506,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<V>::kBlocks)
     const int64_t groups = (int64_t)e * (inter / a.group);
     return Weights{&dn_map, e * inter, a.dn_z + groups * wh, a.dn_s + groups * hidden, wh, SHIFT, c0, wh, c0 + 32, wh};
   };
-  // values of H, each made once for every tile of down, up to which that costs
-  // less than a barrier (1.8 us)
+  // values of H, each made once for every tile of down, up to which that costs less
+  // than another barrier (0.83M values: 62.3 us made by each block, 60.9 made by all)
   const bool own_h = (int64_t)a.T * a.top_k * inter * htiles <= kOwnH;
   bool ok = true;
 
@@ -600,16 +600,15 @@ __global__ void __launch_bounds__(kThreads, Cfg<V>::kBlocks)
         return whole ? gu + sh->pair[p0 + t] * pitch_gu : part + t * kTile;
       });
     });
-    // H of entry seg, channels [c0, c1) of one pair of tiles: the sums of the blocks
-    // that share gate's and up's tile, silu(g) u, and what its rounding leaves
+    // H of entry seg, channels [c0, c1): the sums of the blocks that share gate's and
+    // up's tile, silu(g) u, and what its rounding leaves
     const auto finish = [&](int seg, int c0, int c1) {
-      const int ch = c0 / kTile * kTile, tile = 2 * (c0 / kTile);
       const int n = sh->seg_n[seg], p0 = sh->seg_first[seg], quads = (c1 - c0) / 4;
       const bool rest_too = h_rows(n) > n;
-      const int2 gb = up.blocks(up.at(seg, tile)), ub = up.blocks(up.at(seg, tile + 1));
       for (int i = tid; i < n * quads; i += kConsumers) {
-        const int t = i / quads, c = c0 + 4 * (i - t * quads);
+        const int t = i / quads, c = c0 + 4 * (i - t * quads), ch = c / kTile * kTile;
         const int64_t row = sh->pair[p0 + t];
+        const int2 gb = up.blocks(up.at(seg, 2 * (c / kTile))), ub = up.blocks(up.at(seg, 2 * (c / kTile) + 1));
         // part j: a whole tile's sums, or those of the j-th of its blocks, which but for the first enter inside it
         const auto part = [&](int2 b, int64_t off) {
           return [=](int j) {
@@ -633,9 +632,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<V>::kBlocks)
     ok = grid_barrier(a.barrier + 1, &sh->flag, st, a.max_polls, 0xE11u);
     if (ok && own_h) {  // other blocks may write the same values
       each_stretch(down, (int)blockIdx.x, [&](const Stretch &s, int u0, int u1) {
-        const int end = min(u1 * 128, inter);
-        for (int c = u0 * 128; c < end; c = c / kTile * kTile + kTile)
-          finish(s.seg, c, min(c / kTile * kTile + kTile, end));
+        finish(s.seg, u0 * 128, min(u1 * 128, inter));
       });
       asm volatile("bar.sync 2, 288;" ::: "memory");  // the producer waits for it
     } else if (ok) {

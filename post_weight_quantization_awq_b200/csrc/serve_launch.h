@@ -48,7 +48,7 @@ struct LoraArgs {
 // Y = X W^T + c_a (X A_a^T) B_a^T; in % 64 == 0, out % 32 == 0, rank % 8 == 0.
 // Up to kLoraStreamT tokens it streams the packed words; `U` then holds [T, rank] fp32.
 constexpr int64_t kLoraStreamT = 64;
-cudaError_t launch_lora(const LoraArgs &a, cudaStream_t stream);
+cudaError_t launch_lora(const LoraArgs &a, int num_sms, cudaStream_t stream);
 // More tokens: `U` holds lora_prefill_ws() bytes.
 size_t lora_prefill_ws(int64_t T, int64_t in, int64_t out, int rank);
 cudaError_t launch_lora_prefill(const LoraArgs &a, int num_sms, cudaStream_t stream);
