@@ -63,6 +63,7 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
 template <int TEAM, int ROWS, int VPT>
 __global__ void __launch_bounds__(TEAM *ROWS) block_norm_kernel(const NormArgs a) {
   __shared__ float red[2][32];
+  pdl_wait();
   const int lane = threadIdx.x % TEAM;
   const int64_t row = (int64_t)blockIdx.x * ROWS + threadIdx.x / TEAM;
   if (row >= a.T) return;  // ROWS > 1 only with TEAM = 32: no barrier is missed
@@ -146,8 +147,7 @@ __global__ void __launch_bounds__(TEAM *ROWS) block_norm_kernel(const NormArgs a
 
 template <int TEAM, int ROWS, int VPT>
 cudaError_t go(const NormArgs &a, cudaStream_t stream) {
-  block_norm_kernel<TEAM, ROWS, VPT><<<(unsigned)((a.T + ROWS - 1) / ROWS), TEAM * ROWS, 0, stream>>>(a);
-  return cudaGetLastError();
+  return launch_after(block_norm_kernel<TEAM, ROWS, VPT>, (a.T + ROWS - 1) / ROWS, TEAM * ROWS, 0, stream, a);
 }
 }  // namespace
 

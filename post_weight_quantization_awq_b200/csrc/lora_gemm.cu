@@ -20,9 +20,6 @@ namespace {
 namespace cg = cooperative_groups;
 using namespace w4s;
 
-__device__ __forceinline__ void pdl_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-
 __device__ __forceinline__ float dot8(uint4 a, uint4 b, float s) {
   const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
@@ -40,6 +37,7 @@ __device__ __forceinline__ float dot8(uint4 a, uint4 b, float s) {
 constexpr int kShrinkR = 8;
 __global__ void __launch_bounds__(256) lora_shrink_kernel(const LoraArgs a) {
   __shared__ float part[8][kShrinkR];
+  pdl_wait();  // the work before this call: its results are the stream kernel's inputs too
   pdl_launch();
   if (blockIdx.x == 0 && threadIdx.x == 0) *a.st = DevStatus{};
   const int chunks = a.rank / kShrinkR, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -128,6 +126,7 @@ __global__ void __launch_bounds__(kThreads, MINB)
   const int n = (int)(a.T - t0 < MAXTOK ? a.T - t0 : MAXTOK);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) ring_init(bars);
+  if (FUSED) pdl_wait();  // the work before this call
   __syncthreads();
   // input rows of this rank, in units of 256 (128) rows so that groups stay whole
   const int64_t unit = a.in >= 512 * splits ? 256 : 128, units = (a.in + unit - 1) / unit;
@@ -393,24 +392,22 @@ struct Stream {
     cudaError_t e = make_tmap_f16_box(&map, a.qweight, a.in, a.out / 4, a.out / 4, 64, kBoxK);
     if (e != cudaSuccess) return e;
     if (!FUSED) {
-      const int64_t blocks = a.T * (a.rank / kShrinkR);
-      lora_shrink_kernel<<<(unsigned)blocks, 256, 0, stream>>>(a);
-      e = cudaGetLastError();
+      e = launch_after(lora_shrink_kernel, a.T * (a.rank / kShrinkR), 256, 0, stream, a);
       if (e != cudaSuccess) return e;
     }
     cudaLaunchAttribute at[2];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = (unsigned)p.s;
-    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[1].val.programmaticStreamSerializationAllowed = 1;
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = (unsigned)p.s;
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)((a.out + kBoxN - 1) / kBoxN * p.s), (unsigned)p.groups);
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = kSmem;
     cfg.stream = stream;
     cfg.attrs = at;
-    cfg.numAttrs = FUSED ? 1 : 2;
+    cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, kernel, a, map, p.s);
   }
 

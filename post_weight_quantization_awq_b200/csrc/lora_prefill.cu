@@ -102,7 +102,6 @@ __device__ void shrink_block(const LoraArgs &a, int64_t t0, uint8_t *smem) {
   if (tid < kShT) {
     const int id = tid < n ? a.ids[t0 + tid] : -1;
     ids[tid] = id >= 0 && id < a.adapters ? id : -1;
-    if (id < -1 || id >= a.adapters) dev_fail(a.st, kDevBadAdapter, 0xE02u);
   }
   __syncthreads();
   const int count = adapter_list(ids, n, list, scratch);
@@ -156,7 +155,9 @@ constexpr int kShrinkSmem = kShWarps * kShT * (kShR + 1) * 4 + (256 + 256 + 16) 
 // lists[tile][bm + 1] = count, ids.
 __global__ void __launch_bounds__(kShThreads) lora_shrink_mma_kernel(const LoraArgs a, int n_shrink, int bm, int *lists) {
   __shared__ __align__(16) uint8_t smem[kShrinkSmem];
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  pdl_wait();
+  pdl_launch();
+  if (blockIdx.x == 0 && threadIdx.x == 0) *a.st = DevStatus{};
   int64_t b = blockIdx.x;
   if (b < n_shrink) {
     shrink_block(a, b * kShT, smem);
@@ -180,7 +181,7 @@ __global__ void __launch_bounds__(256) lora_dequant_kernel(const LoraArgs a, __h
   const int64_t tiles_o = (a.out + kWideOut - 1) / kWideOut, b = blockIdx.x;
   dequant_wide(tile, a.qweight, a.qzeros, a.scales, a.in, a.out, a.group, b % tiles_o * kWideOut,
                b / tiles_o * kWideIn, Wd);
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // its end is the shrink product's too
+  pdl_wait();  // its end is the shrink product's too
 }
 
 // ---------------------------------------------------------------------------
@@ -276,6 +277,7 @@ __global__ void __launch_bounds__(320, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tail->tmem;
+  pdl_wait();
 
   if (warp == 0) {
     if (lane == 0) {
@@ -446,6 +448,8 @@ __global__ void __launch_bounds__(320, 1)
       if (lane == 0) mbar_arrive(&tail->tempty[acc]);
     }
   }
+  for (int64_t t = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; t < a.T; t += (int64_t)gridDim.x * blockDim.x)
+    if (a.ids[t] < -1 || a.ids[t] >= a.adapters) dev_fail(a.st, kDevBadAdapter, 0xE02u);
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {
@@ -469,8 +473,7 @@ cudaError_t launch_product(const LoraArgs &a, const int *lists, const __half *Wd
   const PrefillArgs p = {a.ids, lists, a.T, a.out, a.ldy, a.adapters, a.rank, (int)((a.T + BM - 1) / BM),
                          (int)((a.out + BN - 1) / BN), (int)(a.in / PK), a.Y, a.st, a.max_polls};
   const int64_t tiles = (int64_t)p.num_m * p.num_n;
-  lora_gemm_kernel<BM, BN><<<(unsigned)i64min(tiles, num_sms), 320, C::kBytes, stream>>>(x, w, u, b, p);
-  return cudaGetLastError();
+  return launch_after(lora_gemm_kernel<BM, BN>, i64min(tiles, num_sms), 320, C::kBytes, stream, x, w, u, b, p);
 }
 }  // namespace
 
@@ -492,23 +495,12 @@ cudaError_t launch_lora_prefill(const LoraArgs &a, int num_sms, cudaStream_t str
   __half *Wd = reinterpret_cast<__half *>(reinterpret_cast<uint8_t *>(lists) +
                                           up(sizeof(int) * (size_t)((a.T + 127) / 128) * 129));
   const int bm = lora_prefill_bm(a.T, a.out, num_sms);
-  cudaError_t e = cudaMemsetAsync(a.st, 0, sizeof(DevStatus), stream);
-  if (e != cudaSuccess) return e;
   const int64_t n_shrink = (a.T + kShT - 1) / kShT, n_lists = (a.T + bm - 1) / bm;
   const int64_t n_deq = ((a.out + kWideOut - 1) / kWideOut) * (a.in / kWideIn);
   if (n_shrink + n_lists > INT32_MAX || n_deq > INT32_MAX) return cudaErrorInvalidValue;
-  lora_shrink_mma_kernel<<<(unsigned)(n_shrink + n_lists), kShThreads, 0, stream>>>(a, (int)n_shrink, bm, lists);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)n_deq);
-  cfg.blockDim = dim3(256);
-  cfg.stream = stream;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  if ((e = cudaLaunchKernelEx(&cfg, lora_dequant_kernel, a, Wd)) != cudaSuccess) return e;
+  cudaError_t e = launch_after(lora_shrink_mma_kernel, n_shrink + n_lists, kShThreads, 0, stream, a, (int)n_shrink, bm, lists);
+  if (e == cudaSuccess) e = launch_after(lora_dequant_kernel, n_deq, 256, 0, stream, a, Wd);
+  if (e != cudaSuccess) return e;
   return bm == 256 ? launch_product<256, 256>(a, lists, Wd, num_sms, stream)
                    : launch_product<128, 128>(a, lists, Wd, num_sms, stream);
 }

@@ -706,7 +706,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<V>::kBlocks)
 }
 
 // The status word and the counters, 512 bytes
-__global__ void moe_clear_kernel(uint4 *ws) { ws[threadIdx.x] = make_uint4(0u, 0u, 0u, 0u); }
+__global__ void moe_clear_kernel(uint4 *ws) {
+  pdl_wait();
+  ws[threadIdx.x] = make_uint4(0u, 0u, 0u, 0u);
+}
 
 template <int V, int SHIFT>
 cudaError_t go(const MoeArgs &a, int num_sms, cudaStream_t stream) {
@@ -739,8 +742,7 @@ cudaError_t go_group(const MoeArgs &a, int num_sms, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t launch_moe(const MoeArgs &a, int num_sms, cudaStream_t stream) {
-  moe_clear_kernel<<<1, 32, 0, stream>>>(reinterpret_cast<uint4 *>(a.st));
-  const cudaError_t e = cudaGetLastError();
+  const cudaError_t e = launch_after(moe_clear_kernel, 1, 32, 0, stream, reinterpret_cast<uint4 *>(a.st));
   if (e != cudaSuccess) return e;
   return a.T <= 8 ? go_group<1>(a, num_sms, stream) : go_group<2>(a, num_sms, stream);
 }

@@ -28,6 +28,28 @@ inline cudaError_t allow_smem(K kernel, size_t bytes, std::atomic<bool> (&done)[
   return e;
 }
 
+// A kernel launched by launch_after is set up while the kernel before it on the
+// stream ends; pdl_wait() returns when that one has ended with all its results
+// visible, and comes before the first access to memory.  pdl_launch() lets the next
+// such kernel start.
+__device__ __forceinline__ void pdl_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+template <class... P, class... A>
+inline cudaError_t launch_after(void (*kernel)(P...), int64_t blocks, int threads, size_t smem, cudaStream_t stream,
+                                const A &...args) {
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)blocks);
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 struct LoraArgs {
   const __half *X;
   int64_t T, in, ldx;
