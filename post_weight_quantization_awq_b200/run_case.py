@@ -54,6 +54,8 @@ def serving(a) -> int:
         A, B = normal(a.adapters, a.rank, a.inn, std=a.inn ** -0.5), normal(a.adapters, a.out, a.rank, std=0.02)
         c = torch.full((a.adapters,), 0.5, device="cuda")
         ids = torch.randint(-1, a.adapters, (T,), generator=gen, dtype=torch.int32).cuda()
+        if T > 64:  # prompts: a request's tokens stand together
+            ids = ids.sort().values
         Y = torch.empty((T, a.out), dtype=torch.float16, device="cuda")
         ws = torch.empty(awq.awq_w4a16_lora_workspace_size(T, a.inn, a.out, a.rank, cfg), dtype=torch.uint8,
                          device="cuda")
