@@ -24,6 +24,11 @@
 //   down     the same over hidden's tiles and all met experts;
 //   combine  a token's experts' sums, weighted with p in fp32, one rounding.
 // Sums are added in an order fixed by the sizes and the routing alone.
+//
+// Measured, 4096 -> 11008 and two of eight experts: 56 us for 1 token (139 MB of
+// words and steps; 5.3 TB/s while gate|up streams, the rest are phases that wait
+// for each other), 244 us for 64 (557 MB; 252-314 cycles for 16 rows x 512 outputs
+// by 8 warps, bound by their instructions and the latency of mma.sync).
 #include <climits>
 #include <cuda_runtime.h>
 #include <type_traits>
@@ -235,8 +240,8 @@ __device__ void router(const MoeArgs &a) {
   }
 }
 
-// Time of a unit of 128 input rows by its token tiles, measured: 174, 236 and
-// 300 cycles a step for 1, 2 and 3 tiles with 8 warps on an SM.
+// Time of a unit of 128 input rows by its token tiles, measured: 196, 252 and
+// 314 cycles a step for 1, 2 and 3 tiles with 8 warps on an SM.
 __host__ __device__ constexpr int unit_cost(int n) { return n <= 8 ? 3 : n <= 16 ? 4 : 5; }
 
 // The experts' token lists, and the entries.  Every block makes its own: an
