@@ -160,7 +160,9 @@ class _Lib:
         return _Lib._lib
 
     def __getattr__(self, name):
-        return getattr(self._get(), name)
+        fn = getattr(self._get(), name)
+        setattr(self, name, fn)  # found without this call the next time
+        return fn
 
     def __getitem__(self, name):
         return self._get()[name]
@@ -333,6 +335,22 @@ def awq_w4a16_workspace_size(T: int, inn: int, out: int, cfg: AwqConfig) -> int:
     return int(n)
 
 
+_serving = None
+
+
+def _current(stream):
+    """(fp16, int32, fp32, uint8, the current device, the stream's handle), without the
+    0.2 us of an import statement."""
+    global _serving
+    if _serving is None:
+        import torch
+        _serving = (torch.float16, torch.int32, torch.float32, torch.uint8, torch._C._cuda_getDevice,
+                    torch._C._cuda_getCurrentRawStream)
+    f16, i32, f32, u8, device, raw_stream = _serving
+    dev = device()
+    return f16, i32, f32, u8, dev, raw_stream(dev) if stream is None else int(stream)
+
+
 def _refuse(func: str, dev: int, rows, dense) -> None:
     """Names the tensor for which a serving call was refused: rows and dense are
     (name, tensor or None, dtype, shape), the first with rows that may lie apart."""
@@ -358,9 +376,7 @@ def awq_w4a16_lora_gemm(X, qweight, qzeros, scales, cfg: AwqConfig, A, B, c, ada
     """Y [T, out] fp16 = X times the packed weights, plus for each token its
     adapter's c_a (X A_a^T) B_a^T: A fp16 [n, rank, in], B fp16 [n, out, rank],
     c fp32 [n], adapter int32 [T] (-1: none)."""
-    import torch
-    f16, i32, f32 = torch.float16, torch.int32, torch.float32
-    dev = torch._C._cuda_getDevice()
+    f16, i32, f32, _, dev, stream = _current(stream)
     T, inn = X.shape
     n, rank, _ = A.shape
     out, g = Y.shape[-1], cfg.group_size
@@ -383,7 +399,7 @@ def awq_w4a16_lora_gemm(X, qweight, qzeros, scales, cfg: AwqConfig, A, B, c, ada
     _check("awq_w4a16_lora_gemm", LIB.awq_w4a16_lora_gemm(
         X.data_ptr(), T, inn, xs[0], qweight.data_ptr(), qzeros.data_ptr(), scales.data_ptr(),
         out, ctypes.byref(cfg), A.data_ptr(), B.data_ptr(), c.data_ptr(), n, rank, adapter.data_ptr(),
-        Y.data_ptr(), ys[0], ws.data_ptr(), ws.numel() * ws.element_size(), _stream(stream)))
+        Y.data_ptr(), ys[0], ws.data_ptr(), ws.numel() * ws.element_size(), stream))
 
 
 def awq_w4a16_lora_workspace_size(T: int, inn: int, out: int, rank: int, cfg: AwqConfig) -> int:
@@ -399,9 +415,7 @@ def awq_w4a16_moe(X, router, gate_up, down, cfg: AwqConfig, renormalize: bool, m
     fp16 [E, hidden], gate_up and down (qweight, qzeros, scales) with a leading
     expert axis, mask uint8 [T] or None; outputs Y [T, hidden] fp16, ids int32
     and weights fp32 [T, top_k]."""
-    import torch
-    f16, i32, f32 = torch.float16, torch.int32, torch.float32
-    dev = torch._C._cuda_getDevice()
+    f16, i32, f32, u8, dev, stream = _current(stream)
     gq, gz, gs = gate_up
     dq, dz, ds = down
     T, hidden = X.shape
@@ -421,7 +435,7 @@ def awq_w4a16_moe(X, router, gate_up, down, cfg: AwqConfig, renormalize: bool, m
             and gz.numel() * 4 == E * (hidden // g) * inter and ds.numel() == E * (inter // g) * hidden
             and dz.numel() * 8 == E * (inter // g) * hidden and Y.numel() == T * hidden
             and ids.numel() == T * top_k and weights.numel() == T * top_k
-            and (mask is None or (mask.get_device() == dev and mask.dtype is torch.uint8 and mask.is_contiguous()
+            and (mask is None or (mask.get_device() == dev and mask.dtype is u8 and mask.is_contiguous()
                                   and mask.numel() == T))):
         _refuse("awq_w4a16_moe", dev, (("X", X, f16, (T, hidden)), ("Y", Y, f16, (T, hidden))), (
             ("router", router, f16, (E, hidden)),
@@ -429,13 +443,13 @@ def awq_w4a16_moe(X, router, gate_up, down, cfg: AwqConfig, renormalize: bool, m
             ("gate_up qzeros", gz, i32, (E, hidden // g, inter // 4)),
             ("gate_up scales", gs, f16, (E, hidden // g, 2 * inter)),
             ("down qweight", dq, i32, (E, inter, hidden // 8)), ("down qzeros", dz, i32, (E, inter // g, hidden // 8)),
-            ("down scales", ds, f16, (E, inter // g, hidden)), ("mask", mask, torch.uint8, (T,)),
+            ("down scales", ds, f16, (E, inter // g, hidden)), ("mask", mask, u8, (T,)),
             ("ids", ids, i32, (T, top_k)), ("weights", weights, f32, (T, top_k)), ("ws", ws, ws.dtype, ws.shape)))
     _check("awq_w4a16_moe", LIB.awq_w4a16_moe(
         X.data_ptr(), T, hidden, xs[0], None if mask is None else mask.data_ptr(), router.data_ptr(), E, top_k,
         1 if renormalize else 0, gq.data_ptr(), gz.data_ptr(), gs.data_ptr(), inter, dq.data_ptr(), dz.data_ptr(),
         ds.data_ptr(), ctypes.byref(cfg), Y.data_ptr(), ys[0], ids.data_ptr(), weights.data_ptr(), ws.data_ptr(),
-        ws.numel() * ws.element_size(), _stream(stream)))
+        ws.numel() * ws.element_size(), stream))
 
 
 def awq_w4a16_moe_workspace_size(T: int, hidden: int, inter: int, n_experts: int, top_k: int,
@@ -450,8 +464,8 @@ def awq_block_norm(R, V, post, gate, c: float, pre, eps: float, R_out, N_out, st
     """R_out = R + c gate rmsnorm(V) post and N_out = rmsnorm(R_out) pre over
     fp16 rows [T, d]; V, post, gate ([T, d] or [d]), pre and one of the outputs
     may be None."""
-    import torch
-    f16, dev, none = torch.float16, torch._C._cuda_getDevice(), (0, 1)
+    f16, _, _, _, dev, stream = _current(stream)
+    none = (0, 1)
     shape = T, d = R.shape
     by_token = gate is not None and gate.dim() == 2
     ldr, r1 = R.stride()
@@ -478,7 +492,7 @@ def awq_block_norm(R, V, post, gate, c: float, pre, eps: float, R_out, N_out, st
         R.data_ptr(), ldr, None if V is None else V.data_ptr(), ldv, T, d, None if post is None else post.data_ptr(),
         None if gate is None else gate.data_ptr(), ldg, c, None if pre is None else pre.data_ptr(), eps,
         None if R_out is None else R_out.data_ptr(), ldro, None if N_out is None else N_out.data_ptr(), ldno,
-        _stream(stream)))
+        stream))
 
 
 def awq_device_status(ws, stream=None) -> None:
