@@ -9,15 +9,16 @@
 // dependent launch) lora_dequant_kernel dequantises W once, in x out work instead
 // of once per token tile.
 // lora_gemm_kernel: the low-rank part is K steps like any other, appended to a
-// tile's K loop for each adapter on its list: A is U's rows, of which the
-// waiting epilogue warps zero those of other adapters in shared memory, B is
-// B_a's rows by TMA.  No partial result leaves the accumulators, so the whole is
+// tile's K loop for each adapter on its list: A is U's rows, which the waiting
+// epilogue warps write to shared memory from registers, those of other adapters as
+// zeros, B is B_a's rows by TMA.  No partial result leaves the accumulators, so the whole is
 // rounded once, and the part costs rank / in of the product for rows that stand
 // together by adapter.
 //
-// Measured, replayed: 146 us for 1531 tokens on 4096 x 11008 at rank 32 (the product
-// 124 us = 1.13 PFLOP/s, two rounds of 256 x 256 tiles on 148 SMs), 246 us for 8192 on
-// 4096 x 4096 at rank 16 (223 us = 1.24 PFLOP/s); bound by the tensor cores.
+// Measured, replayed: 138 us for 1531 tokens on 4096 x 11008 at rank 32 (the product
+// 109, two rounds of 256 x 256 tiles on 148 SMs, 735 ns a step of 64 columns = 1.69
+// PFLOP/s while a tile is at work), 245 us for 8192 on 4096 x 4096 at rank 16 (product
+// 211); bound by the tensor cores at the clock they hold.
 #include <cuda.h>
 
 #include "awq_launch.h"
@@ -190,7 +191,7 @@ __global__ void __launch_bounds__(256) lora_dequant_kernel(const LoraArgs a, __h
 
 // ---------------------------------------------------------------------------
 // Product.  One block per SM, persistent over BM x BN tiles: warp 0 TMA, warp 1
-// MMA, warps 2..9 zero the U rows of other adapters and store the tile.
+// MMA, warps 2..9 write the adapters' A operands and store the tile.
 // ---------------------------------------------------------------------------
 constexpr int PK = 64;
 constexpr uint32_t kPDrain = 1u << 22;
@@ -210,7 +211,7 @@ struct PCfg {
 template <int STAGES>
 struct __align__(8) PTail {
   uint64_t full[STAGES], empty[STAGES];  // words of X and Wd; read
-  uint64_t ufull[STAGES], masked[STAGES];  // U and B_a: landed; U's other rows zeroed
+  uint64_t ufull[STAGES], masked[STAGES];  // B_a landed; U written
   uint64_t tfull[2], tempty[2], done;
   uint32_t tmem;
   int abort_flag;
@@ -224,6 +225,7 @@ __device__ __forceinline__ void p_abort(PTail<STAGES> *t, DevStatus *st, uint32_
 
 struct PrefillArgs {
   const int32_t *ids;
+  const __half *U;
   const int *lists;
   int64_t T, out, ldy;
   int adapters, rank, num_m, num_n, num_kb;
@@ -242,7 +244,7 @@ __device__ __forceinline__ void p_tile(int tile, int num_m, int num_n, int &m, i
 template <int BM, int BN>
 __global__ void __launch_bounds__(320, 1)
     lora_gemm_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
-                     const __grid_constant__ CUtensorMap tmU, const __grid_constant__ CUtensorMap tmB,
+                     const __grid_constant__ CUtensorMap tmB,
                      const __grid_constant__ PrefillArgs a) {
   using C = PCfg<BM, BN>;
   constexpr int STAGES = C::kStages;
@@ -272,7 +274,6 @@ __global__ void __launch_bounds__(320, 1)
     fence_mbar_init();
     tma_prefetch_desc(&tmX);
     tma_prefetch_desc(&tmW);
-    tma_prefetch_desc(&tmU);
     tma_prefetch_desc(&tmB);
   }
   if (warp == 1) {
@@ -303,14 +304,13 @@ __global__ void __launch_bounds__(320, 1)
           }
           const bool low = k >= a.num_kb;
           uint64_t *bar = low ? &tail->ufull[s] : &tail->full[s];
-          mbar_arrive_expect_tx(bar, C::kA + C::kB);
+          mbar_arrive_expect_tx(bar, low ? C::kB : C::kA + C::kB);
           if (!low) {
             tma_load_2d(sA + s * C::kA, &tmX, bar, k * PK, m * BM);
             tma_load_2d(sB + s * C::kB, &tmW, bar, k * PK, n * BN);
           } else {
             const int e = (k - a.num_kb) / rsteps, r = (k - a.num_kb) % rsteps;
             // rows past this adapter's outputs are the next one's: their columns are not stored
-            tma_load_2d(sA + s * C::kA, &tmU, bar, r * PK, m * BM);
             tma_load_2d(sB + s * C::kB, &tmB, bar, r * PK, (int)(list[1 + e] * a.out + n * BN));
           }
           (low ? uphase : fphase) ^= 1u << s;
@@ -395,25 +395,38 @@ __global__ void __launch_bounds__(320, 1)
       if (count) {
         const int64_t row = (int64_t)m * BM + tid;  // tid >= BM: no row
         const int id = tid < BM && row < a.T ? a.ids[row] : -1;
-        for (int e = 0; e < count * rsteps && ok; ++e, ++step) {
-          const int s = step % STAGES;
-          int got = 1;
-          if (lane == 0) got = mbar_wait_long(&tail->ufull[s], (uphase >> s) & 1u, a.max_polls, abort_flag);
-          uphase ^= 1u << s;
-          got = __shfl_sync(0xffffffffu, got, 0);
-          if (!got) {
-            if (lane == 0) p_abort(tail, a.st, 0xE33u);
-            ok = false;
-            break;
-          }
-          if (tid < BM && id != list[1 + e / rsteps]) {
-            uint4 *r = reinterpret_cast<uint4 *>(sA + s * C::kA + tid * (PK * 2));
+        const uint4 *u = reinterpret_cast<const uint4 *>(a.U + row * a.rank);
+        const auto chunk = [&](int i) {  // 8 values of this row's U
+          return id >= 0 && 8 * i < a.rank ? __ldg(u + i) : make_uint4(0u, 0u, 0u, 0u);
+        };
+        uint4 first[PK / 8];  // loaded once for all adapters of the tile
+        int next = list[1];
 #pragma unroll
-            for (int i = 0; i < PK / 8; ++i) r[(i + tid) & 7] = make_uint4(0u, 0u, 0u, 0u);
+        for (int i = 0; i < PK / 8; ++i) first[i] = chunk(i);
+        for (int e = 0; e < count && ok; ++e) {
+          const int mine = id == next;
+          if (e + 1 < count) next = list[2 + e];
+          for (int r = 0; r < rsteps; ++r, ++step) {
+            const int s = step % STAGES;
+            int got = 1;
+            if (lane == 0) got = mbar_wait_long(&tail->ufull[s], (uphase >> s) & 1u, a.max_polls, abort_flag);
+            uphase ^= 1u << s;
+            got = __shfl_sync(0xffffffffu, got, 0);
+            if (!got) {
+              if (lane == 0) p_abort(tail, a.st, 0xE33u);
+              ok = false;
+              break;
+            }
+            if (tid < BM) {
+              uint4 *d = reinterpret_cast<uint4 *>(sA + s * C::kA + tid * (PK * 2));
+#pragma unroll
+              for (int i = 0; i < PK / 8; ++i)  // 128-byte swizzle
+                d[i ^ (tid & 7)] = !mine ? make_uint4(0u, 0u, 0u, 0u) : r == 0 ? first[i] : chunk(PK / 8 * r + i);
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&tail->masked[s]);
           }
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&tail->masked[s]);
         }
         if (!ok) break;
       }
@@ -482,22 +495,21 @@ cudaError_t launch_product(const LoraArgs &a, const int *lists, const __half *Wd
   static_assert(sizeof(PTail<C::kStages>) <= 512 && C::kBytes <= 232448, "shared memory");
   cudaError_t e = allow_smem(lora_gemm_kernel<BM, BN>, C::kBytes, done);
   if (e != cudaSuccess) return e;
-  CUtensorMap x, w, u, b;
+  CUtensorMap x, w, b;
   if ((e = make_tmap_f16_box(&x, a.X, a.T, a.in, a.ldx, PK, BM)) != cudaSuccess) return e;
   if ((e = make_tmap_f16_box(&w, Wd, a.out, a.in, a.in, PK, BN)) != cudaSuccess) return e;
-  if ((e = make_tmap_f16_box(&u, a.U, a.T, a.rank, a.rank, PK, BM)) != cudaSuccess) return e;
   if ((e = make_tmap_f16_box(&b, a.B, (int64_t)a.adapters * a.out, a.rank, a.rank, PK, BN)) != cudaSuccess) return e;
-  const PrefillArgs p = {a.ids, lists, a.T, a.out, a.ldy, a.adapters, a.rank, (int)((a.T + BM - 1) / BM),
+  const PrefillArgs p = {a.ids, reinterpret_cast<const __half *>(a.U), lists, a.T, a.out, a.ldy, a.adapters, a.rank, (int)((a.T + BM - 1) / BM),
                          (int)((a.out + BN - 1) / BN), (int)(a.in / PK), a.Y, a.st, a.max_polls};
   const int64_t tiles = (int64_t)p.num_m * p.num_n;
-  return launch_after(lora_gemm_kernel<BM, BN>, i64min(tiles, num_sms), 320, C::kBytes, stream, x, w, u, b, p);
+  return launch_after(lora_gemm_kernel<BM, BN>, i64min(tiles, num_sms), 320, C::kBytes, stream, x, w, b, p);
 }
 }  // namespace
 
 // Token rows of a tile of the product.  A step of 64 columns of a 256 x 256 tile takes
 // 735 ns (the tensor cores' rate at the clock they hold), one of a 128 x 128 tile 490
 // (L2 feeds 148 SMs at 9.7 TB/s), and the SMs work in rounds of tiles: 785 tokens on 2816
-// x 6176 take 92 us in three rounds of the small tiles and 58 in one of the large.
+// x 6176 take 92 us in three rounds of the small tiles and 48 in one of the large.
 int lora_prefill_bm(int64_t T, int64_t out, int num_sms) {
   const auto rounds = [&](int64_t b) { return (((T + b - 1) / b) * ((out + b - 1) / b) + num_sms - 1) / num_sms; };
   return rounds(256) * 735 <= rounds(128) * 490 ? 256 : 128;
