@@ -95,10 +95,21 @@ __device__ __forceinline__ void shrink_pass(float (&acc)[4][4], const __half *x0
   }
 }
 
-// U of 16 tokens for each adapter among them.  `split` of the 16 warps share an
-// adapter's K, so that each has at least four steps of it, and the others take
-// other adapters.
-__device__ void shrink_block(const LoraArgs &a, int64_t t0, uint8_t *smem) {
+// The rank rows of an adapter go in passes of 32, then 16 and 8: the i-th one's first
+// row and its rows.
+__device__ __forceinline__ int2 shrink_rows(int rank, int i) {
+  const int full = rank / 32, left = rank % 32;
+  if (i < full) return make_int2(32 * i, 32);
+  if (i == full && left >= 16) return make_int2(32 * full, 16);
+  return make_int2(rank - 8, 8);
+}
+__host__ __device__ constexpr int shrink_passes(int rank) { return rank / 32 + (rank / 16 & 1) + (rank / 8 & 1); }
+
+// U of 16 tokens for the adapters among them: items of an adapter and a pass.
+// `split` of the 16 warps share an item's K, so that each has at least four steps of
+// it, and the others take other items.  `shares` blocks deal the items of the same
+// tokens out between them (this is the `share`-th).
+__device__ void shrink_block(const LoraArgs &a, int64_t t0, int share, int shares, uint8_t *smem) {
   float *red = reinterpret_cast<float *>(smem);  // [16][16][kShR + 1]
   int *ids = reinterpret_cast<int *>(smem + kShWarps * kShT * (kShR + 1) * 4);
   int *list = ids + 256, *scratch = list + 256;
@@ -109,7 +120,7 @@ __device__ void shrink_block(const LoraArgs &a, int64_t t0, uint8_t *smem) {
     ids[tid] = id >= 0 && id < a.adapters ? id : -1;
   }
   __syncthreads();
-  const int count = adapter_list(ids, n, list, scratch);
+  const int passes = shrink_passes(a.rank), items = adapter_list(ids, n, list, scratch) * passes;
   const int steps = (int)(a.in / 32);
   int split = kShWarps;
   while (split > 1 && split * 4 > steps) split /= 2;
@@ -117,58 +128,57 @@ __device__ void shrink_block(const LoraArgs &a, int64_t t0, uint8_t *smem) {
   const int s0 = steps * part / split, s1 = steps * (part + 1) / split;
   // rows g and g + 8 (the last one again past the end)
   const __half *x0 = a.X + (t0 + min(g, n - 1)) * a.ldx + 8 * q, *x1 = a.X + (t0 + min(g + 8, n - 1)) * a.ldx + 8 * q;
-  for (int j0 = 0; j0 < count; j0 += teams) {
-    const bool works = j0 + team < count;
-    for (int r0 = 0, rows; r0 < a.rank; r0 += rows) {
-      const int left = a.rank - r0;
-      rows = left >= 32 ? 32 : left >= 16 ? 16 : 8;
-      if (works) {
-        float acc[4][4];
+  for (int i0 = share * teams; i0 < items; i0 += shares * teams) {
+    if (i0 + team < items) {
+      const int j = (i0 + team) / passes;
+      const int2 rows = shrink_rows(a.rank, i0 + team - j * passes);
+      float acc[4][4];
 #pragma unroll
-        for (int x = 0; x < 4; ++x)
+      for (int x = 0; x < 4; ++x)
 #pragma unroll
-          for (int c = 0; c < 4; ++c) acc[x][c] = 0.0f;
-        const __half *ar = a.A + ((int64_t)list[j0 + team] * a.rank + r0 + g) * a.in + 8 * q;
-        if (rows == 32)
-          shrink_pass<4>(acc, x0, x1, ar, a.in, s0, s1);
-        else if (rows == 16)
-          shrink_pass<2>(acc, x0, x1, ar, a.in, s0, s1);
-        else
-          shrink_pass<1>(acc, x0, x1, ar, a.in, s0, s1);
+        for (int c = 0; c < 4; ++c) acc[x][c] = 0.0f;
+      const __half *ar = a.A + ((int64_t)list[j] * a.rank + rows.x + g) * a.in + 8 * q;
+      if (rows.y == 32)
+        shrink_pass<4>(acc, x0, x1, ar, a.in, s0, s1);
+      else if (rows.y == 16)
+        shrink_pass<2>(acc, x0, x1, ar, a.in, s0, s1);
+      else
+        shrink_pass<1>(acc, x0, x1, ar, a.in, s0, s1);
 #pragma unroll
-        for (int x = 0; x < 4; ++x)
+      for (int x = 0; x < 4; ++x)
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
-            red[(warp * kShT + g + 8 * (c >> 1)) * (kShR + 1) + 8 * x + 2 * q + (c & 1)] = acc[x][c];
-      }
-      __syncthreads();
-      for (int i = tid; i < min(teams, count - j0) * kShT * rows; i += kShThreads) {
-        const int m = i / (kShT * rows), t = i / rows % kShT, r = i % rows, id = list[j0 + m];
-        if (t >= n || ids[t] != id) continue;
-        float v = 0.0f;
-        for (int w = 0; w < split; ++w) v += red[((m * split + w) * kShT + t) * (kShR + 1) + r];
-        reinterpret_cast<__half *>(a.U)[(t0 + t) * a.rank + r0 + r] = __float2half_rn(a.c[id] * v);
-      }
-      __syncthreads();
+        for (int c = 0; c < 4; ++c)
+          red[(warp * kShT + g + 8 * (c >> 1)) * (kShR + 1) + 8 * x + 2 * q + (c & 1)] = acc[x][c];
     }
+    __syncthreads();
+    for (int i = tid; i < min(teams, items - i0) * kShT * kShR; i += kShThreads) {
+      const int m = i / (kShT * kShR), t = i / kShR % kShT, r = i % kShR, j = (i0 + m) / passes, id = list[j];
+      const int2 rows = shrink_rows(a.rank, i0 + m - j * passes);
+      if (r >= rows.y || t >= n || ids[t] != id) continue;
+      float v = 0.0f;
+      for (int w = 0; w < split; ++w) v += red[((m * split + w) * kShT + t) * (kShR + 1) + r];
+      reinterpret_cast<__half *>(a.U)[(t0 + t) * a.rank + rows.x + r] = __float2half_rn(a.c[id] * v);
+    }
+    __syncthreads();
   }
 }
 
 constexpr int kShrinkSmem = kShWarps * kShT * (kShR + 1) * 4 + (256 + 256 + 16) * 4;
 
-// Blocks [0, n_shrink): U; the rest: the lists of `bm`-row tiles,
+// Blocks [0, n_shrink shares): U; the rest: the lists of `bm`-row tiles,
 // lists[tile][bm + 1] = count, ids.
-__global__ void __launch_bounds__(kShThreads) lora_shrink_mma_kernel(const LoraArgs a, int n_shrink, int bm, int *lists) {
+__global__ void __launch_bounds__(kShThreads)
+    lora_shrink_mma_kernel(const LoraArgs a, int n_shrink, int shares, int bm, int *lists) {
   __shared__ __align__(16) uint8_t smem[kShrinkSmem];
   pdl_wait();
   pdl_launch();
   if (blockIdx.x == 0 && threadIdx.x == 0) *a.st = DevStatus{};
   int64_t b = blockIdx.x;
-  if (b < n_shrink) {
-    shrink_block(a, b * kShT, smem);
+  if (b < (int64_t)n_shrink * shares) {
+    shrink_block(a, b % n_shrink * kShT, (int)(b / n_shrink), shares, smem);
     return;
   }
-  b -= n_shrink;
+  b -= (int64_t)n_shrink * shares;
   int *ids = reinterpret_cast<int *>(smem), *list = ids + 256, *scratch = list + 256;
   const int64_t t0 = b * bm;
   const int n = (int)i64min(bm, a.T - t0), tid = threadIdx.x;
@@ -530,8 +540,13 @@ cudaError_t launch_lora_prefill(const LoraArgs &a, int num_sms, cudaStream_t str
   const int bm = lora_prefill_bm(a.T, a.out, num_sms);
   const int64_t n_shrink = (a.T + kShT - 1) / kShT, n_lists = (a.T + bm - 1) / bm;
   const int64_t n_deq = ((a.out + kWideOut - 1) / kWideOut) * (a.in / kWideIn);
-  if (n_shrink + n_lists > INT32_MAX || n_deq > INT32_MAX) return cudaErrorInvalidValue;
-  cudaError_t e = launch_after(lora_shrink_mma_kernel, n_shrink + n_lists, kShThreads, 0, stream, a, (int)n_shrink, bm, lists);
+  // few tokens: as many blocks for each 16 as fill the SMs and as there can be items
+  // (785 tokens with nine mixed adapters: 19 us, 31 with one)
+  const int64_t most = i64min(kShT, a.adapters) * shrink_passes(a.rank);
+  const int shares = (int)i64max(1, i64min(num_sms / n_shrink, most));
+  if (n_shrink * shares + n_lists > INT32_MAX || n_deq > INT32_MAX) return cudaErrorInvalidValue;
+  cudaError_t e = launch_after(lora_shrink_mma_kernel, n_shrink * shares + n_lists, kShThreads, 0, stream, a, (int)n_shrink, shares, bm,
+                               lists);
   if (e == cudaSuccess) e = launch_after(lora_dequant_kernel, n_deq, 256, 0, stream, a, Wd);
   if (e != cudaSuccess) return e;
   return bm == 256 ? launch_product<256, 256>(a, lists, Wd, num_sms, stream)

@@ -113,7 +113,6 @@ struct MoeArgs {
 struct MoeLayout {
   size_t logits, H, sums, dn_sums, partial, dn_partial, end;
 };
-__host__ __device__ constexpr int64_t i64max_(int64_t a, int64_t b) { return a > b ? a : b; }
 MoeLayout moe_layout(int64_t T, int64_t hidden, int64_t inter, int64_t experts, int64_t top_k, int num_sms);
 cudaError_t launch_moe(const MoeArgs &a, int num_sms, cudaStream_t stream);
 
