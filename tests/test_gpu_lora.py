@@ -255,3 +255,40 @@ def test_lora_tensors_the_call_cannot_read_are_refused():
                                     a["ws"])
         assert e.value.status_name == "AWQ_ERR_INVALID_ARG", name
     assert bool((ok["Y"] == 7.0).all())
+
+
+@pytest.mark.parametrize("T,inn,out,rank,n,group", [
+    # as many tiles as make groups of 16 tokens fill the SMs, and more, where all tokens stay in one block
+    (20, 256, 12288, 24, 3, 128), (45, 128, 12288, 8, 5, 64), (64, 192, 12288, 16, 2, 32),
+    (20, 128, 39936, 8, 3, 128), (45, 128, 32768, 40, 7, 128), (64, 128, 32768, 8, 4, 64), (45, 64, 39936, 8, 2, 32),
+    # past 64 tokens: few rows and many tiles, one row of tiles that is not full, ranks of several passes
+    (70, 64, 39936, 8, 3, 64), (129, 192, 8224, 120, 9, 32), (257, 128, 4096, 56, 48, 128), (90, 64, 32, 256, 30, 64)])
+def test_lora_many_tiles_and_passes(T, inn, out, rank, n, group):
+    X, packed, A, B, c, ids = _case(T, inn, out, rank, n, group, T + out)
+    Yg = _run(X, packed, group, A, B, c, ids)
+    Yo, mags = lora(X, packed, group, A, B, c, ids)
+    err = np.abs(Yg.astype(np.float64) - Yo)
+    assert np.all(err <= lora_tolerance(Yo, mags, inn, rank, rounded=T > 64)), err.max()
+
+
+@pytest.mark.parametrize("T", [2, 12, 40, 150])
+def test_lora_two_graphs_share_a_workspace(T):
+    """Two captured calls of different inputs on one workspace, replayed in turn."""
+    cfg = awq.AwqConfig.make()
+    d = lambda a: torch.from_numpy(np.ascontiguousarray(a)).cuda()  # noqa: E731
+    ws = torch.empty(awq.awq_w4a16_lora_workspace_size(T, 512, 544, 16, cfg), dtype=torch.uint8, device="cuda")
+    graphs = []
+    for seed in (T, T + 1):
+        X, packed, A, B, c, ids = _case(T, 512, 544, 16, 4, 128, seed)
+        Y = torch.zeros((T, 544), dtype=torch.float16, device="cuda")
+        t = [d(X), *map(d, packed)], [d(A), d(B), d(c), d(ids), Y]
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            awq.awq_w4a16_lora_gemm(*t[0], cfg, *t[1], ws)
+        graphs.append((g, t, _run(X, packed, 128, A, B, c, ids)))
+    for g, t, want in graphs * 3:
+        t[1][-1].zero_()
+        g.replay()
+        assert np.array_equal(t[1][-1].cpu().numpy().view(np.uint16), want.view(np.uint16))
+    awq.awq_device_status(ws)
+    del g, graphs

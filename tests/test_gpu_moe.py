@@ -239,3 +239,32 @@ def test_moe_tensors_the_call_cannot_read_are_refused():
             a.call()
         assert e.value.status_name == "AWQ_ERR_INVALID_ARG", change
         assert bool((a.Y == 7.0).all()) or "Y" in change
+
+
+@pytest.mark.parametrize("T", [1, 6, 30])
+def test_moe_two_graphs_share_a_workspace(T):
+    """Two captured layers of different inputs on one workspace, replayed in turn."""
+    layers = []
+    for seed in (T, T + 50):
+        X, router, gu, dn = _case(T, 256, 192, 6, 64, seed)
+        a = _Layer(X, router, gu, dn, 64, 2, True)
+        want = a.run()
+        if layers:
+            a.ws = layers[0][0].ws
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            a.call()
+        layers.append((a, g, want))
+    for a, g, want in layers * 3:
+        a.Y.zero_()
+        g.replay()
+        assert np.array_equal(a.Y.cpu().numpy(), want[0]) and np.array_equal(a.ids.cpu().numpy(), want[1])
+    awq.awq_device_status(layers[0][0].ws)
+    del g, layers
+
+
+def test_moe_choices_that_are_not_a_power_of_two():
+    """3, 6 and 11 experts a token: lanes without a choice in the last sum."""
+    for k in (3, 6, 11):
+        X, router, gu, dn = _case(5, 192, 128, 12, 64, k)
+        _check(_Layer(X, router, gu, dn, 64, k, False).run(), X, router, gu, dn, 64, k, False)
