@@ -3,12 +3,12 @@
 //   Y[t][o] = RN16( sum_j X[t][j] (q - z) s  +  c_a sum_r U[t][r] B_a[o][r] ),
 //   U[t][r] = sum_j X[t][j] A_a[r][j],  a = ids[t]  (-1: no adapter)
 //
-// For a handful of tokens one launch does it all: the blocks of a cluster compute
-// c_a U over their input rows while the first words travel, and add it through
-// distributed shared memory.  Where that would read more of A than of the words
-// (every output tile's cluster reads all of it), lora_shrink_kernel computes U
-// first and lets its successor start at once (programmatic dependent launch),
-// which meanwhile streams the words and waits for U only before its epilogue.
+// lora_shrink_kernel computes U and lets its successor start at once (programmatic
+// dependent launch), which meanwhile streams the words and waits for U only before
+// its epilogue.  (One launch, in which the blocks of a cluster compute U over their
+// input rows while the first words travel, took longer for every adapter: 13.6 against
+// 12.3 us for 1 token at rank 16, 18.5 against 14.2 at rank 64, since every output
+// tile's cluster reads all of A.)
 //
 // Measured at 4096 x 4096, rank 16: 10.3 us for 1 token, 13.9 for 16, where the words
 // are 1.4 us: bound by the latency of the launches, the loads and the sums that meet.
@@ -87,22 +87,18 @@ __global__ void __launch_bounds__(256) lora_shrink_kernel(const LoraArgs a) {
 // are A operands straight from global memory, and U (fp32) is an fp16 pair
 // hi + lo of 22 bits under a power of two of its token, so nothing is rounded
 // away and no U overflows.  An adapter's sums are added for its own tokens only.
-constexpr int kFusedU = 64;  // values of U a cluster computes itself, at most
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
-
 template <Mode M, int NT, int MAXTOK, int STAGES>
 struct LoraShared {
   static constexpr uint32_t kRing = STAGES * stage_bytes<M, MAXTOK>();
   static constexpr uint32_t kRed = (MAXTOK * kRedPitch * 4 + 15) / 16 * 16;  // in the ring, after the product
   static constexpr int kUPitch = 2 * (256 + 8);                               // bytes of a token's hi (lo) row
   static constexpr uint32_t kU = 2 * MAXTOK * kUPitch;                        // behind it
-  static constexpr uint32_t kTail = sizeof(RingBars<STAGES>) + MAXTOK * 16 + 16 + 2 * kFusedU * 4;
+  static constexpr uint32_t kTail = sizeof(RingBars<STAGES>) + MAXTOK * 16 + 16 + kLoraStreamT * 4;
   static constexpr uint32_t kBytes = 1024 + kRing + kTail;
   static_assert(kRed + kU <= kRing, "the sums and U reuse the ring");
 };
 
-template <Mode M, int NT, int MAXTOK, int STAGES, int MINB, bool FUSED, int SHIFT>
+template <Mode M, int NT, int MAXTOK, int STAGES, int MINB, int SHIFT>
 __global__ void __launch_bounds__(kThreads, MINB)
     lora_stream_kernel(const __grid_constant__ LoraArgs a, const __grid_constant__ CUtensorMap map, const int splits) {
   using L = LoraShared<M, NT, MAXTOK, STAGES>;
@@ -118,11 +114,7 @@ __global__ void __launch_bounds__(kThreads, MINB)
   int *list = perm + MAXTOK;                     // the different adapters' first place | end << 16
   float *uscale = reinterpret_cast<float *>(list + MAXTOK);
   int *n_list = reinterpret_cast<int *>(uscale + MAXTOK);
-  float *upart = reinterpret_cast<float *>(n_list + 4);  // FUSED: U over this block's rows, [token][rank row]
-  float *usum = upart + kFusedU;                         // and over all (16-byte aligned, like all before it)
-  int *all_ids = reinterpret_cast<int *>(upart);         // before that: all tokens' adapters
-  static_assert(sizeof(RingBars<STAGES>) % 16 == 0 && MAXTOK % 4 == 0 && kFusedU % 4 == 0, "alignment");
-  static_assert(kFusedU >= kLoraStreamT, "all tokens' adapters");
+  int *all_ids = n_list + 4;                     // all tokens' adapters
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = (int)(blockIdx.x % (unsigned)splits);
   const int64_t tile = blockIdx.x / (unsigned)splits;
@@ -130,7 +122,6 @@ __global__ void __launch_bounds__(kThreads, MINB)
   const int n = (int)(a.T - t0 < MAXTOK ? a.T - t0 : MAXTOK);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) ring_init(bars);
-  if (FUSED) pdl_wait();  // the work before this call
   __syncthreads();
   // input rows of this rank, in units of 256 (128) rows so that groups stay whole
   const int64_t unit = a.in >= 512 * splits ? 256 : 128, units = (a.in + unit - 1) / unit;
@@ -140,10 +131,6 @@ __global__ void __launch_bounds__(kThreads, MINB)
     Producer<M, MAXTOK> p(Weights{&map, 0, a.qzeros, a.scales, a.out / 8, SHIFT,
                   (int)(tile * 32), (int)(a.out / 8), (int)(tile * 32), (int)(a.out / 8)});
     RingPos pos;
-    if (FUSED) {
-      if (blockIdx.x == 0 && lane == 0) *a.st = DevStatus{};
-      __syncwarp();
-    }
     // the first words do not wait for the tokens' order
     const int ahead = min(num_stages<M>(max(k1 - k0, 0)), STAGES);
     for (int s = 0; s < ahead; ++s)
@@ -151,11 +138,6 @@ __global__ void __launch_bounds__(kThreads, MINB)
     asm volatile("bar.sync 2, 288;" ::: "memory");
     p.rows(a.X, a.ldx, n, [&](int t) { return perm[t]; });
     p.run(pos, smem_u32(ring), bars, k0, k1, a.max_polls, a.st, ahead);
-    if (FUSED) {
-      __syncwarp();
-      cluster_arrive();
-      cluster_wait();
-    }
     if (*reinterpret_cast<volatile int *>(&bars->abort)) ring_drain(bars, pos);
   } else {
     RingPos pos;
@@ -192,41 +174,15 @@ __global__ void __launch_bounds__(kThreads, MINB)
       }
       if (lane == 0) *n_list = count;
     }
-    if (FUSED) {  // U over rows [k0, k1), a warp to a value
-      for (int i = warp; i < n * a.rank; i += kConsumers / 32) {
-        const int t = i / a.rank, r = i - t * a.rank, id = ids[t];
-        if (id < 0) continue;
-        const uint4 *x = reinterpret_cast<const uint4 *>(a.X + perm[t] * a.ldx);
-        const uint4 *w = reinterpret_cast<const uint4 *>(a.A + ((int64_t)id * a.rank + r) * a.in);
-        float s = 0.0f;
-#pragma unroll 2
-        for (int k = k0 / 8 + lane; k < k1 / 8; k += 32) s = dot8(__ldg(x + k), __ldg(w + k), s);
-#pragma unroll
-        for (int m = 16; m; m >>= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
-        if (lane == 0) upart[i] = a.c[id] * s;
-      }
-      __syncwarp();
-      cluster_arrive();
-    }
     consume<M, NT, MAXTOK, STAGES, SHIFT>(acc, pos, ring, bars, k0, k1, true, a.max_polls, a.st);
-    if (FUSED) {
-      cluster_wait();
-      for (int i = tid; i < n * a.rank; i += kConsumers) {
-        float u = 0.0f;
-        if (ids[i / a.rank] >= 0)
-          for (int s = 0; s < splits; ++s) u += cluster.map_shared_rank(upart, s)[i];
-        usum[i] = u;
-      }
-    } else {
-      pdl_wait();  // U and the cleared status word
-    }
+    pdl_wait();  // U and the cleared status word
     consumer_sync();
     const int r32 = (a.rank + 31) / 32 * 32;
     {  // a team of threads to a token, all tokens at once
       constexpr int kTeam = MAXTOK <= 8 ? 32 : MAXTOK <= 16 ? 16 : MAXTOK <= 32 ? 8 : 4;
       const int t = tid / kTeam, part = tid % kTeam;
       const bool on = t < n && ids[t] >= 0;
-      const float4 *u = reinterpret_cast<const float4 *>(FUSED ? usum + t * a.rank : a.U + (on ? perm[t] : 0) * a.rank);
+      const float4 *u = reinterpret_cast<const float4 *>(a.U + (on ? perm[t] : 0) * a.rank);
       float m = 0.0f;
 #pragma unroll 4
       for (int k = part; k < a.rank / 4; k += kTeam)
@@ -311,7 +267,7 @@ __global__ void __launch_bounds__(kThreads, MINB)
     store_sums<M, NT>(acc, red);
   }
   if (blockIdx.x == 0 && blockIdx.y == 0 && warp == kConsumers / 32) {
-    if (!FUSED) pdl_wait();
+    pdl_wait();
     for (int t = lane; t < a.T; t += 32) {
       const int id = a.ids[t];
       if (id < -1 || id >= a.adapters) dev_fail(a.st, kDevBadAdapter, 0xE01u);
@@ -372,11 +328,11 @@ struct Split {
   int s;
   int64_t groups, cycles;
 };
-template <Mode M, int NT, int MAXTOK, int STAGES, int MINB, bool FUSED, int SHIFT>
+template <Mode M, int NT, int MAXTOK, int STAGES, int MINB, int SHIFT>
 struct Stream {
   static constexpr size_t kSmem = LoraShared<M, NT, MAXTOK, STAGES>::kBytes;
   static_assert(MINB * (kSmem + 1024) <= 233472, "resident blocks");
-  static constexpr auto kernel = lora_stream_kernel<M, NT, MAXTOK, STAGES, MINB, FUSED, SHIFT>;
+  static constexpr auto kernel = lora_stream_kernel<M, NT, MAXTOK, STAGES, MINB, SHIFT>;
 
   static cudaError_t split(const LoraArgs &a, int num_sms, Split &p) {
     static std::atomic<bool> done[64];
@@ -395,10 +351,8 @@ struct Stream {
     CUtensorMap map;  // the words as pairs of 16-bit values
     cudaError_t e = make_tmap_f16_box(&map, a.qweight, a.in, a.out / 4, a.out / 4, 64, kBoxK);
     if (e != cudaSuccess) return e;
-    if (!FUSED) {
-      e = launch_after(lora_shrink_kernel, a.T * (a.rank / kShrinkR), 256, 0, stream, a);
-      if (e != cudaSuccess) return e;
-    }
+    e = launch_after(lora_shrink_kernel, a.T * (a.rank / kShrinkR), 256, 0, stream, a);
+    if (e != cudaSuccess) return e;
     cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
@@ -424,7 +378,8 @@ struct Stream {
 
 // 17 tokens and more: all of them in one block, or 16 in each of several blocks of a
 // tile, whichever fills the SMs better (45 tokens on 4096 x 12288: 45 us in 48 clusters
-// of 2, since 48 of 3 do not fit, 37 us in 3 groups of 16).
+// of 2, since 48 of 3 do not fit, 37 us in 3 groups of 16; on 4096 x 32768, rank 16, 70 us
+// in 128 blocks, 101 in groups).
 template <class Whole, class Groups>
 cudaError_t launch_wide(const LoraArgs &a, int num_sms, cudaStream_t stream) {
   Split w, g;
@@ -436,15 +391,12 @@ cudaError_t launch_wide(const LoraArgs &a, int num_sms, cudaStream_t stream) {
 
 template <int SHIFT>
 cudaError_t launch_group(const LoraArgs &a, int num_sms, cudaStream_t stream) {
-  // on its own up to as many values of U as keep A's part below the words'
-  // (1 token at rank 64: as many bytes of A as of words for a block)
-  if (a.T <= 8 && a.T * a.rank <= kFusedU) return Stream<Mode::kK, 1, 8, 4, 2, true, SHIFT>::run(a, num_sms, stream);
-  if (a.T <= 8) return Stream<Mode::kK, 1, 8, 4, 2, false, SHIFT>::run(a, num_sms, stream);
-  using Groups = Stream<Mode::kK, 2, 16, 8, 1, false, SHIFT>;
+  if (a.T <= 8) return Stream<Mode::kK, 1, 8, 4, 2, SHIFT>::run(a, num_sms, stream);
+  using Groups = Stream<Mode::kK, 2, 16, 8, 1, SHIFT>;
   if (a.T <= 16) return Groups::run(a, num_sms, stream);
-  if (a.T <= 32) return launch_wide<Stream<Mode::kTok, 2, 32, 6, 1, false, SHIFT>, Groups>(a, num_sms, stream);
-  if (a.T <= 48) return launch_wide<Stream<Mode::kTok, 3, 48, 6, 1, false, SHIFT>, Groups>(a, num_sms, stream);
-  return launch_wide<Stream<Mode::kTok, 4, 64, 5, 1, false, SHIFT>, Groups>(a, num_sms, stream);
+  if (a.T <= 32) return launch_wide<Stream<Mode::kTok, 2, 32, 6, 1, SHIFT>, Groups>(a, num_sms, stream);
+  if (a.T <= 48) return launch_wide<Stream<Mode::kTok, 3, 48, 6, 1, SHIFT>, Groups>(a, num_sms, stream);
+  return launch_wide<Stream<Mode::kTok, 4, 64, 5, 1, SHIFT>, Groups>(a, num_sms, stream);
 }
 }  // namespace
 
