@@ -10,7 +10,7 @@
 // 12.3 us for 1 token at rank 16, 18.5 against 14.2 at rank 64, since every output
 // tile's cluster reads all of A.)
 //
-// Measured at 4096 x 4096, rank 16: 10.3 us for 1 token, 13.9 for 16, where the words
+// Measured at 4096 x 4096, rank 16: 12.3 us for 1 token, 13.8 for 16, where the words
 // are 1.4 us: bound by the latency of the launches, the loads and the sums that meet.
 // 45 tokens on 4096 x 12288, rank 64: 37 us, bound by the core's instructions.
 #include <cooperative_groups.h>
@@ -49,6 +49,7 @@ __global__ void __launch_bounds__(256) lora_shrink_kernel(const LoraArgs a) {
   const int r0 = (int)(blockIdx.x - t * chunks) * kShrinkR;
   const int id = a.ids[t];
   if (id < 0 || id >= a.adapters) return;  // never read
+  const float scale = __ldg(a.c + id);
   const int n = (int)(a.in / 8), c0 = n * warp / 8, c1 = n * (warp + 1) / 8;  // 16-byte chunks
   const uint4 *x = reinterpret_cast<const uint4 *>(a.X + t * a.ldx);
   const uint4 *w = reinterpret_cast<const uint4 *>(a.A + ((int64_t)id * a.rank + r0) * a.in);
@@ -75,7 +76,7 @@ __global__ void __launch_bounds__(256) lora_shrink_kernel(const LoraArgs a) {
     float u = 0.0f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) u += part[i][threadIdx.x];
-    a.U[t * a.rank + r0 + threadIdx.x] = a.c[id] * u;
+    a.U[t * a.rank + r0 + threadIdx.x] = scale * u;
   }
 }
 
