@@ -160,3 +160,52 @@ def test_run_case_serving_ops(args, capsys):
     from post_weight_quantization_awq_b200 import run_case
     assert run_case.main(args.split() + ["--repeat", "2"]) == 0
     assert args.split()[1] + ": T=" in capsys.readouterr().out
+
+
+@pytest.mark.parametrize("T", [3, 40])
+def test_calls_behind_two_streams_that_join(T):
+    """Each call's inputs come from two streams that meet before it (X from one, the
+    residual from another), captured and eager: the call waits for both."""
+    b = Block(T)
+    b.step()
+    b.status()
+    want = {k: v.clone() for k, v in b.t.items()}
+    src = {k: want[k].clone() for k in ("n1", "r0", "p", "n2", "r1", "y")}
+    big = torch.zeros((64 << 20,), device="cuda")
+    side = torch.cuda.Stream()
+
+    def calls():
+        t, w = b.t, b.w
+        main = torch.cuda.current_stream()
+        for first, second, call in (
+                ("n1", "r0", lambda: awq.awq_w4a16_lora_gemm(t["n1"], *b.packed, b.cfg, w["A"], w["B"], w["c"],
+                                                             w["ids"], t["p"], b.ws1)),
+                ("r0", "p", lambda: awq.awq_block_norm(t["r0"], t["p"], None, None, 1.0, w["pre2"], 1e-6, t["r1"],
+                                                       t["n2"])),
+                ("n2", "r1", lambda: awq.awq_w4a16_moe(t["n2"], w["router"], w["gu"], w["dn"], b.cfg64, True, w["mask"],
+                                                       t["y"], t["eids"], t["wt"], b.ws2)),
+                ("r1", "y", lambda: awq.awq_block_norm(t["r1"], t["y"], w["post"], None, 0.5, w["pre3"], 1e-6, t["r2"],
+                                                       t["n3"]))):
+            t[first].zero_()
+            t[second].zero_()
+            side.wait_stream(main)
+            with torch.cuda.stream(side):
+                big.add_(1.0)  # late
+                t[first].copy_(src[first])
+            t[second].copy_(src[second])
+            main.wait_stream(side)
+            call()
+
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        calls()
+    for run in (g.replay, calls):
+        for k in ("p", "n2", "y", "eids", "wt", "r2", "n3"):
+            b.t[k].zero_()
+        torch.cuda.synchronize()
+        run()
+        b.status()
+        torch.cuda.synchronize()
+        for k in ("p", "n2", "y", "eids", "wt", "r2", "n3"):
+            assert torch.equal(b.t[k], want[k]), k
+    del g
