@@ -138,7 +138,7 @@ __global__ void __launch_bounds__(kThreads, MINB)
       p.issue_words(smem_u32(ring) + s * stage_bytes<M, MAXTOK>(), &bars->full[s], k0, k1, s);
     asm volatile("bar.sync 2, 288;" ::: "memory");
     p.rows(a.X, a.ldx, n, [&](int t) { return perm[t]; });
-    p.run(pos, smem_u32(ring), bars, k0, k1, a.max_polls, a.st, ahead);
+    p.run(pos, smem_u32(ring), bars, k0, k1, a.max_polls, nullptr, ahead);
     if (*reinterpret_cast<volatile int *>(&bars->abort)) ring_drain(bars, pos);
   } else {
     RingPos pos;
@@ -175,7 +175,7 @@ __global__ void __launch_bounds__(kThreads, MINB)
       }
       if (lane == 0) *n_list = count;
     }
-    consume<M, NT, MAXTOK, STAGES, SHIFT>(acc, pos, ring, bars, k0, k1, true, a.max_polls, a.st);
+    consume<M, NT, MAXTOK, STAGES, SHIFT>(acc, pos, ring, bars, k0, k1, true, a.max_polls, nullptr);
     pdl_wait();  // U and the cleared status word
     consumer_sync();
     const int r32 = (a.rank + 31) / 32 * 32;
@@ -275,6 +275,9 @@ __global__ void __launch_bounds__(kThreads, MINB)
     }
   }
   cluster.sync();
+  // A wait of the ring that ran out.  It may have done so before the shrink kernel cleared
+  // the status word; this thread has seen that kernel end
+  if (tid == 0 && *reinterpret_cast<volatile int *>(&bars->abort)) dev_fail(a.st, kDevTimeout, 0xE21u);
   for (int i = rank * kConsumers + tid; tid < kConsumers && i < n * (kBoxN / 2); i += splits * kConsumers) {
     const int t = i / (kBoxN / 2), oo = 2 * (i % (kBoxN / 2));
     const int64_t o = tile * kBoxN + oo;
