@@ -225,7 +225,40 @@ struct __align__(8) PTail {
   uint64_t tfull[2], tempty[2], done;
   uint32_t tmem;
   int abort_flag;
+  // the last tile, by i % 4 of the block's i-th (the warps are at most two apart), whose
+  // listed adapters have non-finite values: i + 1
+  volatile int odd[4];
 };
+
+// Of the two fp16 of w, the sign bits of those that are infinite or NaN.
+__device__ __forceinline__ uint32_t non_finite(uint32_t w) { return ((w & 0x7C007C00u) + 0x04000400u) & 0x80008000u; }
+
+// A row of B_a's landed box (16-byte chunks i, i + step, .. of `chunks`, swizzled by the row)
+// with 0 for what is not finite; whether there was any.
+__device__ __forceinline__ bool make_finite(uint8_t *box, int row, int i, int step, int chunks) {
+  bool any = false;
+  for (; i < chunks; i += step) {
+    uint4 *p = reinterpret_cast<uint4 *>(box + row * (64 * 2) + ((i ^ (row & 7)) * 16));
+    const uint4 v = *p;
+    const uint32_t x = non_finite(v.x), y = non_finite(v.y), z = non_finite(v.z), w = non_finite(v.w);
+    if (x | y | z | w) {
+      any = true;
+      *p = make_uint4(v.x & ~((x >> 15) * 0xFFFFu), v.y & ~((y >> 15) * 0xFFFFu), v.z & ~((z >> 15) * 0xFFFFu),
+                      v.w & ~((w >> 15) * 0xFFFFu));
+    }
+  }
+  return any;
+}
+
+// The terms U[t][r] B_a[o][r] of one output that make_finite left out.
+__device__ __noinline__ float left_out(const __half *u, const __half *b, int rank) {
+  float s = 0.0f;
+  for (int r = 0; r < rank; ++r) {
+    const float v = __half2float(b[r]);
+    if (!isfinite(v)) s = fmaf(__half2float(u[r]), v, s);
+  }
+  return s;
+}
 
 template <int STAGES>
 __device__ __forceinline__ void p_abort(PTail<STAGES> *t, DevStatus *st, uint32_t where) {
@@ -235,7 +268,7 @@ __device__ __forceinline__ void p_abort(PTail<STAGES> *t, DevStatus *st, uint32_
 
 struct PrefillArgs {
   const int32_t *ids;
-  const __half *U;
+  const __half *U, *B;
   const int *lists;
   int64_t T, out, ldy;
   int adapters, rank, num_m, num_n, num_kb;
@@ -276,11 +309,12 @@ __global__ void __launch_bounds__(320, 1)
       mbar_init(&tail->masked[s], 8);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&tail->tfull[i], 1);
+      mbar_init(&tail->tfull[i], 2);  // the MMAs' end, and the issuing thread
       mbar_init(&tail->tempty[i], 8);
     }
     mbar_init(&tail->done, 1);
     tail->abort_flag = 0;
+    for (int i = 0; i < 4; ++i) tail->odd[i] = 0;
     fence_mbar_init();
     tma_prefetch_desc(&tmX);
     tma_prefetch_desc(&tmW);
@@ -383,6 +417,7 @@ __global__ void __launch_bounds__(320, 1)
         }
         if (!ok) break;
         tc_commit(&tail->tfull[acc]);
+        mbar_arrive(&tail->tfull[acc]);  // hands on what the `masked` arrivals showed this thread (odd)
       }
       if (issued) {
         tc_commit(&tail->done);
@@ -427,6 +462,12 @@ __global__ void __launch_bounds__(320, 1)
               ok = false;
               break;
             }
+            __syncwarp();
+            // The other rows' zeros meet B_a too, and 0 x infinity is NaN: what is not finite
+            // leaves the box, and is added to the adapter's own rows at the end
+            if (n * BN + tid % BN < a.out &&
+                make_finite(sB + s * C::kB, tid % BN, tid / BN, 256 / BN, min(PK, a.rank - r * PK) / 8))
+              tail->odd[it & 3] = it + 1;
             if (tid < BM) {
               uint4 *d = reinterpret_cast<uint4 *>(sA + s * C::kA + tid * (PK * 2));
 #pragma unroll
@@ -456,12 +497,22 @@ __global__ void __launch_bounds__(320, 1)
       const int c0 = C::kMT == 2 ? 0 : part * (BN / 2), c1 = C::kMT == 2 ? BN : c0 + BN / 2;
       const uint32_t d = tmem + ((uint32_t)(q * 32) << 16) + acc * (C::kMT * BN) + (C::kMT == 2 ? part * BN : 0);
       uint8_t *stage = sOut + (warp - 2) * 4096;
+      int own = -1;  // this row's adapter, where one of the tile's is not finite
+      if (count && tail->odd[it & 3] == it + 1) own = t + lane < a.T ? a.ids[t + lane] : -1;
+      if (own >= a.adapters) own = -1;
 #pragma unroll 1
       for (int c = c0; c < c1; c += 64) {
         float v[64];
         tmem_ld_32x32b_x32(d + c, *reinterpret_cast<float(*)[32]>(v));
         tmem_ld_32x32b_x32(d + c + 32, *reinterpret_cast<float(*)[32]>(v + 32));
         tmem_ld_wait();
+        if (own >= 0) {
+          const int64_t o = (int64_t)n * BN + c;
+#pragma unroll
+          for (int i = 0; i < 64; ++i)
+            if (o + i < a.out)
+              v[i] += left_out(a.U + (t + lane) * a.rank, a.B + (own * a.out + o + i) * a.rank, a.rank);
+        }
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           uint32_t w[4];
@@ -509,7 +560,7 @@ cudaError_t launch_product(const LoraArgs &a, const int *lists, const __half *Wd
   if ((e = make_tmap_f16_box(&x, a.X, a.T, a.in, a.ldx, PK, BM)) != cudaSuccess) return e;
   if ((e = make_tmap_f16_box(&w, Wd, a.out, a.in, a.in, PK, BN)) != cudaSuccess) return e;
   if ((e = make_tmap_f16_box(&b, a.B, (int64_t)a.adapters * a.out, a.rank, a.rank, PK, BN)) != cudaSuccess) return e;
-  const PrefillArgs p = {a.ids, reinterpret_cast<const __half *>(a.U), lists, a.T, a.out, a.ldy, a.adapters, a.rank, (int)((a.T + BM - 1) / BM),
+  const PrefillArgs p = {a.ids, reinterpret_cast<const __half *>(a.U), a.B, lists, a.T, a.out, a.ldy, a.adapters, a.rank, (int)((a.T + BM - 1) / BM),
                          (int)((a.out + BN - 1) / BN), (int)(a.in / PK), a.Y, a.st, a.max_polls};
   const int64_t tiles = (int64_t)p.num_m * p.num_n;
   return launch_after(lora_gemm_kernel<BM, BN>, i64min(tiles, num_sms), 320, C::kBytes, stream, x, w, b, p);

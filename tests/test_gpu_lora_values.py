@@ -7,6 +7,7 @@ import pytest
 
 import post_weight_quantization_awq_b200 as awq
 from gpu_helpers import need_cuda
+from serving_oracle import lora, lora_tolerance
 from test_gpu_lora import _case, _run
 
 pytestmark = pytest.mark.gpu
@@ -31,3 +32,40 @@ def test_lora_wait_that_runs_out_is_never_lost(monkeypatch, T, rank):
             assert e.status_name == "AWQ_ERR_TIMEOUT"
     monkeypatch.delenv("AWQ_FAULT")
     assert np.array_equal(_run(X, packed, 128, A, B, c, ids).view(np.uint16), want)
+
+
+def _kind(v):
+    """0 finite, 1 +inf, 2 -inf, 3 NaN."""
+    return np.where(np.isnan(v), 3, np.where(np.isposinf(v), 1, np.where(np.isneginf(v), 2, 0)))
+
+
+def _same_or_close(got, want, tol):
+    """Infinities and NaN where the definition has them, the rest within tol."""
+    got = got.astype(np.float64)
+    assert np.array_equal(_kind(got), _kind(want)), np.argwhere(_kind(got) != _kind(want))[:5]
+    ok = np.isfinite(want)
+    assert np.all(np.abs(got[ok] - want[ok]) <= tol[ok]), np.abs(got[ok] - want[ok]).max()
+
+
+@pytest.mark.parametrize("T,inn,out,rank,n,group,order", [
+    (66, 256, 96, 16, 3, 64, "mixed"),
+    (90, 256, 544, 8, 4, 32, "mixed"), (300, 512, 288, 72, 5, 128, "mixed"), (300, 256, 1056, 40, 9, 64, "runs"),
+    (600, 256, 8224, 16, 3, 128, "mixed")])
+def test_lora_non_finite_b_stays_with_its_rows(T, inn, out, rank, n, group, order):
+    """Infinities and NaN in B of some adapters: the rows of the others, and those
+    without one, keep their bits; an adapter's own rows are the definition's."""
+    X, packed, A, B, c, ids = _case(T, inn, out, rank, n, group, T + out, order)
+    clean = _run(X, packed, group, A, B, c, ids)
+    rng = np.random.default_rng(T)
+    bad = B.copy()
+    for a, v in ((0, np.inf), (2, np.nan), (2, -np.inf)):
+        for o, r in ((0, 0), (out - 1, rank - 1), (int(rng.integers(out)), int(rng.integers(rank)))):
+            bad[a, o, r] = v
+    got = _run(X, packed, group, A, bad, c, ids)
+    other = (ids != 0) & (ids != 2)
+    assert np.array_equal(got[other].view(np.uint16), clean[other].view(np.uint16))
+    with np.errstate(invalid="ignore"):
+        Yo, _ = lora(X, packed, group, A, bad, c, ids)
+    _, mags = lora(X, packed, group, A, B, c, ids)
+    tol = lora_tolerance(np.where(np.isfinite(Yo), Yo, 0), mags, inn, rank, rounded=T > 64)
+    _same_or_close(got, Yo, tol)
