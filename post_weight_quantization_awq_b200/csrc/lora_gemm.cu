@@ -80,6 +80,13 @@ __global__ void __launch_bounds__(256) lora_shrink_kernel(const LoraArgs a) {
   }
 }
 
+// One output's part of a token's adapter in fp32, term by term.
+__device__ __noinline__ float low_rank_dot(const float *u, const __half *b, int rank) {
+  float s = 0.0f;
+  for (int r = 0; r < rank; ++r) s = fmaf(u[r], __half2float(b[r]), s);
+  return s;
+}
+
 // A cluster of `splits` blocks covers 256 outputs x MAXTOK tokens, each block
 // a range of input rows and a share of the adapters; the blocks' fp32 sums meet
 // through distributed shared memory in rank order.
@@ -87,7 +94,9 @@ __global__ void __launch_bounds__(256) lora_shrink_kernel(const LoraArgs a) {
 // The adapters' part joins the accumulators on the tensor cores too: B_a's rows
 // are A operands straight from global memory, and U (fp32) is an fp16 pair
 // hi + lo of 22 bits under a power of two of its token, so nothing is rounded
-// away and no U overflows.  An adapter's sums are added for its own tokens only.
+// away and no U overflows.  An adapter's sums are added for its own tokens only.  With an
+// infinity or a NaN in U or B_a a pair's product is not the value's (0 x infinity is NaN):
+// a sum that is not finite is made again in fp32.
 template <Mode M, int NT, int MAXTOK, int STAGES>
 struct LoraShared {
   static constexpr uint32_t kRing = STAGES * stage_bytes<M, MAXTOK>();
@@ -252,18 +261,29 @@ __global__ void __launch_bounds__(kThreads, MINB)
           }
         }
       }
+      const auto each_sum = [&](auto f) {  // of this adapter's tokens
 #pragma unroll
-      for (int x = 0; x < NT; ++x)
+        for (int x = 0; x < NT; ++x)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int t = tt + x * 8 + 2 * q + e;
-          if (t < lo || t >= hi) continue;
-          const float sc = uscale[t];
+          for (int e = 0; e < 2; ++e) {
+            const int t = tt + x * 8 + 2 * q + e;
+            if (t < lo || t >= hi) continue;
+            const float sc = uscale[t];
 #pragma unroll
-          for (int p = 0; p < 4; ++p)
+            for (int p = 0; p < 4; ++p)
 #pragma unroll
-            for (int h = 0; h < 2; ++h) acc.out[p][x][e + 2 * h] = fmaf(sc, acc.grp[p][x][e + 2 * h], acc.out[p][x][e + 2 * h]);
-        }
+              for (int h = 0; h < 2; ++h) f(t, sc, p + 4 * h, acc.grp[p][x][e + 2 * h], acc.out[p][x][e + 2 * h]);
+          }
+      };
+      float odd = 0.0f;
+      each_sum([&](int, float, int, float v, float &) { odd = fmaf(0.0f, v, odd); });
+      if (odd != 0.0f && o_ok)  // NaN: a sum is not finite
+        each_sum([&](int t, float, int o, float &v, float &out) {
+          if (isfinite(v)) return;
+          out += low_rank_dot(a.U + perm[t] * a.rank, a.B + ((int64_t)id * a.out + o0 + o) * a.rank, a.rank);
+          v = 0.0f;
+        });
+      each_sum([&](int, float sc, int, float v, float &out) { out = fmaf(sc, v, out); });
     }
     store_sums<M, NT>(acc, red);
   }

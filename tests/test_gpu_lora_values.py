@@ -48,7 +48,8 @@ def _same_or_close(got, want, tol):
 
 
 @pytest.mark.parametrize("T,inn,out,rank,n,group,order", [
-    (66, 256, 96, 16, 3, 64, "mixed"),
+    (6, 256, 96, 16, 3, 64, "mixed"), (13, 256, 96, 8, 3, 64, "mixed"), (40, 256, 288, 72, 5, 64, "mixed"),
+    (64, 256, 1056, 24, 4, 128, "runs"), (66, 256, 96, 16, 3, 64, "mixed"),
     (90, 256, 544, 8, 4, 32, "mixed"), (300, 512, 288, 72, 5, 128, "mixed"), (300, 256, 1056, 40, 9, 64, "runs"),
     (600, 256, 8224, 16, 3, 128, "mixed")])
 def test_lora_non_finite_b_stays_with_its_rows(T, inn, out, rank, n, group, order):
@@ -69,3 +70,22 @@ def test_lora_non_finite_b_stays_with_its_rows(T, inn, out, rank, n, group, orde
     _, mags = lora(X, packed, group, A, B, c, ids)
     tol = lora_tolerance(np.where(np.isfinite(Yo), Yo, 0), mags, inn, rank, rounded=T > 64)
     _same_or_close(got, Yo, tol)
+
+
+@pytest.mark.parametrize("T", [6, 13, 40])
+def test_lora_infinite_rank_row_beside_large_ones(T):
+    """One infinite value of U beside others past fp16's range: the infinity decides."""
+    X, packed, A, B, c, ids = _case(T, 256, 96, 16, 2, 64, T)
+    ids[:] = np.arange(T) % 3 - 1
+    c[1] = 1e6
+    B[1] = (B[1].astype(np.float64) * 1e-3).astype(np.float16)
+    B[1][:, 3] = np.where(np.arange(96) % 2 == 0, 0.5, -0.5)
+    A[1, 3, 7] = np.inf
+    with np.errstate(invalid="ignore"):
+        Yo, _ = lora(X, packed, 64, A, B, c, ids)
+    fin = A.copy()
+    fin[1, 3, 7] = 0
+    _, mags = lora(X, packed, 64, fin, B, c, ids)
+    assert (_kind(Yo[ids == 1]) != 3).all() and not np.isfinite(Yo[ids == 1]).any()
+    _same_or_close(_run(X, packed, 64, A, B, c, ids), Yo,
+                   lora_tolerance(np.where(np.isfinite(Yo), Yo, 0), mags, 256, 16, T > 64))
