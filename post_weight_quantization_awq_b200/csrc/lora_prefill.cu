@@ -233,21 +233,36 @@ struct __align__(8) PTail {
 // Of the two fp16 of w, the sign bits of those that are infinite or NaN.
 __device__ __forceinline__ uint32_t non_finite(uint32_t w) { return ((w & 0x7C007C00u) + 0x04000400u) & 0x80008000u; }
 
-// A row of B_a's landed box (16-byte chunks i, i + step, .. of `chunks`, swizzled by the row)
-// with 0 for what is not finite; whether there was any.
-__device__ __forceinline__ bool make_finite(uint8_t *box, int row, int i, int step, int chunks) {
-  bool any = false;
-  for (; i < chunks; i += step) {
-    uint4 *p = reinterpret_cast<uint4 *>(box + row * (64 * 2) + ((i ^ (row & 7)) * 16));
-    const uint4 v = *p;
-    const uint32_t x = non_finite(v.x), y = non_finite(v.y), z = non_finite(v.z), w = non_finite(v.w);
-    if (x | y | z | w) {
-      any = true;
-      *p = make_uint4(v.x & ~((x >> 15) * 0xFFFFu), v.y & ~((y >> 15) * 0xFFFFu), v.z & ~((z >> 15) * 0xFFFFu),
-                      v.w & ~((w >> 15) * 0xFFFFu));
+// A row of B_a's landed box (16-byte chunks i, i + STEP, .. of `chunks`, swizzled by the
+// row): non-zero where a value is not finite.
+template <int STEP>
+__device__ __forceinline__ uint32_t row_non_finite(const uint8_t *row, int swizzle, int first, int chunks) {
+  uint32_t any = 0;
+#pragma unroll
+  for (int i = 0; i < 8; i += STEP)
+    if (first + i < chunks) {
+      const uint4 v = *reinterpret_cast<const uint4 *>(row + (((first + i) ^ swizzle) * 16));
+      any |= non_finite(v.x) | non_finite(v.y) | non_finite(v.z) | non_finite(v.w);
     }
-  }
   return any;
+}
+
+// The same row with 0 for what is not finite.
+__device__ __noinline__ void make_finite(uint8_t *row, int swizzle, int i, int step, int chunks) {
+  for (; i < chunks; i += step) {
+    uint32_t *p = reinterpret_cast<uint32_t *>(row + ((i ^ swizzle) * 16));
+    for (int k = 0; k < 4; ++k) p[k] &= ~((non_finite(p[k]) >> 15) * 0xFFFFu);
+  }
+}
+
+// One column of tensor memory, a value to a lane, waited for.
+__device__ __forceinline__ float tmem_column(uint32_t taddr) {
+  uint32_t r;
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];\n\ttcgen05.wait::ld.sync.aligned;"
+               : "=r"(r)
+               : "r"(taddr)
+               : "memory");
+  return __uint_as_float(r);
 }
 
 // The terms U[t][r] B_a[o][r] of one output that make_finite left out.
@@ -464,15 +479,21 @@ __global__ void __launch_bounds__(320, 1)
             }
             __syncwarp();
             // The other rows' zeros meet B_a too, and 0 x infinity is NaN: what is not finite
-            // leaves the box, and is added to the adapter's own rows at the end
-            if (n * BN + tid % BN < a.out &&
-                make_finite(sB + s * C::kB, tid % BN, tid / BN, 256 / BN, min(PK, a.rank - r * PK) / 8))
-              tail->odd[it & 3] = it + 1;
+            // leaves the box, and is added to the adapter's own rows at the end (0.13 us a step of
+            // 128 rows; looking the adapters over beforehand would read B_a once more)
+            const int left = min(PK, a.rank - r * PK), chunks = n * BN + tid % BN < a.out ? left / 8 : 0;
+            uint8_t *brow = sB + s * C::kB + tid % BN * (PK * 2);
+            const uint32_t bad = row_non_finite<256 / BN>(brow, tid & 7, tid / BN, chunks);
             if (tid < BM) {
               uint4 *d = reinterpret_cast<uint4 *>(sA + s * C::kA + tid * (PK * 2));
 #pragma unroll
-              for (int i = 0; i < PK / 8; ++i)  // 128-byte swizzle
-                d[i ^ (tid & 7)] = !mine ? make_uint4(0u, 0u, 0u, 0u) : r == 0 ? first[i] : chunk(PK / 8 * r + i);
+              for (int i = 0; i < PK / 8; ++i)  // 128-byte swizzle; the MMAs of 16 columns that are issued
+                if (8 * (i & ~1) < left)
+                  d[i ^ (tid & 7)] = !mine ? make_uint4(0u, 0u, 0u, 0u) : r == 0 ? first[i] : chunk(PK / 8 * r + i);
+            }
+            if (__any_sync(0xffffffffu, bad != 0)) {
+              make_finite(brow, tid & 7, tid / BN, 256 / BN, chunks);
+              tail->odd[it & 3] = it + 1;
             }
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
@@ -497,22 +518,26 @@ __global__ void __launch_bounds__(320, 1)
       const int c0 = C::kMT == 2 ? 0 : part * (BN / 2), c1 = C::kMT == 2 ? BN : c0 + BN / 2;
       const uint32_t d = tmem + ((uint32_t)(q * 32) << 16) + acc * (C::kMT * BN) + (C::kMT == 2 ? part * BN : 0);
       uint8_t *stage = sOut + (warp - 2) * 4096;
-      int own = -1;  // this row's adapter, where one of the tile's is not finite
-      if (count && tail->odd[it & 3] == it + 1) own = t + lane < a.T ? a.ids[t + lane] : -1;
-      if (own >= a.adapters) own = -1;
+      const bool odd = count && tail->odd[it & 3] == it + 1;
+      if (odd) {  // a column at a time, with what left the boxes
+        const int id = t + lane < a.T ? a.ids[t + lane] : -1;
+        for (int c = c0; c < c1; ++c) {
+          float v = tmem_column(d + c);
+          const int64_t o = (int64_t)n * BN + c;
+          if (t + lane < a.T && o < a.out) {
+            if (id >= 0 && id < a.adapters)
+              v += left_out(a.U + (t + lane) * a.rank, a.B + (id * a.out + o) * a.rank, a.rank);
+            a.Y[(t + lane) * a.ldy + o] = __float2half_rn(v);
+          }
+          __syncwarp();
+        }
+      }
 #pragma unroll 1
-      for (int c = c0; c < c1; c += 64) {
+      for (int c = odd ? c1 : c0; c < c1; c += 64) {
         float v[64];
         tmem_ld_32x32b_x32(d + c, *reinterpret_cast<float(*)[32]>(v));
         tmem_ld_32x32b_x32(d + c + 32, *reinterpret_cast<float(*)[32]>(v + 32));
         tmem_ld_wait();
-        if (own >= 0) {
-          const int64_t o = (int64_t)n * BN + c;
-#pragma unroll
-          for (int i = 0; i < 64; ++i)
-            if (o + i < a.out)
-              v[i] += left_out(a.U + (t + lane) * a.rank, a.B + (own * a.out + o + i) * a.rank, a.rank);
-        }
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           uint32_t w[4];
