@@ -34,8 +34,8 @@ extern "C" {
  *   ws       awq_w4a16_lora_workspace_size() bytes
  * Up to 64 tokens the packed words are streamed and the weights stay
  * (q - z) scale exactly; beyond, they are rounded to fp16 once, as in
- * awq_w4a16_gemm, and c_a U to fp16 (past fp16's range it is infinite), for one
- * product on the tensor cores.
+ * awq_w4a16_gemm, and c_a U to fp16, for one product on the tensor cores (a token
+ * whose largest c_a U is past 65504, or below 2^-12, keeps it in fp32).
  * Requires in % 64 == 0, out % 32 == 0, rank % 8 == 0 and 8 <= rank <= 256,
  * 1 <= n_adapters <= 65536, n_adapters * out < 2^31; X, A, B and Y 16-byte
  * aligned, c and adapter 4-byte aligned. */

@@ -4,6 +4,8 @@
 //   Y = X Wd^T + sum over the tile's adapters a of mask_a(U) B_a^T,
 //   Wd = RN16((q - z) scale),  U[t] = RN16( c_a (x_t A_a^T) ),  a = ids[t]
 //
+// (a row of U past fp16's range stays fp32, and its part is added to the accumulators).
+//
 // Three launches.  lora_shrink_mma_kernel computes U and, for every token tile of
 // the product, the list of the adapters its rows carry; beside it (programmatic
 // dependent launch) lora_dequant_kernel dequantises W once, in x out work instead
@@ -157,7 +159,10 @@ __device__ void shrink_block(const LoraArgs &a, int64_t t0, int share, int share
       if (r >= rows.y || t >= n || ids[t] != id) continue;
       float v = 0.0f;
       for (int w = 0; w < split; ++w) v += red[((m * split + w) * kShT + t) * (kShR + 1) + r];
-      reinterpret_cast<__half *>(a.U)[(t0 + t) * a.rank + rows.x + r] = __float2half_rn(a.c[id] * v);
+      const int64_t at = (t0 + t) * a.rank + rows.x + r;
+      const float u = a.c[id] * v;
+      a.U[at] = u;
+      reinterpret_cast<__half *>(a.U + a.T * a.rank)[at] = __float2half_rn(u);
     }
     __syncthreads();
   }
@@ -225,8 +230,8 @@ struct __align__(8) PTail {
   uint64_t tfull[2], tempty[2], done;
   uint32_t tmem;
   int abort_flag;
-  // the last tile, by i % 4 of the block's i-th (the warps are at most two apart), whose
-  // listed adapters have non-finite values: i + 1
+  // the last tile, by i % 4 of the block's i-th (the warps are at most two apart), in which
+  // B has values that are not finite, or rows of U are past fp16: i + 1
   volatile int odd[4];
 };
 
@@ -265,12 +270,25 @@ __device__ __forceinline__ float tmem_column(uint32_t taddr) {
   return __uint_as_float(r);
 }
 
-// The terms U[t][r] B_a[o][r] of one output that make_finite left out.
-__device__ __noinline__ float left_out(const __half *u, const __half *b, int rank) {
+// Whether a row of U is no operand of fp16: its largest value past the type's range (or no
+// number), or so small that the type's smallest step, 2^-24, is no longer small beside it.
+__device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
+__device__ __forceinline__ uint32_t abs_bits(float4 v) {
+  return max(max(abs_bits(v.x), abs_bits(v.y)), max(abs_bits(v.z), abs_bits(v.w)));
+}
+__device__ __forceinline__ bool past_fp16(const float *u, int rank) {
+  uint32_t m = 0;
+  for (int r = 0; r < rank; r += 4) m = max(m, abs_bits(__ldg(reinterpret_cast<const float4 *>(u + r))));
+  return m > 0x477FE000u || (m != 0 && m < 0x39800000u);  // 65504; 2^-12
+}
+
+// The terms U[t][r] B_a[o][r] of one output that are not in the product: those that
+// make_finite took out, or all of a row of U past fp16.
+__device__ __noinline__ float left_out(const float *u, const __half *b, int rank, bool all) {
   float s = 0.0f;
   for (int r = 0; r < rank; ++r) {
     const float v = __half2float(b[r]);
-    if (!isfinite(v)) s = fmaf(__half2float(u[r]), v, s);
+    if (all || !isfinite(v)) s = fmaf(u[r], v, s);
   }
   return s;
 }
@@ -283,7 +301,8 @@ __device__ __forceinline__ void p_abort(PTail<STAGES> *t, DevStatus *st, uint32_
 
 struct PrefillArgs {
   const int32_t *ids;
-  const __half *U, *B;
+  const float *U;   // [T, rank], and as fp16
+  const __half *U16, *B;
   const int *lists;
   int64_t T, out, ldy;
   int adapters, rank, num_m, num_n, num_kb;
@@ -455,16 +474,18 @@ __global__ void __launch_bounds__(320, 1)
       if (count) {
         const int64_t row = (int64_t)m * BM + tid;  // tid >= BM: no row
         const int id = tid < BM && row < a.T ? a.ids[row] : -1;
-        const uint4 *u = reinterpret_cast<const uint4 *>(a.U + row * a.rank);
+        const uint4 *u = reinterpret_cast<const uint4 *>(a.U16 + row * a.rank);
         const auto chunk = [&](int i) {  // 8 values of this row's U
           return id >= 0 && 8 * i < a.rank ? __ldg(u + i) : make_uint4(0u, 0u, 0u, 0u);
         };
+        const bool past = id >= 0 && past_fp16(a.U + row * a.rank, a.rank);
         uint4 first[PK / 8];  // loaded once for all adapters of the tile
         int next = list[1];
 #pragma unroll
         for (int i = 0; i < PK / 8; ++i) first[i] = chunk(i);
         for (int e = 0; e < count && ok; ++e) {
-          const int mine = id == next;
+          const bool mine = id == next && !past;
+          if (id == next && past) tail->odd[it & 3] = it + 1;
           if (e + 1 < count) next = list[2 + e];
           for (int r = 0; r < rsteps; ++r, ++step) {
             const int s = step % STAGES;
@@ -519,14 +540,16 @@ __global__ void __launch_bounds__(320, 1)
       const uint32_t d = tmem + ((uint32_t)(q * 32) << 16) + acc * (C::kMT * BN) + (C::kMT == 2 ? part * BN : 0);
       uint8_t *stage = sOut + (warp - 2) * 4096;
       const bool odd = count && tail->odd[it & 3] == it + 1;
-      if (odd) {  // a column at a time, with what left the boxes
+      if (odd) {  // a column at a time, with what is not in the product
         const int id = t + lane < a.T ? a.ids[t + lane] : -1;
+        const bool on = id >= 0 && id < a.adapters;
+        const float *u = a.U + (t + lane) * a.rank;
+        const bool past = on && past_fp16(u, a.rank);
         for (int c = c0; c < c1; ++c) {
           float v = tmem_column(d + c);
           const int64_t o = (int64_t)n * BN + c;
           if (t + lane < a.T && o < a.out) {
-            if (id >= 0 && id < a.adapters)
-              v += left_out(a.U + (t + lane) * a.rank, a.B + (id * a.out + o) * a.rank, a.rank);
+            if (on) v += left_out(u, a.B + (id * a.out + o) * a.rank, a.rank, past);
             a.Y[(t + lane) * a.ldy + o] = __float2half_rn(v);
           }
           __syncwarp();
@@ -585,7 +608,7 @@ cudaError_t launch_product(const LoraArgs &a, const int *lists, const __half *Wd
   if ((e = make_tmap_f16_box(&x, a.X, a.T, a.in, a.ldx, PK, BM)) != cudaSuccess) return e;
   if ((e = make_tmap_f16_box(&w, Wd, a.out, a.in, a.in, PK, BN)) != cudaSuccess) return e;
   if ((e = make_tmap_f16_box(&b, a.B, (int64_t)a.adapters * a.out, a.rank, a.rank, PK, BN)) != cudaSuccess) return e;
-  const PrefillArgs p = {a.ids, reinterpret_cast<const __half *>(a.U), a.B, lists, a.T, a.out, a.ldy, a.adapters, a.rank, (int)((a.T + BM - 1) / BM),
+  const PrefillArgs p = {a.ids, a.U, reinterpret_cast<const __half *>(a.U + a.T * a.rank), a.B, lists, a.T, a.out, a.ldy, a.adapters, a.rank, (int)((a.T + BM - 1) / BM),
                          (int)((a.out + BN - 1) / BN), (int)(a.in / PK), a.Y, a.st, a.max_polls};
   const int64_t tiles = (int64_t)p.num_m * p.num_n;
   return launch_after(lora_gemm_kernel<BM, BN>, i64min(tiles, num_sms), 320, C::kBytes, stream, x, w, b, p);
@@ -603,14 +626,14 @@ int lora_prefill_bm(int64_t T, int64_t out, int num_sms) {
 
 size_t lora_prefill_ws(int64_t T, int64_t in, int64_t out, int rank) {
   auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
-  return up(sizeof(__half) * (size_t)T * rank) + up(sizeof(int) * (size_t)((T + 127) / 128) * 129) +
+  return up((sizeof(float) + sizeof(__half)) * (size_t)T * rank) + up(sizeof(int) * (size_t)((T + 127) / 128) * 129) +
          up(sizeof(__half) * (size_t)in * out);
 }
 
 cudaError_t launch_lora_prefill(const LoraArgs &a, int num_sms, cudaStream_t stream) {
   auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
   uint8_t *ws = reinterpret_cast<uint8_t *>(a.U);
-  int *lists = reinterpret_cast<int *>(ws + up(sizeof(__half) * (size_t)a.T * a.rank));
+  int *lists = reinterpret_cast<int *>(ws + up((sizeof(float) + sizeof(__half)) * (size_t)a.T * a.rank));
   __half *Wd = reinterpret_cast<__half *>(reinterpret_cast<uint8_t *>(lists) +
                                           up(sizeof(int) * (size_t)((a.T + 127) / 128) * 129));
   const int bm = lora_prefill_bm(a.T, a.out, num_sms);

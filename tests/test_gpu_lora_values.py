@@ -72,7 +72,7 @@ def test_lora_non_finite_b_stays_with_its_rows(T, inn, out, rank, n, group, orde
     _same_or_close(got, Yo, tol)
 
 
-@pytest.mark.parametrize("T", [6, 13, 40])
+@pytest.mark.parametrize("T", [6, 13, 40, 90])
 def test_lora_infinite_rank_row_beside_large_ones(T):
     """One infinite value of U beside others past fp16's range: the infinity decides."""
     X, packed, A, B, c, ids = _case(T, 256, 96, 16, 2, 64, T)
@@ -89,3 +89,19 @@ def test_lora_infinite_rank_row_beside_large_ones(T):
     assert (_kind(Yo[ids == 1]) != 3).all() and not np.isfinite(Yo[ids == 1]).any()
     _same_or_close(_run(X, packed, 64, A, B, c, ids), Yo,
                    lora_tolerance(np.where(np.isfinite(Yo), Yo, 0), mags, 256, 16, T > 64))
+
+
+@pytest.mark.parametrize("T,rank", [(5, 16), (40, 64), (65, 16), (90, 8), (300, 136), (300, 64), (700, 16)])
+@pytest.mark.parametrize("c2,b2", [(3e5, 2e-5), (2e-7, 1e5)])
+def test_lora_scaled_products_past_fp16(T, rank, c2, b2):
+    """c_a U past fp16's largest value, or below its smallest normal one, with B_a
+    scaled the other way: Y is an ordinary value, and as near as ever.  The codes
+    are the zero points, so that the low-rank part stands alone."""
+    X, packed, A, B, c, ids = _case(T, 512, 288, rank, 3, 128, T + rank)
+    packed = (np.repeat(packed[1], 128, axis=0), packed[1], packed[2])
+    ids[0] = 1
+    c[1] = c2
+    B[1] = (B[1].astype(np.float64) * b2).astype(np.float16)
+    Yo, mags = lora(X, packed, 128, A, B, c, ids)
+    got = _run(X, packed, 128, A, B, c, ids)
+    _same_or_close(got, Yo, lora_tolerance(Yo, mags, 512, rank, rounded=T > 64))
