@@ -241,8 +241,8 @@ __device__ void router(const MoeArgs &a) {
   }
 }
 
-// Time of a unit of 128 input rows by its token tiles, measured: 196, 252 and
-// 314 cycles a step for 1, 2 and 3 tiles with 8 warps on an SM.
+// Time of a unit of 128 input rows by its token tiles, measured: 207, 252 and
+// 313 cycles a step for 1, 2 and 3 tiles with 8 warps on an SM.
 __host__ __device__ constexpr int unit_cost(int n) { return n <= 8 ? 3 : n <= 16 ? 4 : 5; }
 
 // The experts' token lists, and the entries.  Every block makes its own: an

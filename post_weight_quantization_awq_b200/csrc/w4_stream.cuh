@@ -29,8 +29,8 @@
 //   kTok  one column block, 128 consecutive input rows: every warp works
 //         through both boxes for its half of the tokens.
 //
-// Measured (g = 128, words in shared memory): 196, 252 and 314 cycles for 16 rows x
-// 512 outputs by 8 warps with 1, 2 and 3 token tiles, 248 for two such blocks on an
+// Measured (g = 128, words in shared memory): 207, 252 and 313 cycles for 16 rows x
+// 512 outputs by 8 warps with 1, 2 and 3 token tiles, 260 for two such blocks on an
 // SM with 1.  The bound is the instructions that make fragments of words (24 of them
 // per 4 words and lane, at half rate) and mma.sync (8 cycles each and sub-partition),
 // which two warps a sub-partition overlap in part.
@@ -310,17 +310,15 @@ struct Producer {
 
 // ---------------------------------------------------------------- consumers
 // Accumulators of one warp: 64 outputs x 8 NT tokens.  A group's zero points are
-// either subtracted from the codes (16 packed subtractions a step) or, for one
-// token tile, taken off at the group's end with sum_k x, which one more MMA a step
-// gives: 219 against 255 cycles a step with 16 warps on an SM when it was chosen.
+// subtracted from the codes (16 packed subtractions a step).  Taking off z sum_k x at the
+// group's end instead costs one more MMA a step and is 2 to 4 % faster for one token tile
+// with groups of 128 (10.1 against 9.7 us for 1 token), but gives NaN for every weight
+// where x is infinite.
 template <int NT>
 struct Acc {
-  static constexpr bool kSumX = NT == 1;
   float out[4][NT][4];  // totals: [p][token tile][c], 2^-24 (p even) or 2^-20 (p odd) of the sum
   float grp[4][NT][4];  // this group's sum, in the same units
-  float sx[4];          // this group's sum of x 2^-24
   uint32_t zp[8];       // the group's zero points as subnormal pairs
-  uint32_t zw;          // the group's zero word
   uint4 sc;             // the group's steps (8 fp16)
 };
 
@@ -332,16 +330,13 @@ __device__ __forceinline__ void acc_zero(Acc<NT> &a) {
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int c = 0; c < 4; ++c) a.out[p][n][c] = a.grp[p][n][c] = 0.0f;
-#pragma unroll
-  for (int c = 0; c < 4; ++c) a.sx[c] = 0.0f;
 }
 
 template <int NT>
 __device__ __forceinline__ void open_group(Acc<NT> &a, const uint8_t *sz, int wcol) {
   a.sc = *reinterpret_cast<const uint4 *>(sz + wcol * 16);
-  a.zw = lds32(sz + 512 + wcol * 4);
-  if (Acc<NT>::kSumX) return;
-  uint32_t lo = __byte_perm(a.zw, a.zw, 0x1010), hi = __byte_perm(a.zw, a.zw, 0x3232);
+  const uint32_t zw = lds32(sz + 512 + wcol * 4);
+  uint32_t lo = __byte_perm(zw, zw, 0x1010), hi = __byte_perm(zw, zw, 0x3232);
 #pragma unroll
   for (int p = 0; p < 4; ++p) {
     const uint32_t m = (p & 1) ? 0x00F000F0u : 0x000F000Fu;
@@ -363,22 +358,14 @@ __device__ __forceinline__ void close_group(Acc<NT> &a) {
     const __half2 s2 = *reinterpret_cast<const __half2 *>(&sh[o >> 1]);
     const float s = __half2float((o & 1) ? __high2half(s2) : __low2half(s2));
     const int p = o & 3, h = o >> 2;
-    float nz = 0.0f;  // -z (p even), -16 z (p odd), from the low bits of 2^23 + z
-    if (Acc<NT>::kSumX) {
-      const uint32_t z = (p & 1) ? (a.zw >> (4 * o - 4)) & 0xF0u : (a.zw >> (4 * o)) & 0xFu;
-      nz = 8388608.0f - __uint_as_float(0x4B000000u | z);
-    }
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int c = 2 * h; c < 2 * h + 2; ++c) {
-        const float sum = Acc<NT>::kSumX ? fmaf(nz, a.sx[c & 1], a.grp[p][n][c]) : a.grp[p][n][c];
-        a.out[p][n][c] = fmaf(s, sum, a.out[p][n][c]);
+        a.out[p][n][c] = fmaf(s, a.grp[p][n][c], a.out[p][n][c]);
         a.grp[p][n][c] = 0.0f;
       }
   }
-#pragma unroll
-  for (int c = 0; c < 4; ++c) a.sx[c] = 0.0f;
 }
 
 // Words and token fragments of two 16-row steps: the one at work and the next.
@@ -429,20 +416,13 @@ __device__ __forceinline__ void box(Acc<NT> &a, Frags<NT> &f, const uint8_t *w0,
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[i] >>= 8;
       }
-      uint32_t a0 = v[0] & m, a1 = v[1] & m, a2 = v[2] & m, a3 = v[3] & m;
-      if (!Acc<NT>::kSumX) {
-        a0 = sub2(a0, a.zp[p]);
-        a1 = sub2(a1, a.zp[p + 4]);
-        a2 = sub2(a2, a.zp[p]);
-        a3 = sub2(a3, a.zp[p + 4]);
-      }
+      const uint32_t a0 = sub2(v[0] & m, a.zp[p]), a1 = sub2(v[1] & m, a.zp[p + 4]);
+      const uint32_t a2 = sub2(v[2] & m, a.zp[p]), a3 = sub2(v[3] & m, a.zp[p + 4]);
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         const uint32_t b0 = NT == 1 ? f.b[ks >> 1][0][2 * (ks & 1)] : f.b[ks & 1][n / 2][2 * (n & 1)];
         const uint32_t b1 = NT == 1 ? f.b[ks >> 1][0][2 * (ks & 1) + 1] : f.b[ks & 1][n / 2][2 * (n & 1) + 1];
         mma16816(a.grp[p][n], a0, a1, a2, a3, b0, b1);
-        if (Acc<NT>::kSumX && p == 3)
-          mma16816(a.sx, 0x00010001u, 0x00010001u, 0x00010001u, 0x00010001u, b0, b1);
       }
     }
     if (ks == 1 && SHIFT == 5) {

@@ -105,3 +105,19 @@ def test_lora_scaled_products_past_fp16(T, rank, c2, b2):
     Yo, mags = lora(X, packed, 128, A, B, c, ids)
     got = _run(X, packed, 128, A, B, c, ids)
     _same_or_close(got, Yo, lora_tolerance(Yo, mags, 512, rank, rounded=T > 64))
+
+
+@pytest.mark.parametrize("T", [1, 2, 5, 8, 9, 16, 30, 64, 65, 130])
+@pytest.mark.parametrize("group", [32, 64, 128])
+def test_lora_infinite_inputs(T, group):
+    """An infinite input gives an infinity of its weight's sign in every output (NaN
+    where the code is the zero point), its row alone."""
+    X, packed, A, B, c, ids = _case(T, 512, 288, 16, 3, group, T + group)
+    ids[::2] = -1
+    X[0, 300], X[T // 2, 5], X[T - 1, 511] = np.inf, -np.inf, np.inf
+    with np.errstate(invalid="ignore"):
+        Yo, _ = lora(X, packed, group, A, B, c, ids)
+    _, mags = lora(np.where(np.isfinite(X), X, 0), packed, group, A, B, c, ids)
+    tol = lora_tolerance(np.where(np.isfinite(Yo), Yo, 0), mags, 512, 16, rounded=T > 64)
+    got = _run(X, packed, group, A, B, c, ids)
+    _same_or_close(got, Yo, tol)
