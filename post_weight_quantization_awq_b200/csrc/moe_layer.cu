@@ -628,7 +628,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<V>::kBlocks)
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           hi[k] = __float2half_rn(h[k]);
-          rest[k] = __float2half_rn(isfinite(h[k]) ? h[k] - __half2float(hi[k]) : 0.0f);
+          const float v = __half2float(hi[k]);
+          rest[k] = __float2half_rn(isfinite(v) ? h[k] - v : 0.0f);
         }
         __half *d = a.H + row * inter + c;
         *reinterpret_cast<uint2 *>(d) = *reinterpret_cast<const uint2 *>(hi);
