@@ -7,7 +7,7 @@
 //
 // The layer is bound by reading the met experts' words once.  Phases, between
 // grid barriers:
-//   router   a warp per (token, expert): fp32 products summed in fp64, so that
+//   router   a warp per (token, expert): exact products summed in fp64, so that
 //            a choice next to a border is the definition's; the warp that
 //            writes a token's last logit picks its experts;
 //   lists    every block makes the experts' token lists in shared memory;
@@ -111,17 +111,17 @@ __device__ __forceinline__ bool grid_barrier(uint32_t *counter, int *flag, DevSt
   return *flag != 0;
 }
 
+// Products of fp16 values are exact in fp32; their sum is fp64.
 __device__ __forceinline__ double dot8d(uint4 a, uint4 b) {
   const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
-  float s = 0.0f;
+  double s[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const float2 p = __half22float2(*reinterpret_cast<const __half2 *>(&x[i]));
     const float2 q = __half22float2(*reinterpret_cast<const __half2 *>(&y[i]));
-    s = fmaf(p.x, q.x, s);
-    s = fmaf(p.y, q.y, s);
+    s[i] = (double)__fmul_rn(p.x, q.x) + (double)__fmul_rn(p.y, q.y);
   }
-  return (double)s;
+  return (s[0] + s[1]) + (s[2] + s[3]);
 }
 
 // The logit of one (token, expert) pair by a warp.
