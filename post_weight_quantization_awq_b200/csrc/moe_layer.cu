@@ -58,11 +58,18 @@ struct Cfg {
   static constexpr uint32_t kRing = kStages * kStage;
 };
 
-// Where every block computes all logits itself: one to a warp, from so many router
-// values (64 KB from L2 in about the time of a barrier).  1 token, eight experts, hidden
-// 4096: 27.4 us a layer alone, 28.7 together; 32 logits: 26.7 and 24.6.
-constexpr int kAloneLogits = kThreads / 32, kAloneRouter = 32768;
-constexpr int64_t kOwnH = 1 << 19;
+// Where every block computes all logits itself: one to a warp.  Up to 8 logits of hidden
+// 1024 to 16384 a layer takes 1.7 us less to 0.3 more than with logits made together (1
+// token on eight experts of hidden 1024: 21.2 us, 22.2 together; on two of 16384: 45.8 and
+// 47.5); with 32 logits 2.1 more.
+constexpr int kAloneLogits = kThreads / 32;
+// Where every block makes the values of H that its down units read: this many values in
+// all, each counted once for every tile of down.  Up to 45 000 a layer takes 0.3 to 0.8 us
+// less than with H made once between two barriers (1 token, 2048 -> 1408: 23.4 us, 24.2
+// between barriers), from 65 000 0.4 to 8 more (1 token, 4096 -> 11008: 58.8 and 56.9; 32
+// tokens, 2048 -> 2048, all of eight: 88.8 and 80.7), but for 64 tokens on one or two
+// tiles of hidden (0.5 to 2.6 less).
+constexpr int64_t kOwnH = 3 << 14;
 constexpr int kPieceH = 128;  // channels of H made at a time; divides a tile
 
 template <int V>
@@ -466,7 +473,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<V>::kBlocks)
     // compute together, or each on its own where that is cheaper than meeting
     // (a barrier is 1.8 us)
     const int warp = tid >> 5, lane = tid & 31;
-    const bool alone = a.T * a.experts <= kAloneLogits && a.experts * hidden <= kAloneRouter;
+    const bool alone = a.T * a.experts <= kAloneLogits;
     const int first = alone ? warp : (int)blockIdx.x + (int)gridDim.x * warp;
     const int step = (alone ? 1 : (int)gridDim.x) * (kThreads / 32);
     for (int i = first; i < a.T * a.experts; i += step) {
@@ -512,8 +519,6 @@ __global__ void __launch_bounds__(kThreads, Cfg<V>::kBlocks)
     const int64_t groups = (int64_t)e * (inter / a.group);
     return Weights{&dn_map, e * inter, a.dn_z + groups * wh, a.dn_s + groups * hidden, wh, SHIFT, c0, wh, c0 + 32, wh};
   };
-  // values of H, each made once for every tile of down, up to which that costs less
-  // than another barrier (0.83M values: 62.3 us made by each block, 60.9 made by all)
   const bool own_h = (int64_t)a.T * a.top_k * inter * htiles <= kOwnH;
   bool ok = true;
 
