@@ -388,10 +388,10 @@ def awq_w4a16_lora_gemm(X, qweight, qzeros, scales, cfg: AwqConfig, A, B, c, ada
             and i32 is qweight.dtype is qzeros.dtype is adapter.dtype and c.dtype is f32
             and xs[1] == 1 and ys[1] == 1 and qweight.is_contiguous() and qzeros.is_contiguous()
             and scales.is_contiguous() and A.is_contiguous() and B.is_contiguous() and c.is_contiguous()
-            and adapter.is_contiguous() and A.numel() == n * rank * inn and B.numel() == n * out * rank
-            and c.numel() == n and adapter.numel() == T and Y.numel() == T * out
-            and qweight.numel() * 8 == inn * out and scales.numel() == inn // g * out
-            and qzeros.numel() == inn // g * (out // 8)):
+            and adapter.is_contiguous() and ws.is_contiguous() and A.shape[2] == inn and B.shape == (n, out, rank)
+            and c.numel() == n and adapter.numel() == T and Y.shape == (T, out)
+            and qweight.shape == (inn, out // 8) and scales.shape == (inn // g, out)
+            and qzeros.shape == (inn // g, out // 8)):
         _refuse("awq_w4a16_lora_gemm", dev, (("X", X, f16, (T, inn)), ("Y", Y, f16, (T, out))), (
             ("qweight", qweight, i32, (inn, out // 8)), ("qzeros", qzeros, i32, (inn // g, out // 8)),
             ("scales", scales, f16, (inn // g, out)), ("A", A, f16, (n, rank, inn)), ("B", B, f16, (n, out, rank)),
@@ -429,12 +429,12 @@ def awq_w4a16_moe(X, router, gate_up, down, cfg: AwqConfig, renormalize: bool, m
             and i32 is gq.dtype is gz.dtype is dq.dtype is dz.dtype is ids.dtype and weights.dtype is f32
             and xs[1] == 1 and ys[1] == 1 and router.is_contiguous() and gq.is_contiguous() and gz.is_contiguous()
             and gs.is_contiguous() and dq.is_contiguous() and dz.is_contiguous() and ds.is_contiguous()
-            and ids.is_contiguous() and weights.is_contiguous()
-            and router.numel() == E * hidden and gq.numel() * 4 == E * hidden * inter
-            and dq.numel() * 8 == E * hidden * inter and gs.numel() == E * (hidden // g) * 2 * inter
-            and gz.numel() * 4 == E * (hidden // g) * inter and ds.numel() == E * (inter // g) * hidden
-            and dz.numel() * 8 == E * (inter // g) * hidden and Y.numel() == T * hidden
-            and ids.numel() == T * top_k and weights.numel() == T * top_k
+            and ids.is_contiguous() and weights.is_contiguous() and ws.is_contiguous()
+            and router.shape == (E, hidden) and gq.shape == (E, hidden, inter // 4)
+            and dq.shape == (E, inter, hidden // 8) and gs.shape == (E, hidden // g, 2 * inter)
+            and gz.shape == (E, hidden // g, inter // 4) and ds.shape == (E, inter // g, hidden)
+            and dz.shape == (E, inter // g, hidden // 8) and Y.shape == (T, hidden)
+            and ids.shape == (T, top_k) and weights.shape == (T, top_k)
             and (mask is None or (mask.get_device() == dev and mask.dtype is u8 and mask.is_contiguous()
                                   and mask.numel() == T))):
         _refuse("awq_w4a16_moe", dev, (("X", X, f16, (T, hidden)), ("Y", Y, f16, (T, hidden))), (
