@@ -152,9 +152,11 @@ __global__ void __launch_bounds__(kThreads, MINB)
   } else {
     RingPos pos;
     Acc<NT> acc;
-    // the tokens' order, while the first words travel
+    // The tokens' order, while the first words travel.  What is read before pdl_wait() (ids,
+    // token rows, words) comes from L2: it is where the work before the shrink kernel has
+    // left its results when that kernel lets this one start, and an L1 need not know of them
     if (tid < a.T) {
-      const int id = __ldg(a.ids + tid);
+      const int id = __ldcg(a.ids + tid);
       all_ids[tid] = id >= 0 && id < a.adapters ? id : -1;
     }
     if (tid < MAXTOK) ids[tid] = -1;

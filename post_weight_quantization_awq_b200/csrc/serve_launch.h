@@ -31,7 +31,9 @@ inline cudaError_t allow_smem(K kernel, size_t bytes, std::atomic<bool> (&done)[
 // A kernel launched by launch_after is set up while the kernel before it on the
 // stream ends; pdl_wait() returns when that one has ended with all its results
 // visible, and comes before the first access to memory.  pdl_launch() lets the next
-// such kernel start.
+// such kernel start: called behind the block's own pdl_wait(), so that all work before
+// this kernel has ended by then, and the next one may read that work's results (not this
+// kernel's) before its own pdl_wait(), from L2 (ld.cg, cp.async.cg, TMA).
 __device__ __forceinline__ void pdl_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 template <class... P, class... A>

@@ -105,7 +105,8 @@ __device__ __forceinline__ void dequant_tile(__half *tile, const int32_t *__rest
 // row of weights at a time, which HBM reads and writes faster than 32 bytes.  The
 // 16-byte chunks of an output's 64 weights are XOR-swizzled by its word column, and
 // the 4-byte pairs inside a chunk by the column's upper bits, so that a warp's
-// writes (32 word columns, one input pair) fall in different banks.
+// writes (32 word columns, one input pair) fall in different banks.  Loads pass by L1: the
+// kernel may start before the one that precedes it has ended (serve_launch.h).
 constexpr int kWideIn = 64, kWideOut = 256;
 
 __device__ __forceinline__ void dequant_wide(__half *tile, const int32_t *__restrict__ qweight,
@@ -121,9 +122,9 @@ __device__ __forceinline__ void dequant_wide(__half *tile, const int32_t *__rest
   if (ok) {
     const int64_t gi = j / group;
 #pragma unroll
-    for (int r = 0; r < 8; ++r) wv[r] = (uint32_t)__ldg(qweight + (j + r) * words + wc);
-    nib_pairs((uint32_t)__ldg(qzeros + gi * words + wc), zp);
-    scale_pairs(__ldg(reinterpret_cast<const uint4 *>(scales + gi * out + 8 * wc)), sp);
+    for (int r = 0; r < 8; ++r) wv[r] = (uint32_t)__ldcg(qweight + (j + r) * words + wc);
+    nib_pairs((uint32_t)__ldcg(qzeros + gi * words + wc), zp);
+    scale_pairs(__ldcg(reinterpret_cast<const uint4 *>(scales + gi * out + 8 * wc)), sp);
     uint32_t *t = reinterpret_cast<uint32_t *>(tile) + 8 * ow * (kWideIn / 2) + ((jw ^ (ow & 7)) << 2);
 #pragma unroll
     for (int r = 0; r < 8; r += 2) {
