@@ -57,9 +57,10 @@ size_t awq_w4a16_lora_workspace_size(int64_t T, int64_t in, int64_t out, int32_t
  *   lowest expert;  p = softmax of l_t over all experts, divided by the chosen
  *   ones' sum when renormalize = 1;
  *   H = RN16( silu(x gate_e) (x up_e) );  Y[t] = RN16( sum_k p_k down_e(H) )
- * with every packed weight (q - z) scale unrounded.  Up to four tokens of an expert
- * keep what H's rounding leaves too (22 bits); H past 65504 is infinite, as its
- * rounding says, and so are its token's outputs.
+ * with every packed weight (q - z) scale unrounded.  An expert's tokens are taken 24
+ * at a time (8 at a time up to 8 tokens in all); where that leaves up to four, what
+ * H's rounding loses is kept too (22 bits).  H past 65504 is infinite, as its rounding
+ * says, and so are its token's outputs.
  *   X       device fp16 [T, hidden], row stride ldx
  *   mask    device uint8 [T] or NULL: rows with 0 (the padding of a captured
  *           step) meet no expert and get ids -1, weights 0 and Y = 0; their X
