@@ -1111,7 +1111,9 @@ awq_status awq_bounds_status(void) {
   };
   const Unit units[] = {{"quant_kernels", bounds_status_quant}, {"search_gemm", bounds_status_gemm},
                         {"clip_kernels", bounds_status_clip}, {"gram_search", bounds_status_gram},
-                        {"w4a16_gemm", bounds_status_w4a16}, {"fused_search", bounds_status_fused}};
+                        {"w4a16_gemm", bounds_status_w4a16}, {"fused_search", bounds_status_fused},
+                        {"block_norm", bounds_status_norm}, {"lora_gemm", bounds_status_lora},
+                        {"lora_prefill", bounds_status_prefill}, {"moe_layer", bounds_status_moe}};
   const char *bad = nullptr;
   uint32_t site = 0;
   for (const Unit &u : units) {

@@ -193,6 +193,10 @@ cudaError_t bounds_status_clip(DevStatus *h);
 cudaError_t bounds_status_gram(DevStatus *h);
 cudaError_t bounds_status_w4a16(DevStatus *h);
 cudaError_t bounds_status_fused(DevStatus *h);
+cudaError_t bounds_status_norm(DevStatus *h);
+cudaError_t bounds_status_lora(DevStatus *h);
+cudaError_t bounds_status_prefill(DevStatus *h);
+cudaError_t bounds_status_moe(DevStatus *h);
 #endif
 
 }  // namespace awq

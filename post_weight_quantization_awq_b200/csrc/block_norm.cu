@@ -79,7 +79,7 @@ __global__ void __launch_bounds__(TEAM *ROWS) block_norm_kernel(const NormArgs a
   for (int i = 0; i < VPT; ++i) {
     const int c = lane + i * TEAM;
     rv[i] = vv[i] = make_uint4(0u, 0u, 0u, 0u);
-    if (c < nvec) {
+    if (c < nvec && AWQ_IN_BOUNDS(row < a.T && 8 * (c + 1) <= a.d, 0xB080u)) {
       rv[i] = R[c];
       if (V) vv[i] = V[c];
     }
@@ -125,7 +125,8 @@ __global__ void __launch_bounds__(TEAM *ROWS) block_norm_kernel(const NormArgs a
     }
 #pragma unroll
     for (int k = 0; k < 8; ++k) s = fmaf(r[i][k], r[i][k], s);
-    if (a.R_out && c < nvec) reinterpret_cast<uint4 *>(a.R_out + row * a.ldro)[c] = pack8(r[i]);
+    if (a.R_out && c < nvec && AWQ_IN_BOUNDS(row < a.T && 8 * (c + 1) <= a.d, 0xB081u))
+      reinterpret_cast<uint4 *>(a.R_out + row * a.ldro)[c] = pack8(r[i]);
   }
   if (!a.N_out) return;
   s = team_sum<TEAM>(s, red[1]);
@@ -133,7 +134,7 @@ __global__ void __launch_bounds__(TEAM *ROWS) block_norm_kernel(const NormArgs a
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
     const int c = lane + i * TEAM;
-    if (c < nvec) {
+    if (c < nvec && AWQ_IN_BOUNDS(row < a.T && 8 * (c + 1) <= a.d, 0xB082u)) {
       float w[8];
       if (a.pre)
         unpack8(__ldg(reinterpret_cast<const uint4 *>(a.pre) + c), w);
@@ -166,5 +167,7 @@ cudaError_t launch_block_norm(const NormArgs &a, cudaStream_t stream) {
   if (nvec <= 4096) return go<1024, 1, 4>(a, stream);
   return cudaErrorInvalidValue;
 }
+
+AWQ_BOUNDS_READER(bounds_status_norm)
 
 }  // namespace awq

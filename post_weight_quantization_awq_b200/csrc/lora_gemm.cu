@@ -72,7 +72,7 @@ __global__ void __launch_bounds__(256) lora_shrink_kernel(const LoraArgs a) {
     if (lane == 0) part[warp][r] = s[r];
   }
   __syncthreads();
-  if (threadIdx.x < kShrinkR) {
+  if (threadIdx.x < kShrinkR && AWQ_IN_BOUNDS(t < a.T && r0 + kShrinkR <= a.rank, 0xB0A0u)) {
     float u = 0.0f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) u += part[i][threadIdx.x];
@@ -138,7 +138,7 @@ __global__ void __launch_bounds__(kThreads, MINB)
   const int k0 = (int)(units * rank / splits * unit);
   const int k1 = (int)i64min(units * (rank + 1) / splits * unit, a.in);
   if (tid >= kConsumers) {
-    Producer<M, MAXTOK> p(Weights{&map, 0, a.qzeros, a.scales, a.out / 8, SHIFT,
+    Producer<M, MAXTOK> p(Weights{&map, 0, a.qzeros, a.scales, a.out / 8, (int)a.in, SHIFT,
                   (int)(tile * 32), (int)(a.out / 8), (int)(tile * 32), (int)(a.out / 8)});
     RingPos pos;
     // the first words do not wait for the tokens' order
@@ -146,7 +146,7 @@ __global__ void __launch_bounds__(kThreads, MINB)
     for (int s = 0; s < ahead; ++s)
       p.issue_words(smem_u32(ring) + s * stage_bytes<M, MAXTOK>(), &bars->full[s], k0, k1, s);
     asm volatile("bar.sync 2, 288;" ::: "memory");
-    p.rows(a.X, a.ldx, n, [&](int t) { return perm[t]; });
+    p.rows(a.X, a.ldx, a.T, n, [&](int t) { return perm[t]; });
     p.run(pos, smem_u32(ring), bars, k0, k1, a.max_polls, nullptr, ahead);
     if (*reinterpret_cast<volatile int *>(&bars->abort)) ring_drain(bars, pos);
   } else {
@@ -193,7 +193,7 @@ __global__ void __launch_bounds__(kThreads, MINB)
     {  // a team of threads to a token, all tokens at once
       constexpr int kTeam = MAXTOK <= 8 ? 32 : MAXTOK <= 16 ? 16 : MAXTOK <= 32 ? 8 : 4;
       const int t = tid / kTeam, part = tid % kTeam;
-      const bool on = t < n && ids[t] >= 0;
+      const bool on = t < n && ids[t] >= 0 && AWQ_IN_BOUNDS(perm[t] >= 0 && perm[t] < a.T, 0xB0A2u);
       const float4 *u = reinterpret_cast<const float4 *>(a.U + (on ? perm[t] : 0) * a.rank);
       float m = 0.0f;
 #pragma unroll 4
@@ -241,7 +241,8 @@ __global__ void __launch_bounds__(kThreads, MINB)
 #pragma unroll
           for (int c = 0; c < 4; ++c) acc.grp[p][x][c] = 0.0f;
       const __half *bp = a.B + ((int64_t)id * a.out + o0) * a.rank + 8 * q;
-      const bool o_ok = o0 < a.out;  // out % 32 == 0: the 8 outputs are all in or all out
+      // out % 32 == 0: the 8 outputs are all in or all out
+      const bool o_ok = o0 < a.out && AWQ_IN_BOUNDS(id >= 0 && id < a.adapters && o0 + 8 <= a.out, 0xB0A1u);
 #pragma unroll 1
       for (int k = 0; k < r32; k += 32) {
         uint4 af[8];
@@ -303,7 +304,7 @@ __global__ void __launch_bounds__(kThreads, MINB)
   for (int i = rank * kConsumers + tid; tid < kConsumers && i < n * (kBoxN / 2); i += splits * kConsumers) {
     const int t = i / (kBoxN / 2), oo = 2 * (i % (kBoxN / 2));
     const int64_t o = tile * kBoxN + oo;
-    if (o >= a.out) continue;
+    if (o >= a.out || !AWQ_IN_BOUNDS(o + 2 <= a.out && perm[t] >= 0 && perm[t] < a.T, 0xB0A3u)) continue;
     float s0 = 0.0f, s1 = 0.0f;
 #pragma unroll 8
     for (int s = 0; s < splits; ++s) {
@@ -431,5 +432,7 @@ cudaError_t launch_lora(const LoraArgs &a, int num_sms, cudaStream_t stream) {
          : a.group == 64 ? launch_group<6>(a, num_sms, stream)
                          : launch_group<5>(a, num_sms, stream);
 }
+
+AWQ_BOUNDS_READER(bounds_status_lora)
 
 }  // namespace awq

@@ -131,7 +131,7 @@ __device__ void shrink_block(const LoraArgs &a, int64_t t0, int share, int share
   // rows g and g + 8 (the last one again past the end)
   const __half *x0 = a.X + (t0 + min(g, n - 1)) * a.ldx + 8 * q, *x1 = a.X + (t0 + min(g + 8, n - 1)) * a.ldx + 8 * q;
   for (int i0 = share * teams; i0 < items; i0 += shares * teams) {
-    if (i0 + team < items) {
+    if (i0 + team < items && AWQ_IN_BOUNDS(list[(i0 + team) / passes] >= 0 && list[(i0 + team) / passes] < a.adapters, 0xB0B1u)) {
       const int j = (i0 + team) / passes;
       const int2 rows = shrink_rows(a.rank, i0 + team - j * passes);
       float acc[4][4];
@@ -157,6 +157,7 @@ __device__ void shrink_block(const LoraArgs &a, int64_t t0, int share, int share
       const int m = i / (kShT * kShR), t = i / kShR % kShT, r = i % kShR, j = (i0 + m) / passes, id = list[j];
       const int2 rows = shrink_rows(a.rank, i0 + m - j * passes);
       if (r >= rows.y || t >= n || ids[t] != id) continue;
+      if (!AWQ_IN_BOUNDS(t0 + t < a.T && rows.x + r < a.rank, 0xB0B0u)) continue;
       float v = 0.0f;
       for (int w = 0; w < split; ++w) v += red[((m * split + w) * kShT + t) * (kShR + 1) + r];
       const int64_t at = (t0 + t) * a.rank + rows.x + r;
@@ -191,6 +192,7 @@ __global__ void __launch_bounds__(kShThreads)
   if (tid < 256) ids[tid] = id >= 0 && id < a.adapters ? id : -1;
   __syncthreads();
   const int count = adapter_list(ids, n, list, scratch);
+  if (!AWQ_IN_BOUNDS(t0 < a.T && count <= n, 0xB0B2u)) return;
   int *dst = lists + b * (bm + 1);
   if (tid == 0) dst[0] = count;
   if (tid < count) dst[1 + tid] = list[tid];
@@ -473,7 +475,8 @@ __global__ void __launch_bounds__(320, 1)
       step += a.num_kb;
       if (count) {
         const int64_t row = (int64_t)m * BM + tid;  // tid >= BM: no row
-        const int id = tid < BM && row < a.T ? a.ids[row] : -1;
+        int id = tid < BM && row < a.T ? a.ids[row] : -1;
+        if (!AWQ_IN_BOUNDS(count <= BM, 0xB0B5u)) id = -1;
         const uint4 *u = reinterpret_cast<const uint4 *>(a.U16 + row * a.rank);
         const auto chunk = [&](int i) {  // 8 values of this row's U
           return id >= 0 && 8 * i < a.rank ? __ldg(u + i) : make_uint4(0u, 0u, 0u, 0u);
@@ -548,7 +551,7 @@ __global__ void __launch_bounds__(320, 1)
         for (int c = c0; c < c1; ++c) {
           float v = tmem_column(d + c);
           const int64_t o = (int64_t)n * BN + c;
-          if (t + lane < a.T && o < a.out) {
+          if (t + lane < a.T && o < a.out && AWQ_IN_BOUNDS(!on || (int64_t)id * a.out + o < (int64_t)a.adapters * a.out, 0xB0B4u)) {
             if (on) v += left_out(u, a.B + (id * a.out + o) * a.rank, a.rank, past);
             a.Y[(t + lane) * a.ldy + o] = __float2half_rn(v);
           }
@@ -576,7 +579,7 @@ __global__ void __launch_bounds__(320, 1)
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const int row = 4 * i + (lane >> 3);
-          if (t + row < a.T && o < a.out)
+          if (t + row < a.T && o < a.out && AWQ_IN_BOUNDS(o + 8 <= a.out, 0xB0B3u))
             *reinterpret_cast<uint4 *>(a.Y + (t + row) * a.ldy + o) =
                 *reinterpret_cast<const uint4 *>(stage + row * 128 + (((lane & 7) ^ (row & 7)) * 16));
         }
@@ -651,5 +654,7 @@ cudaError_t launch_lora_prefill(const LoraArgs &a, int num_sms, cudaStream_t str
   return bm == 256 ? launch_product<256, 256>(a, lists, Wd, num_sms, stream)
                    : launch_product<128, 128>(a, lists, Wd, num_sms, stream);
 }
+
+AWQ_BOUNDS_READER(bounds_status_prefill)
 
 }  // namespace awq

@@ -231,14 +231,14 @@ __device__ void router(const MoeArgs &a) {
     int last = masked && e == 0;
     if (!masked) {
       const double s = warp_logit(a, t, e);
-      if (lane == 0) {
+      if (lane == 0 && AWQ_IN_BOUNDS(t < a.T && e < a.experts, 0xB0D0u)) {
         a.logits[i] = s;
         __threadfence();
         last = atomicAdd(a.tok_count + t, 1) == a.experts - 1;
       }
       last = __shfl_sync(0xffffffffu, last, 0);
     }
-    if (last) {
+    if (last && AWQ_IN_BOUNDS(t < a.T, 0xB0D1u)) {
       __threadfence();
       choose(a, a.logits + (int64_t)t * a.experts, masked, [&](int slot, int id, float w) {
         a.ids[t * a.top_k + slot] = id;
@@ -508,16 +508,20 @@ __global__ void __launch_bounds__(kThreads, Cfg<V>::kBlocks)
   const int64_t pitch_gu = 2 * a.inter;  // a row of the gate|up sums
   // the words of a stretch
   const auto up_weights = [&](const Stretch &s) {
-    const int e = sh->seg_expert[s.seg], tile = s.tile;
+    const int e = AWQ_IN_BOUNDS(s.seg < sh->n_seg && sh->seg_expert[s.seg] >= 0 && sh->seg_expert[s.seg] < a.experts, 0xB0D2u)
+                      ? sh->seg_expert[s.seg] : 0;
+    const int tile = AWQ_IN_BOUNDS(s.tile < 2 * itiles, 0xB0D3u) ? s.tile : 0;
     const int64_t groups = (int64_t)e * (hidden / a.group);
     const int c0 = (tile & 1) * wi + (tile >> 1) * 64, end = (tile & 1) ? 2 * wi : wi;
-    return Weights{&gu_map, e * hidden, a.gu_z + groups * 2 * wi, a.gu_s + groups * 2 * inter, 2 * wi, SHIFT,
+    return Weights{&gu_map, e * hidden, a.gu_z + groups * 2 * wi, a.gu_s + groups * 2 * inter, 2 * wi, hidden, SHIFT,
                    c0, end, c0 + 32, end};
   };
   const auto down_weights = [&](const Stretch &s) {
-    const int e = sh->seg_expert[s.seg], c0 = s.tile * 64;
+    const int e = AWQ_IN_BOUNDS(s.seg < sh->n_seg && sh->seg_expert[s.seg] >= 0 && sh->seg_expert[s.seg] < a.experts, 0xB0D4u)
+                      ? sh->seg_expert[s.seg] : 0;
+    const int c0 = AWQ_IN_BOUNDS(s.tile < htiles, 0xB0D5u) ? s.tile * 64 : 0;
     const int64_t groups = (int64_t)e * (inter / a.group);
-    return Weights{&dn_map, e * inter, a.dn_z + groups * wh, a.dn_s + groups * hidden, wh, SHIFT, c0, wh, c0 + 32, wh};
+    return Weights{&dn_map, e * inter, a.dn_z + groups * wh, a.dn_s + groups * hidden, wh, inter, SHIFT, c0, wh, c0 + 32, wh};
   };
   const bool own_h = (int64_t)a.T * a.top_k * inter * htiles <= kOwnH;
   bool ok = true;
@@ -528,7 +532,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<V>::kBlocks)
     each_stretch(up, (int)blockIdx.x, [&](const Stretch &s, int u0, int u1) {
       Producer<Mode::kN, C::kTok> p(up_weights(s));
       const int seg = s.seg, p0 = sh->seg_first[seg];
-      p.rows(a.X, a.ldx, sh->seg_n[seg], [&](int t) { return sh->pair[p0 + t] / a.top_k; });
+      p.rows(a.X, a.ldx, a.T, sh->seg_n[seg], [&](int t) { return sh->pair[p0 + t] / a.top_k; });
       p.template run<C::kStages>(pos, ring_u, bars, u0 * 128, min(u1 * 128, hidden), a.max_polls, st);
     });
     // the first words of the down product do not wait for H
@@ -556,7 +560,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<V>::kBlocks)
       }
       if (!ok) return;
       const int seg = s.seg, p0 = sh->seg_first[seg], n = sh->seg_n[seg], pairs = a.T * a.top_k;
-      p.rows(a.H, inter, h_rows(n),
+      p.rows(a.H, inter, 2 * pairs, h_rows(n),
              [&](int t) { return t < n ? sh->pair[p0 + t] : pairs + sh->pair[p0 + t - n]; });
       p.template run<C::kStages>(pos, ring_u, bars, k0, k1, a.max_polls, st, ahead);
       ahead = 0;
@@ -583,7 +587,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<V>::kBlocks)
             const int t = n * 8 + 2 * q + e;
             float v[8];
             outputs8<NT>(acc, n, e, v);
-            if (t < rows) {
+            if (t < rows && AWQ_IN_BOUNDS(rows <= C::kTok && lane_col + 8 <= cols, 0xB0D6u)) {
               float4 *d = reinterpret_cast<float4 *>(dst(t) + lane_col);
               __stcg(d, make_float4(v[0], v[1], v[2], v[3]));
               __stcg(d + 1, make_float4(v[4], v[5], v[6], v[7]));
@@ -619,7 +623,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<V>::kBlocks)
       for (int i = tid; i < n * quads; i += kConsumers) {
         const int t = i / quads, c = c0 + 4 * (i - t * quads), ch = c / kTile * kTile;
         const int64_t row = sh->pair[p0 + t];
+        if (!AWQ_IN_BOUNDS(row >= 0 && row < a.T * a.top_k && c + 4 <= inter, 0xB0D7u)) continue;
         const int2 gb = up.blocks(up.at(seg, 2 * (c / kTile))), ub = up.blocks(up.at(seg, 2 * (c / kTile) + 1));
+        if (!AWQ_IN_BOUNDS(gb.x >= 0 && ub.x >= 0 && gb.y < (int)gridDim.x && ub.y < (int)gridDim.x && t < C::kTok, 0xB0D8u)) continue;
         // part j: a whole tile's sums, or those of the j-th of its blocks, which but for the first enter inside it
         const auto part = [&](int2 b, int64_t off) {
           return [=](int j) {
@@ -694,12 +700,13 @@ __global__ void __launch_bounds__(kThreads, Cfg<V>::kBlocks)
       const int n = sh->seg_n[seg], row = at - sh->seg_first[seg];
       const int2 db = down.blocks(down.at(seg, o / kTile));
       const int parts = db.y - db.x + 1, w = o % kTile;
+      const bool in = AWQ_IN_BOUNDS(db.x >= 0 && db.y < (int)gridDim.x && row < n && h_rows(n) <= C::kTok && p < a.T * a.top_k, 0xB0D9u);
       const auto part = [&](int j, int rest) -> const float * {
         return parts == 1 ? a.dn_sums + (int64_t)(rest * a.T * a.top_k + p) * hidden + o
                           : a.dn_partial + (((int64_t)db.x + j) * 2 + (j == 0)) * C::kTok * kTile + (rest * n + row) * kTile + w;
       };
       float4 v, r;
-      sum_parts(parts, [&](int j) { return part(j, 0); }, h_rows(n) > n ? parts : 0, [&](int j) { return part(j, 1); }, v, r);
+      sum_parts(in ? parts : 0, [&](int j) { return part(j, 0); }, in && h_rows(n) > n ? parts : 0, [&](int j) { return part(j, 1); }, v, r);
       const float pw = sh->wt[p];
       y = make_float4(pw * (v.x + r.x), pw * (v.y + r.y), pw * (v.z + r.z), pw * (v.w + r.w));
     }
@@ -709,7 +716,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<V>::kBlocks)
       y.z += __shfl_xor_sync(0xffffffffu, y.z, d);
       y.w += __shfl_xor_sync(0xffffffffu, y.w, d);
     }
-    if (k == 0 && quad < quads) {
+    if (k == 0 && quad < quads && AWQ_IN_BOUNDS(t < a.T && o + 4 <= hidden, 0xB0DAu)) {
       const __half2 h0 = __floats2half2_rn(y.x, y.y), h1 = __floats2half2_rn(y.z, y.w);
       *reinterpret_cast<uint2 *>(a.Y + t * a.ldy + o) =
           make_uint2(*reinterpret_cast<const uint32_t *>(&h0), *reinterpret_cast<const uint32_t *>(&h1));
@@ -758,6 +765,8 @@ cudaError_t launch_moe(const MoeArgs &a, int num_sms, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   return a.T <= 8 ? go_group<1>(a, num_sms, stream) : go_group<2>(a, num_sms, stream);
 }
+
+AWQ_BOUNDS_READER(bounds_status_moe)
 
 MoeLayout moe_layout(int64_t T, int64_t hidden, int64_t inter, int64_t experts, int64_t top_k, int num_sms) {
   MoeLayout l;

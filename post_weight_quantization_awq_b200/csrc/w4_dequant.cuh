@@ -6,6 +6,8 @@
 #include <cuda_fp16.h>
 #include <stdint.h>
 
+#include "awq_device.cuh"
+
 namespace awq {
 namespace {
 
@@ -118,7 +120,7 @@ __device__ __forceinline__ void dequant_wide(__half *tile, const int32_t *__rest
   const int64_t wc = o0 / 8 + ow, j = j0 + 8 * jw;
   uint32_t wv[8];
   __half2 zp[4], sp[4];
-  const bool ok = wc < words && j < in;  // in % 64 == 0
+  const bool ok = wc < words && j < in && AWQ_IN_BOUNDS(j + 8 <= in, 0xB0C1u);  // in % 64 == 0
   if (ok) {
     const int64_t gi = j / group;
 #pragma unroll
@@ -143,7 +145,7 @@ __device__ __forceinline__ void dequant_wide(__half *tile, const int32_t *__rest
   for (int i = 0; i < kWideOut * (kWideIn / 8) / 256; ++i) {
     const int c = threadIdx.x + 256 * i, oo = c >> 3, jc = c & 7;  // output, 8-input chunk
     const int64_t o = o0 + oo, jj = j0 + 8 * jc;
-    if (o >= out || jj >= in) continue;
+    if (o >= out || jj >= in || !AWQ_IN_BOUNDS(jj + 8 <= in, 0xB0C0u)) continue;
     const uint4 v = *reinterpret_cast<const uint4 *>(tile + oo * kWideIn + 8 * (jc ^ ((oo >> 3) & 7)));
     const int x = oo >> 6;  // undo the pairs' swizzle: pair i lies at i ^ x
     const uint32_t a = (x & 1) ? v.y : v.x, b = (x & 1) ? v.x : v.y, e = (x & 1) ? v.w : v.z, f = (x & 1) ? v.z : v.w;

@@ -181,6 +181,7 @@ struct Weights {
   const int32_t *qzeros;
   const __half *scales;
   int64_t words;  // out / 8
+  int in;         // input rows
   int shift;      // log2 of the group size
   int col0, end0, col1, end1;
 };
@@ -210,6 +211,9 @@ template <Mode M, int MAXTOK>
 struct Producer {
   static constexpr int kX = (MAXTOK + 3) / 4;  // token rows of a lane
   int n, shift, row0, x0, x1;                   // x0, x1: the boxes' columns in the words' tensor map
+#ifdef AWQ_DEBUG_BOUNDS
+  int in;
+#endif
   const CUtensorMap *map;
   // this lane's chunk of either box's steps, and (lanes 0..7, 8..15) of their zero
   // words, in group 0; bytes between groups
@@ -223,6 +227,9 @@ struct Producer {
     map = w.map;
     row0 = w.row0;
     shift = w.shift;
+#ifdef AWQ_DEBUG_BOUNDS
+    in = w.in;
+#endif
     x0 = w.col0 * 2;
     x1 = w.col1 * 2;
     box1 = w.col1 < w.end1;
@@ -239,13 +246,14 @@ struct Producer {
   }
 
   template <class RowOf>
-  __device__ __forceinline__ void rows(const __half *base, int64_t ld, int count, RowOf row) {
+  __device__ __forceinline__ void rows(const __half *base, int64_t ld, int64_t rows, int count, RowOf row) {
     const int lane = threadIdx.x & 31;
     n = count;
 #pragma unroll
     for (int j = 0; j < kX; ++j) {
       const int t = (lane >> 3) + 4 * j;
-      x[j] = reinterpret_cast<const char *>(base + (t < n ? (int64_t)row(t) * ld : 0) + (lane & 7) * 8);
+      const int64_t r = t < n ? row(t) : 0;
+      x[j] = reinterpret_cast<const char *>(base + (AWQ_IN_BOUNDS(r >= 0 && r < rows, 0xB090u) ? r * ld : 0) + (lane & 7) * 8);
     }
   }
 
@@ -264,6 +272,7 @@ struct Producer {
     const bool first0 = shift != 7 || !(kb0 & 64), first1 = ok1 && (shift != 7 || !(kb1 & 64));
     // a group of 128 comes with its first box
     const uint32_t g0 = (uint32_t)kb0 >> shift, g1 = (uint32_t)kb1 >> shift;
+    if (!AWQ_IN_BOUNDS(kb0 + kBoxK <= in && (!ok1 || kb1 + kBoxK <= in), 0xB091u)) return;
     if (first0) cp16(d, sc[0] + (uint64_t)g0 * sc_row, sc_ok[0]);
     if (first1) cp16(d + 2 * kSz, sc[1] + (uint64_t)g1 * sc_row, sc_ok[1]);
     if (lane < 16 && (lane < 8 ? first0 : first1)) cp16(st + zp_at, zp + (uint64_t)(lane < 8 ? g0 : g1) * zp_row, zp_ok);
