@@ -262,18 +262,21 @@ __device__ __noinline__ void make_finite(uint8_t *row, int swizzle, int i, int s
   }
 }
 
-// One column of tensor memory, a value to a lane, waited for.
-__device__ __forceinline__ float tmem_column(uint32_t taddr) {
-  uint32_t r;
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];\n\ttcgen05.wait::ld.sync.aligned;"
-               : "=r"(r)
-               : "r"(taddr)
-               : "memory");
-  return __uint_as_float(r);
+// 8 columns of tensor memory, waited for.
+__device__ __forceinline__ void tmem_columns8(uint32_t taddr, float (&v)[8]) {
+  uint32_t r[8];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n\ttcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+      : "r"(taddr)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
 }
 
-// Whether a row of U is no operand of fp16: its largest value past the type's range (or no
-// number), or so small that the type's smallest step, 2^-24, is no longer small beside it.
+// Whether a row of U is no operand of fp16: its largest value past the type's range, or so
+// small that the type's smallest step, 2^-24, is no longer small beside it.  A row with a
+// NaN is one: all its outputs are NaN.
 __device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
 __device__ __forceinline__ uint32_t abs_bits(float4 v) {
   return max(max(abs_bits(v.x), abs_bits(v.y)), max(abs_bits(v.z), abs_bits(v.w)));
@@ -281,18 +284,29 @@ __device__ __forceinline__ uint32_t abs_bits(float4 v) {
 __device__ __forceinline__ bool past_fp16(const float *u, int rank) {
   uint32_t m = 0;
   for (int r = 0; r < rank; r += 4) m = max(m, abs_bits(__ldg(reinterpret_cast<const float4 *>(u + r))));
-  return m > 0x477FE000u || (m != 0 && m < 0x39800000u);  // 65504; 2^-12
+  return (m > 0x477FE000u && m <= 0x7F800000u) || (m != 0 && m < 0x39800000u);  // 65504, infinity; 2^-12
 }
 
-// The terms U[t][r] B_a[o][r] of one output that are not in the product: those that
-// make_finite took out, or all of a row of U past fp16.
-__device__ __noinline__ float left_out(const float *u, const __half *b, int rank, bool all) {
-  float s = 0.0f;
-  for (int r = 0; r < rank; ++r) {
-    const float v = __half2float(b[r]);
-    if (all || !isfinite(v)) s = fmaf(u[r], v, s);
+// Adds to v the terms U[t][r] B_a[o][r] of 8 outputs (b: the first one's row) that are not
+// in the product: those that make_finite took out, or all of a row of U past fp16.
+__device__ __noinline__ void left_out(float (&v)[8], const float *u, const __half *b, int rank, bool all) {
+  for (int r = 0; r < rank; r += 8) {
+    uint4 w[8];
+    const float4 x0 = __ldg(reinterpret_cast<const float4 *>(u + r)), x1 = __ldg(reinterpret_cast<const float4 *>(u + r) + 1);
+    const float x[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = __ldg(reinterpret_cast<const uint4 *>(b + (int64_t)i * rank + r));
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t h[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+      if (!all && !(non_finite(h[0]) | non_finite(h[1]) | non_finite(h[2]) | non_finite(h[3]))) continue;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float y = __half2float(__ushort_as_half((unsigned short)(h[k / 2] >> (16 * (k & 1)))));
+        if (all || !isfinite(y)) v[i] = fmaf(x[k], y, v[i]);
+      }
+    }
   }
-  return s;
 }
 
 template <int STAGES>
@@ -543,17 +557,25 @@ __global__ void __launch_bounds__(320, 1)
       const uint32_t d = tmem + ((uint32_t)(q * 32) << 16) + acc * (C::kMT * BN) + (C::kMT == 2 ? part * BN : 0);
       uint8_t *stage = sOut + (warp - 2) * 4096;
       const bool odd = count && tail->odd[it & 3] == it + 1;
-      if (odd) {  // a column at a time, with what is not in the product
+      if (odd) {  // a lane its row, 8 columns at a time, with what is not in the product
         const int id = t + lane < a.T ? a.ids[t + lane] : -1;
         const bool on = id >= 0 && id < a.adapters;
         const float *u = a.U + (t + lane) * a.rank;
         const bool past = on && past_fp16(u, a.rank);
-        for (int c = c0; c < c1; ++c) {
-          float v = tmem_column(d + c);
+#pragma unroll 1
+        for (int c = c0; c < c1; c += 8) {
+          float v[8];
+          tmem_columns8(d + c, v);
           const int64_t o = (int64_t)n * BN + c;
-          if (t + lane < a.T && o < a.out && AWQ_IN_BOUNDS(!on || (int64_t)id * a.out + o < (int64_t)a.adapters * a.out, 0xB0B4u)) {
-            if (on) v += left_out(u, a.B + (id * a.out + o) * a.rank, a.rank, past);
-            a.Y[(t + lane) * a.ldy + o] = __float2half_rn(v);
+          if (t + lane < a.T && o < a.out && AWQ_IN_BOUNDS(o + 8 <= a.out, 0xB0B4u)) {
+            if (on) left_out(v, u, a.B + (id * a.out + o) * a.rank, a.rank, past);
+            uint32_t w[4];
+#pragma unroll
+            for (int h = 0; h < 4; ++h) {
+              const __half2 p = __floats2half2_rn(v[2 * h], v[2 * h + 1]);
+              w[h] = *reinterpret_cast<const uint32_t *>(&p);
+            }
+            *reinterpret_cast<uint4 *>(a.Y + (t + lane) * a.ldy + o) = make_uint4(w[0], w[1], w[2], w[3]);
           }
           __syncwarp();
         }
