@@ -195,16 +195,21 @@ __global__ void __launch_bounds__(kThreads, MINB)
       const int t = tid / kTeam, part = tid % kTeam;
       const bool on = t < n && ids[t] >= 0 && AWQ_IN_BOUNDS(perm[t] >= 0 && perm[t] < a.T, 0xB0A2u);
       const float4 *u = reinterpret_cast<const float4 *>(a.U + (on ? perm[t] : 0) * a.rank);
-      float m = 0.0f;
+      uint32_t m = 0;  // the largest magnitude's bits; a NaN's are larger than all
 #pragma unroll 4
       for (int k = part; k < a.rank / 4; k += kTeam)
-        if (on) m = fmaxf(m, fmaxf(fmaxf(fabsf(u[k].x), fabsf(u[k].y)), fmaxf(fabsf(u[k].z), fabsf(u[k].w))));
+        if (on) {
+          const float4 v = u[k];
+          m = max(max(m, max(__float_as_uint(v.x) & 0x7fffffffu, __float_as_uint(v.y) & 0x7fffffffu)),
+                  max(__float_as_uint(v.z) & 0x7fffffffu, __float_as_uint(v.w) & 0x7fffffffu));
+        }
 #pragma unroll
-      for (int d = kTeam / 2; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-      // 2^e with |u| / 2^e in [1, 2) at most; not for 0, infinities and the ends of the range
-      const int e = (int)(__float_as_uint(m) >> 23) - 127;
+      for (int d = kTeam / 2; d; d >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
+      // 2^e with |u| / 2^e in [1, 2) at most; not for 0, infinities and the ends of the range;
+      // NaN where U has one
+      const int e = (int)(m >> 23) - 127;
       const bool scaled = e > -120 && e < 120;
-      const float up = scaled ? __uint_as_float((uint32_t)(127 + e) << 23) : 1.0f;
+      const float up = scaled ? __uint_as_float((uint32_t)(127 + e) << 23) : m > 0x7f800000u ? __uint_as_float(m) : 1.0f;
       const float down = scaled ? __uint_as_float((uint32_t)(127 - e) << 23) : 1.0f;
       if (t < MAXTOK) {
         if (part == 0) uscale[t] = up;
@@ -281,8 +286,8 @@ __global__ void __launch_bounds__(kThreads, MINB)
       float odd = 0.0f;
       each_sum([&](int, float, int, float v, float &) { odd = fmaf(0.0f, v, odd); });
       if (odd != 0.0f && o_ok)  // NaN: a sum is not finite
-        each_sum([&](int t, float, int o, float &v, float &out) {
-          if (isfinite(v)) return;
+        each_sum([&](int t, float sc, int o, float &v, float &out) {
+          if (isfinite(v) || isnan(sc)) return;  // NaN in U: all its outputs are
           out += low_rank_dot(a.U + perm[t] * a.rank, a.B + ((int64_t)id * a.out + o0 + o) * a.rank, a.rank);
           v = 0.0f;
         });
