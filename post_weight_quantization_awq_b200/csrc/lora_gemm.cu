@@ -291,6 +291,7 @@ __global__ void __launch_bounds__(kThreads, MINB)
           out += low_rank_dot(a.U + perm[t] * a.rank, a.B + ((int64_t)id * a.out + o0 + o) * a.rank, a.rank);
           v = 0.0f;
         });
+      __syncwarp();  // the next adapter's MMAs take all lanes
       each_sum([&](int, float sc, int, float v, float &out) { out = fmaf(sc, v, out); });
     }
     store_sums<M, NT>(acc, red);
