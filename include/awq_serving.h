@@ -51,7 +51,7 @@ size_t awq_w4a16_lora_workspace_size(int64_t T, int64_t in, int64_t out, int32_t
                                      const awq_config *cfg);
 
 /* A whole mixture-of-experts layer on packed experts, for a few tokens (a
- * decode step or a small batch), in one kernel: router, choice, gate|up,
+ * decode step or a small batch), in one call: router, choice, gate|up,
  * SwiGLU, down and the weighted sum,
  *   l_te = sum_j X[t][j] router[e][j];  the top_k largest of a row, ties to the
  *   lowest expert;  p = softmax of l_t over all experts, divided by the chosen

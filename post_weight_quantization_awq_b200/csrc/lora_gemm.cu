@@ -10,9 +10,10 @@
 // 12.3 us for 1 token at rank 16, 18.5 against 14.2 at rank 64, since every output
 // tile's cluster reads all of A.)
 //
-// Measured at 4096 x 4096, rank 16: 12.3 us for 1 token, 13.8 for 16, where the words
-// are 1.4 us: bound by the latency of the launches, the loads and the sums that meet.
-// 45 tokens on 4096 x 12288, rank 64: 37 us, bound by the core's instructions.
+// Measured at 4096 x 4096, rank 16: 11.0 us for 1 token (9.8 without an adapter), 13.7
+// for 16, where the words are 1.4 us: bound by the latency of the launches, the loads and
+// the sums that meet.  45 tokens on 4096 x 12288, rank 64: 39.6 us, bound by the core's
+// instructions.
 #include <cooperative_groups.h>
 
 #include "awq_launch.h"

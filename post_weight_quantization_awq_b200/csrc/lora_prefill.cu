@@ -17,10 +17,13 @@
 // rounded once, and the part costs rank / in of the product for rows that stand
 // together by adapter.
 //
-// Measured, replayed: 138 us for 1531 tokens on 4096 x 11008 at rank 32 (the product
-// 109, two rounds of 256 x 256 tiles on 148 SMs, 735 ns a step of 64 columns = 1.69
-// PFLOP/s while a tile is at work), 245 us for 8192 on 4096 x 4096 at rank 16 (product
-// 211); bound by the tensor cores at the clock they hold.
+// Measured, replayed: 140 us for 1531 tokens on 4096 x 11008 at rank 32 (the product
+// 111, two rounds of 256 x 256 tiles on 148 SMs, 735 ns a step of 64 columns = 1.69
+// PFLOP/s while a tile is at work), 245-251 us for 8192 on 4096 x 4096 at rank 16 (product
+// 213); bound by the tensor cores at the clock they hold.  Tiles with values that leave the
+// product (non-finite B, rows of U past fp16) are stored 8 columns at a time with those
+// terms added in fp32: 253 us for the 1531 tokens with one infinity in one adapter's B, 1.2
+// ms with every row of U past fp16.
 #include <cuda.h>
 
 #include "awq_launch.h"

@@ -1,5 +1,5 @@
 // A whole mixture-of-experts layer on packed 4-bit experts for a few tokens,
-// one cooperative kernel:
+// one cooperative kernel (and one that clears its status word and counters):
 //
 //   l = x Wr^T;  the k largest logits (ties to the lowest expert), p = softmax
 //   over all experts (divided by the chosen ones' sum when renormalize);
@@ -25,9 +25,9 @@
 //   combine  a token's experts' sums, weighted with p in fp32, one rounding.
 // Sums are added in an order fixed by the sizes and the routing alone.
 //
-// Measured, 4096 -> 11008 and two of eight experts: 56 us for 1 token (139 MB of
+// Measured, 4096 -> 11008 and two of eight experts: 58 us for 1 token (139 MB of
 // words and steps; 5.3 TB/s while gate|up streams, the rest are phases that wait
-// for each other), 244 us for 64 (557 MB; 252-314 cycles for 16 rows x 512 outputs
+// for each other), 241 us for 64 (557 MB; 252-313 cycles for 16 rows x 512 outputs
 // by 8 warps, bound by their instructions and the latency of mma.sync).
 #include <climits>
 #include <cuda_runtime.h>

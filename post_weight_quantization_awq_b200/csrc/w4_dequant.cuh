@@ -103,7 +103,8 @@ __device__ __forceinline__ void dequant_tile(__half *tile, const int32_t *__rest
   }
 }
 
-// The same with 256-output tiles of 64 inputs: 128 bytes of a row of words and of a
+// The same weights with 256-output tiles of 64 inputs (the adapter product's; w4a16_gemm.cu's
+// dequantise-once form has the tiles above): 128 bytes of a row of words and of a
 // row of weights at a time, which HBM reads and writes faster than 32 bytes.  The
 // 16-byte chunks of an output's 64 weights are XOR-swizzled by its word column, and
 // the 4-byte pairs inside a chunk by the column's upper bits, so that a warp's
