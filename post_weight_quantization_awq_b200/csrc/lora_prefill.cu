@@ -17,8 +17,8 @@
 // rounded once, and the part costs rank / in of the product for rows that stand
 // together by adapter.
 //
-// Measured, replayed: 140 us for 1531 tokens on 4096 x 11008 at rank 32 (the product
-// 111, two rounds of 256 x 256 tiles on 148 SMs, 735 ns a step of 64 columns = 1.69
+// Measured, replayed: 138 us for 1531 tokens on 4096 x 11008 at rank 32 (the product
+// 110, two rounds of 256 x 256 tiles on 148 SMs, 735 ns a step of 64 columns = 1.69
 // PFLOP/s while a tile is at work), 245-251 us for 8192 on 4096 x 4096 at rank 16 (product
 // 213); bound by the tensor cores at the clock they hold.  Tiles with values that leave the
 // product (non-finite B, rows of U past fp16) are stored 8 columns at a time with those
@@ -166,7 +166,9 @@ __device__ void shrink_block(const LoraArgs &a, int64_t t0, int share, int share
       const int64_t at = (t0 + t) * a.rank + rows.x + r;
       const float u = a.c[id] * v;
       a.U[at] = u;
-      reinterpret_cast<__half *>(a.U + a.T * a.rank)[at] = __float2half_rn(u);
+      __half h = __float2half_rn(u);
+      if (u != 0.0f && __heq(h, __float2half_rn(0.0f))) h = __float2half_rn(copysignf(0x1p-24f, u));  // past_fp16
+      reinterpret_cast<__half *>(a.U + a.T * a.rank)[at] = h;
     }
     __syncthreads();
   }
@@ -278,16 +280,18 @@ __device__ __forceinline__ void tmem_columns8(uint32_t taddr, float (&v)[8]) {
 }
 
 // Whether a row of U is no operand of fp16: its largest value past the type's range, or so
-// small that the type's smallest step, 2^-24, is no longer small beside it.  A row with a
-// NaN is one: all its outputs are NaN.
-__device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
-__device__ __forceinline__ uint32_t abs_bits(float4 v) {
-  return max(max(abs_bits(v.x), abs_bits(v.y)), max(abs_bits(v.z), abs_bits(v.w)));
-}
-__device__ __forceinline__ bool past_fp16(const float *u, int rank) {
+// small that the type's smallest step, 2^-24, is no longer small beside it (a value that
+// rounds to 0 is stored as that step, so that the row's fp16 form tells).  A row with a NaN
+// is one: all its outputs are NaN.
+__device__ __forceinline__ bool past_fp16(const __half *u, int rank) {
   uint32_t m = 0;
-  for (int r = 0; r < rank; r += 4) m = max(m, abs_bits(__ldg(reinterpret_cast<const float4 *>(u + r))));
-  return (m > 0x477FE000u && m <= 0x7F800000u) || (m != 0 && m < 0x39800000u);  // 65504, infinity; 2^-12
+#pragma unroll 4
+  for (int r = 0; r < rank; r += 8) {
+    const uint4 v = __ldg(reinterpret_cast<const uint4 *>(u + r));
+    m = __vmaxu2(__vmaxu2(m, v.x & 0x7FFF7FFFu), __vmaxu2(__vmaxu2(v.y & 0x7FFF7FFFu, v.z & 0x7FFF7FFFu), v.w & 0x7FFF7FFFu));
+  }
+  m = max(m & 0xFFFFu, m >> 16);
+  return m == 0x7C00u || (m != 0 && m < 0x0C00u);  // infinity; 2^-12
 }
 
 // Adds to v the terms U[t][r] B_a[o][r] of 8 outputs (b: the first one's row) that are not
@@ -498,17 +502,17 @@ __global__ void __launch_bounds__(320, 1)
         const auto chunk = [&](int i) {  // 8 values of this row's U
           return id >= 0 && 8 * i < a.rank ? __ldg(u + i) : make_uint4(0u, 0u, 0u, 0u);
         };
-        const bool past = id >= 0 && past_fp16(a.U + row * a.rank, a.rank);
-        uint4 first[PK / 8];  // loaded once for all adapters of the tile
+        const bool past = id >= 0 && past_fp16(a.U16 + row * a.rank, a.rank);
         int next = list[1];
-#pragma unroll
-        for (int i = 0; i < PK / 8; ++i) first[i] = chunk(i);
         for (int e = 0; e < count && ok; ++e) {
           const bool mine = id == next && !past;
           if (id == next && past) tail->odd[it & 3] = it + 1;
           if (e + 1 < count) next = list[2 + e];
           for (int r = 0; r < rsteps; ++r, ++step) {
-            const int s = step % STAGES;
+            const int s = step % STAGES, left = min(PK, a.rank - r * PK);
+            uint4 v[PK / 8];  // on its way while B_a is
+#pragma unroll
+            for (int i = 0; i < PK / 8; ++i) v[i] = mine ? chunk(PK / 8 * r + i) : make_uint4(0u, 0u, 0u, 0u);
             int got = 1;
             if (lane == 0) got = mbar_wait_long(&tail->ufull[s], (uphase >> s) & 1u, a.max_polls, abort_flag);
             uphase ^= 1u << s;
@@ -522,15 +526,14 @@ __global__ void __launch_bounds__(320, 1)
             // The other rows' zeros meet B_a too, and 0 x infinity is NaN: what is not finite
             // leaves the box, and is added to the adapter's own rows at the end (0.13 us a step of
             // 128 rows; looking the adapters over beforehand would read B_a once more)
-            const int left = min(PK, a.rank - r * PK), chunks = n * BN + tid % BN < a.out ? left / 8 : 0;
+            const int chunks = n * BN + tid % BN < a.out ? left / 8 : 0;
             uint8_t *brow = sB + s * C::kB + tid % BN * (PK * 2);
             const uint32_t bad = row_non_finite<256 / BN>(brow, tid & 7, tid / BN, chunks);
             if (tid < BM) {
               uint4 *d = reinterpret_cast<uint4 *>(sA + s * C::kA + tid * (PK * 2));
 #pragma unroll
               for (int i = 0; i < PK / 8; ++i)  // 128-byte swizzle; the MMAs of 16 columns that are issued
-                if (8 * (i & ~1) < left)
-                  d[i ^ (tid & 7)] = !mine ? make_uint4(0u, 0u, 0u, 0u) : r == 0 ? first[i] : chunk(PK / 8 * r + i);
+                if (8 * (i & ~1) < left) d[i ^ (tid & 7)] = v[i];
             }
             if (__any_sync(0xffffffffu, bad != 0)) {
               make_finite(brow, tid & 7, tid / BN, 256 / BN, chunks);
@@ -564,7 +567,7 @@ __global__ void __launch_bounds__(320, 1)
         const int id = t + lane < a.T ? a.ids[t + lane] : -1;
         const bool on = id >= 0 && id < a.adapters;
         const float *u = a.U + (t + lane) * a.rank;
-        const bool past = on && past_fp16(u, a.rank);
+        const bool past = on && past_fp16(a.U16 + (t + lane) * a.rank, a.rank);
 #pragma unroll 1
         for (int c = c0; c < c1; c += 8) {
           float v[8];
