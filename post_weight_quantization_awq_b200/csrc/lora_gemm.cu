@@ -10,9 +10,9 @@
 // 12.3 us for 1 token at rank 16, 18.5 against 14.2 at rank 64, since every output
 // tile's cluster reads all of A.)
 //
-// Measured at 4096 x 4096, rank 16: 11.0 us for 1 token (9.8 without an adapter), 13.7
+// Measured at 4096 x 4096, rank 16: 10.7 us for 1 token (9.6 without an adapter), 13.7
 // for 16, where the words are 1.4 us: bound by the latency of the launches, the loads and
-// the sums that meet.  45 tokens on 4096 x 12288, rank 64: 39.6 us, bound by the core's
+// the sums that meet.  45 tokens on 4096 x 12288, rank 64: 39.5 us, bound by the core's
 // instructions.
 #include <cooperative_groups.h>
 
@@ -81,11 +81,17 @@ __global__ void __launch_bounds__(256) lora_shrink_kernel(const LoraArgs a) {
   }
 }
 
-// One output's part of a token's adapter in fp32, term by term.
-__device__ __noinline__ float low_rank_dot(const float *u, const __half *b, int rank) {
+// One output's part of a token's adapter in fp32, term by term; 0 where U and B_a are
+// finite throughout.
+__device__ __noinline__ float non_finite_dot(const float *u, const __half *b, int rank) {
   float s = 0.0f;
-  for (int r = 0; r < rank; ++r) s = fmaf(u[r], __half2float(b[r]), s);
-  return s;
+  bool any = false;
+  for (int r = 0; r < rank; ++r) {
+    const float x = u[r], y = __half2float(b[r]);
+    any |= !isfinite(x) || !isfinite(y);
+    s = fmaf(x, y, s);
+  }
+  return any ? s : 0.0f;
 }
 
 // A cluster of `splits` blocks covers 256 outputs x MAXTOK tokens, each block
@@ -97,7 +103,7 @@ __device__ __noinline__ float low_rank_dot(const float *u, const __half *b, int 
 // hi + lo of 22 bits under a power of two of its token, so nothing is rounded
 // away and no U overflows.  An adapter's sums are added for its own tokens only.  With an
 // infinity or a NaN in U or B_a a pair's product is not the value's (0 x infinity is NaN):
-// a sum that is not finite is made again in fp32.
+// a sum that is not finite is left out and made in fp32 afterwards.
 template <Mode M, int NT, int MAXTOK, int STAGES>
 struct LoraShared {
   static constexpr uint32_t kRing = STAGES * stage_bytes<M, MAXTOK>();
@@ -206,12 +212,10 @@ __global__ void __launch_bounds__(kThreads, MINB)
         }
 #pragma unroll
       for (int d = kTeam / 2; d; d >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
-      // 2^e with |u| / 2^e in [1, 2) at most; not for 0, infinities and the ends of the range;
-      // NaN where U has one
-      const int e = (int)(m >> 23) - 127;
-      const bool scaled = e > -120 && e < 120;
-      const float up = scaled ? __uint_as_float((uint32_t)(127 + e) << 23) : m > 0x7f800000u ? __uint_as_float(m) : 1.0f;
-      const float down = scaled ? __uint_as_float((uint32_t)(127 - e) << 23) : 1.0f;
+      // 2^e with |u| / 2^e below 4, NaN where U has one
+      const int e = min(max((int)(m >> 23) - 127, -126), 126);
+      const float up = m > 0x7f800000u ? __uint_as_float(m) : __uint_as_float((uint32_t)(127 + e) << 23);
+      const float down = __uint_as_float((uint32_t)(127 - e) << 23);
       if (t < MAXTOK) {
         if (part == 0) uscale[t] = up;
         __half2 *d = reinterpret_cast<__half2 *>(uhl + t * L::kUPitch);
@@ -237,6 +241,7 @@ __global__ void __launch_bounds__(kThreads, MINB)
     // 32 rank rows a step, a lane's 16 bytes at 8q of a row of B_a (or of U) being
     // its fragments of two MMAs
     const uint8_t *ul = uhl + (tt + g) * L::kUPitch + q * 16;
+    bool left_out = false;
     for (int j = first; j < *n_list; j += step) {
       const int lo = list[j] & 0xffff, hi = list[j] >> 16, id = ids[lo];
       if (hi <= tt || lo >= tt + 8 * NT) continue;  // none of this warp's tokens
@@ -281,19 +286,46 @@ __global__ void __launch_bounds__(kThreads, MINB)
 #pragma unroll
             for (int p = 0; p < 4; ++p)
 #pragma unroll
-              for (int h = 0; h < 2; ++h) f(t, sc, p + 4 * h, acc.grp[p][x][e + 2 * h], acc.out[p][x][e + 2 * h]);
+              for (int h = 0; h < 2; ++h) f(sc, acc.grp[p][x][e + 2 * h], acc.out[p][x][e + 2 * h]);
           }
       };
-      float odd = 0.0f;
-      each_sum([&](int, float, int, float v, float &) { odd = fmaf(0.0f, v, odd); });
-      if (odd != 0.0f && o_ok)  // NaN: a sum is not finite
-        each_sum([&](int t, float sc, int o, float &v, float &out) {
-          if (isfinite(v) || isnan(sc)) return;  // NaN in U: all its outputs are
-          out += low_rank_dot(a.U + perm[t] * a.rank, a.B + ((int64_t)id * a.out + o0 + o) * a.rank, a.rank);
+      float bad[8] = {};  // NaN where a sum is not finite (of whichever token: fewer tests)
+#pragma unroll
+      for (int x = 0; x < NT; ++x)
+#pragma unroll
+        for (int p = 0; p < 4; ++p)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) bad[2 * p + (c & 1)] = fmaf(0.0f, acc.grp[p][x][c], bad[2 * p + (c & 1)]);
+      const float odd = ((bad[0] + bad[1]) + (bad[2] + bad[3])) + ((bad[4] + bad[5]) + (bad[6] + bad[7]));
+      if (__any_sync(0xffffffffu, odd != 0.0f))
+        each_sum([&](float sc, float &v, float &) {
+          if (isfinite(v)) return;
           v = 0.0f;
+          left_out |= !isnan(sc);  // NaN in U: all its outputs are
         });
-      __syncwarp();  // the next adapter's MMAs take all lanes
-      each_sum([&](int, float sc, int, float v, float &out) { out = fmaf(sc, v, out); });
+      each_sum([&](float sc, float v, float &out) { out = fmaf(sc, v, out); });
+    }
+    // The sums left out, in a loop of their own: beside the MMAs they cost 20 % (36 tokens
+    // with 31 adapters of rank 64)
+    if (__any_sync(0xffffffffu, left_out)) {
+      for (int j = first; j < *n_list; j += step) {
+        const int lo = list[j] & 0xffff, hi = list[j] >> 16;
+        if (o0 >= a.out) break;
+        const __half *b = a.B + ((int64_t)ids[lo] * a.out + o0) * a.rank;
+#pragma unroll
+        for (int x = 0; x < NT; ++x)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int t = tt + x * 8 + 2 * q + e;
+            if (t < lo || t >= hi || isnan(uscale[t])) continue;
+            const float *u = a.U + perm[t] * a.rank;
+#pragma unroll
+            for (int p = 0; p < 4; ++p)
+#pragma unroll
+              for (int h = 0; h < 2; ++h) acc.out[p][x][e + 2 * h] += non_finite_dot(u, b + (p + 4 * h) * a.rank, a.rank);
+          }
+      }
+      __syncwarp();
     }
     store_sums<M, NT>(acc, red);
   }
